@@ -461,6 +461,147 @@ int pkv_decode_attention_noalloc(const pkv_pool *pool, const uint16_t *q, const 
                                  const int32_t *seq_lens_dev, int B, float scale, int pages_per_chunk,
                                  uint16_t *out, int32_t *dev_err_flag, void *cuda_stream);
 
+/* --------------------------------------------------- a window and the first tokens */
+
+/* Paged decode attention over a sliding window and the first tokens, for one layer.
+ * The pages have no counterpart; the definition is pkv_decode_attention's with fewer
+ * tokens (KV-cache tutorial section 3.2), for contexts whose cache is not kept whole:
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . K_t) V_t   over t < L, L = seq_lens[b],
+ *               with t < sinks or t >= L - window.
+ * window >= 1 counts the newest token; sinks >= 0.  window >= L attends to everything.
+ * Only the pages that hold such a token are read and looked up: the entries of the
+ * others may be anything, e.g. pages given back to the pool.
+ *   pages_per_chunk 1..128 pages per work unit, counted along the visited pages, or 0:
+ *              the library chooses by B and the most pages a sequence can visit.  With a
+ *              fixed value a sequence's result is bit-identical alone or in any batch.
+ *   workspace  >= pkv_decode_window_workspace_bytes(...) bytes for the same arguments,
+ *              16-byte aligned (may be NULL when every sequence's visited pages fit one
+ *              chunk); zeroing, sharing and the launch contract (programmatic dependent
+ *              launch) as for pkv_decode_attention.
+ *   options    PKV_DECODE_DEFAULT / _MMA, optionally | PKV_STEP_NO_PDL, PKV_STEP_RING(n),
+ *              PKV_STEP_SORTED, PKV_STEP_TEST_EXPIRE_WAIT; none changes a result bit.
+ *              PKV_DECODE_SIMT is PKV_ERR_UNSUPPORTED.
+ * Device checks as pkv_decode_attention (lengths up to 16*max_blocks; the ids of
+ * visited pages).  BF16 and FP8 pools. */
+int pkv_decode_window(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
+                      const int32_t *seq_lens_dev, int B, float scale, int window, int sinks, int pages_per_chunk,
+                      void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *dev_err_flag,
+                      void *cuda_stream, int options);
+
+/* pkv_decode_step with pkv_decode_window's attention: append and attention in one
+ * launch, bit-identical to pkv_append_rope followed by pkv_decode_window. */
+int pkv_decode_step_window(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, uint16_t *q,
+                           const int32_t *bt_dev, int max_blocks, const int32_t *seq_lens_dev, int B,
+                           const float *rope_table, int max_pos, float scale, int window, int sinks,
+                           int pages_per_chunk, void *workspace, size_t workspace_bytes, uint16_t *out,
+                           int32_t *dev_err_flag, void *cuda_stream, int options);
+
+/* Workspace of the two calls above; 0 for arguments they refuse. */
+size_t pkv_decode_window_workspace_bytes(int B, int max_blocks, int window, int sinks, int pages_per_chunk);
+
+/* ------------------------------------------------------------- a shared prefix */
+
+/* Paged decode attention for groups of sequences that share a prefix, for one layer:
+ * pkv_decode_attention's result, with every shared page read once for its whole group
+ * instead of once per sequence.  The pages have no counterpart.
+ *   group_starts_dev int32 [groups + 1]: group i is the sequences group_starts[i] ..
+ *              group_starts[i + 1] - 1 (group_starts[0] = 0, group_starts[groups] = B,
+ *              increasing);
+ *   prefix_pages_dev int32 [groups]: the group's shared prefix in whole pages (0: none).
+ *              The prefix is 16 * prefix_pages tokens; its pages are the first
+ *              prefix_pages entries of the table row of the group's FIRST sequence (the
+ *              other rows' first entries are not read);
+ *   max_prefix_pages  host-side bound on prefix_pages (sizes the launch and the
+ *              workspace), 0..max_blocks.
+ * A sequence's length counts its prefix: seq_lens[b] >= 16 * prefix_pages, and the
+ * tokens behind the prefix are in its own row's pages as for pkv_decode_attention.
+ *   pages_per_chunk, prefix_pages_per_chunk: pages per work unit of the sequences' own
+ *              pages (1..128) and of the prefixes (rounded up to a multiple of 8); 0: the
+ *              library chooses by the host-side arguments.  With fixed values a
+ *              sequence's result is bit-identical in any group and batch.
+ *   workspace  >= pkv_decode_shared_workspace_bytes(...) bytes, 16-byte aligned; zeroing
+ *              and sharing as for pkv_decode_attention.
+ *   options    PKV_DECODE_DEFAULT / _MMA, optionally | PKV_STEP_NO_PDL, PKV_STEP_RING(n),
+ *              PKV_STEP_TEST_EXPIRE_WAIT; PKV_STEP_SORTED and PKV_DECODE_SIMT are
+ *              PKV_ERR_UNSUPPORTED.
+ * Launch contract as for pkv_decode_attention; group_starts and prefix_pages count with
+ * seq_lens and bt_dev.
+ * Device checks: as pkv_decode_attention; a sequence in no group, or whose group's
+ * prefix is negative, above max_prefix_pages or longer than the sequence, has zeros as
+ * its outputs and sets PKV_DEVERR_LENGTH. */
+int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
+                      const int32_t *seq_lens_dev, int B, const int32_t *group_starts_dev,
+                      const int32_t *prefix_pages_dev, int groups, int max_prefix_pages, float scale,
+                      int pages_per_chunk, int prefix_pages_per_chunk, void *workspace, size_t workspace_bytes,
+                      uint16_t *out, int32_t *dev_err_flag, void *cuda_stream, int options);
+
+size_t pkv_decode_shared_workspace_bytes(int B, int max_blocks, int groups, int max_prefix_pages,
+                                         int pages_per_chunk, int prefix_pages_per_chunk);
+
+/* ------------------------------------- weights gathered by the cache, and eviction */
+
+/* pkv_decode_attention that also adds each cached token's softmax weight, summed over
+ * the 4 query heads of a KV head, to an accumulator:
+ *   acc_out[b][g][t] = acc[b][g][t] + sum_{h/4 = g} softmax_t(scale * q[b][h] . K_t),
+ *   t < seq_lens[b];
+ * entries from seq_lens[b] on are neither read nor written.  acc and acc_out are FP32
+ * [B][8][acc_stride], acc_stride >= 16 * max_blocks, and may be the same array.  The sums
+ * have one order: results do not vary from run to run.
+ *   workspace  >= pkv_decode_scored_workspace_bytes(...) bytes, 16-byte aligned: the
+ *              attention's workspace, then the scores (128 bytes per table token); zeroing
+ *              and sharing as for pkv_decode_attention.
+ *   pages_per_chunk (0: the library chooses) and options as for pkv_decode_window.
+ * Device checks as pkv_decode_attention; the tokens of a work unit with a page id
+ * outside the pool weigh nothing, and a sequence of invalid length adds nothing. */
+int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
+                      const int32_t *seq_lens_dev, int B, float scale, const float *acc, float *acc_out,
+                      int64_t acc_stride, int pages_per_chunk, void *workspace, size_t workspace_bytes, uint16_t *out,
+                      int32_t *dev_err_flag, void *cuda_stream, int options);
+
+size_t pkv_decode_scored_workspace_bytes(int B, int max_blocks, int pages_per_chunk);
+
+/* Cut caches to `keep` tokens per KV head by the weights they have gathered, for one
+ * layer (or several: tables, lengths and weights of layers * B sequences).  For a
+ * sequence of length L > keep and KV head g the first `sinks` tokens and the last
+ * `recent` stay, and of the others the keep - sinks - recent with the largest
+ * acc[b][g][t]; of equal weights the lowest t stays, and NaN counts as the least.
+ * (sinks + recent <= keep.)  A sequence with L <= keep stays whole; length 0 is allowed.
+ * Each KV head keeps tokens of its own.  Their K and V rows (and FP8 row scales) are
+ * copied bit by bit, in order, to slots 0 .. n-1, n = min(L, keep), of the pages of
+ * bt_dst_dev [B][dst_blocks]; keys keep the rotation of their position.  Slots from n on
+ * stay as they were, and so do the source pages: when the call's work is done the caller
+ * gives them back.  The destination pages must be distinct from each other and from the
+ * call's source pages (otherwise their contents are undefined).
+ *   acc        FP32 [B][8][acc_stride], acc_stride >= 16 * src_blocks
+ *   acc_out    FP32 [B][8][acc_out_stride], acc_out_stride >= 16 * dst_blocks: the kept
+ *              tokens' weights, zeros behind them; may be acc itself with the same stride
+ *   kept       int32 [B][8][keep]: the kept tokens' old indices, -1 behind them; or NULL,
+ *              then `workspace` holds them (pkv_evict_workspace_bytes, 4-byte aligned)
+ *   seq_lens_out int32 [B]: n; may be seq_lens_dev itself
+ * The next token of such a sequence is appended with pkv_append_rope_at: its position is
+ * no longer its slot.  The next pkv_decode_* launch on this pool goes without
+ * programmatic dependent launch, because it may read these pages.
+ * Device checks: L outside [0, 16*src_blocks] or n > 16*dst_blocks sets
+ * PKV_DEVERR_LENGTH, and the sequence is treated as empty; a page id outside the pool
+ * sets PKV_DEVERR_PAGE_RANGE, and the rows concerned are not copied. */
+int pkv_evict(const pkv_pool *pool, const int32_t *bt_src_dev, int src_blocks, const int32_t *seq_lens_dev, int B,
+              const int32_t *bt_dst_dev, int dst_blocks, int keep, int recent, int sinks, const float *acc,
+              int64_t acc_stride, float *acc_out, int64_t acc_out_stride, int32_t *kept, int32_t *seq_lens_out,
+              void *workspace, size_t workspace_bytes, int32_t *dev_err_flag, void *cuda_stream);
+
+size_t pkv_evict_workspace_bytes(int B, int keep);
+
+/* pkv_append_rope with the rotation's position and the token's place in the cache
+ * apart: k_new[b] and q[b] are rotated to position pos_dev[b], and the new rows go to
+ * page bt_dev[b][slots_dev[b] / 16], slot slots_dev[b] % 16.  The rotated query rows go to
+ * q_out, which may be q; both may be NULL.  Device checks: pos outside [0, max_pos), a
+ * slot outside [0, 16*max_blocks) or a page id outside the pool sets the flag and skips
+ * that sequence. */
+int pkv_append_rope_at(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, const uint16_t *q,
+                       uint16_t *q_out, const int32_t *bt_dev, int max_blocks, const int32_t *pos_dev,
+                       const int32_t *slots_dev, int B, const float *rope_table, int max_pos, int32_t *dev_err_flag,
+                       void *cuda_stream);
+
 /* ------------------------------------------------------------------ misc */
 
 /* Synchronise the stream, read the device error flag into *host_flag (may be

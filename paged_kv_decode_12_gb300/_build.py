@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libpkv.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["pkv_host.cpp", "pkv_sched.cpp", "pkv_layers.cpp", "pkv_append.cu", "pkv_decode.cu", "pkv_step.cu",
-           "pkv_fp8.cu", "pkv_probe.cu"]
+           "pkv_fp8.cu", "pkv_probe.cu", "pkv_window.cu", "pkv_shared.cu", "pkv_scored.cu", "pkv_evict.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

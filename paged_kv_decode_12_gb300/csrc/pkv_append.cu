@@ -26,27 +26,27 @@ constexpr int kAppendThreads = 256;
 
 __global__ void __launch_bounds__(kAppendThreads)
 append_rope_kernel(uint16_t *__restrict__ slab, int num_pages, const uint16_t *__restrict__ k_new,
-                   const uint16_t *__restrict__ v_new, uint16_t *__restrict__ q, const int32_t *__restrict__ bt,
-                   int max_blocks, const int32_t *__restrict__ pos, const float4 *__restrict__ rope, int max_pos,
+                   const uint16_t *__restrict__ v_new, const uint16_t *q, uint16_t *q_out,
+                   const int32_t *__restrict__ bt, int max_blocks, const int32_t *__restrict__ pos,
+                   const int32_t *__restrict__ slots, const float4 *__restrict__ rope, int max_pos,
                    int32_t *__restrict__ err)
 {
     dev::grid_dependency_wait();
     dev::allow_dependent_launch();
     const int b = blockIdx.x;
-    const int p = pos[b];
-    const int limit = min(max_pos, max_blocks * kPage);
-    if (p < 0 || p >= limit) {
+    const int p = pos[b], at = slots[b];  // the rotation's position, the token's place in the cache
+    if (p < 0 || p >= max_pos || at < 0 || at >= (int64_t)max_blocks * kPage) {
         if (threadIdx.x == 0 && err)
             atomicOr(err, PKV_DEVERR_LENGTH);
         return;
     }
-    const int page = bt[(size_t)b * max_blocks + p / kPage];
+    const int page = bt[(size_t)b * max_blocks + at / kPage];
     if (page < 0 || page >= num_pages) {
         if (threadIdx.x == 0 && err)
             atomicOr(err, PKV_DEVERR_PAGE_RANGE);
         return;
     }
-    const int slot = p % kPage;
+    const int slot = at % kPage;
     uint16_t *page_base = slab + (size_t)page * kPageElems;
 
     // values: 8 heads x 64 dims x 2 B = 64 chunks of 16 B
@@ -68,7 +68,8 @@ append_rope_kernel(uint16_t *__restrict__ slab, int num_pages, const uint16_t *_
             src = k_new + ((size_t)b * kHkv + r) * kD;
             dst = page_base + ((size_t)r * kPage + slot) * kD;
         } else {
-            src = dst = q + ((size_t)b * kHq + (r - kHkv)) * kD;
+            src = q + ((size_t)b * kHq + (r - kHkv)) * kD;
+            dst = q_out + ((size_t)b * kHq + (r - kHkv)) * kD;
         }
         const __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162 *>(src + 2 * j);
         const __nv_bfloat162 hi = *reinterpret_cast<const __nv_bfloat162 *>(src + kD / 2 + 2 * j);
@@ -85,25 +86,37 @@ append_rope_kernel(uint16_t *__restrict__ slab, int num_pages, const uint16_t *_
 }  // namespace
 }  // namespace pkv
 
-extern "C" int pkv_append_rope(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, uint16_t *q,
-                               const int32_t *bt_dev, int max_blocks, const int32_t *pos_dev, int B,
-                               const float *rope_table, int max_pos, int32_t *dev_err_flag, void *cuda_stream)
+extern "C" int pkv_append_rope_at(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new,
+                                  const uint16_t *q, uint16_t *q_out, const int32_t *bt_dev, int max_blocks,
+                                  const int32_t *pos_dev, const int32_t *slots_dev, int B, const float *rope_table,
+                                  int max_pos, int32_t *dev_err_flag, void *cuda_stream)
 {
     using namespace pkv;
-    if (!pool || !k_new || !v_new || !bt_dev || !pos_dev || !rope_table)
+    if (!pool || !k_new || !v_new || !bt_dev || !pos_dev || !slots_dev || !rope_table || (q == nullptr) != (q_out == nullptr))
         return PKV_ERR_INVALID_ARG;
     if (B < 1 || B > INT32_MAX / 2 || max_blocks < 1 || max_pos < 1)
         return PKV_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new) |
-         reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(rope_table)) & 15u)
+         reinterpret_cast<uintptr_t>(q) | reinterpret_cast<uintptr_t>(q_out) |
+         reinterpret_cast<uintptr_t>(rope_table)) & 15u)
         return PKV_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     if (pool->kv_format == PKV_KV_FP8)
-        return fp8_append_rope(pool, k_new, v_new, q, bt_dev, max_blocks, pos_dev, B, rope_table, max_pos,
-                               dev_err_flag, s);
+        return fp8_append_rope(pool, k_new, v_new, q, q_out, bt_dev, max_blocks, pos_dev, slots_dev, B, rope_table,
+                               max_pos, dev_err_flag, s);
     return launch_kernel(append_rope_kernel, dim3(B), dim3(kAppendThreads), 0, s, true,
-                         reinterpret_cast<uint16_t *>(pool->slab), pool->num_pages, k_new, v_new, q, bt_dev,
-                         max_blocks, pos_dev, reinterpret_cast<const float4 *>(rope_table), max_pos, dev_err_flag);
+                         reinterpret_cast<uint16_t *>(pool->slab), pool->num_pages, k_new, v_new, q, q_out, bt_dev,
+                         max_blocks, pos_dev, slots_dev, reinterpret_cast<const float4 *>(rope_table), max_pos,
+                         dev_err_flag);
+}
+
+// The token's place is its position, and the query rows are rotated in place.
+extern "C" int pkv_append_rope(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, uint16_t *q,
+                               const int32_t *bt_dev, int max_blocks, const int32_t *pos_dev, int B,
+                               const float *rope_table, int max_pos, int32_t *dev_err_flag, void *cuda_stream)
+{
+    return pkv_append_rope_at(pool, k_new, v_new, q, q, bt_dev, max_blocks, pos_dev, pos_dev, B, rope_table, max_pos,
+                              dev_err_flag, cuda_stream);
 }
 
 // ---------------------------------------------------------------------------

@@ -139,8 +139,8 @@ __global__ void __launch_bounds__(kThreads) decode_split_kernel(const __grid_con
 
     Warp w;
     w.init(a.q + ((size_t)b * kHq + g * kGroup) * kD, a.scale_log2, lane, sm.scratch + warp * kScratchFloats);
-    if (!consume_pages<STAGES>(&tmap, my_stages, my_bars, w, my_page, nmine, j0, warp, lane, L, g, policy,
-                               NoPatch{}) &&
+    if (!consume_list<STAGES>(&tmap, my_stages, my_bars, w, my_page, nmine, j0, warp, lane, WholeSequence{L}, g,
+                              policy, NoPatch{}, EmitNothing{}) &&
         lane == 0 && a.err)
         atomicOr(a.err, PKV_DEVERR_TIMEOUT);
 

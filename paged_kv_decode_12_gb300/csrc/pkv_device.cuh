@@ -159,6 +159,26 @@ __device__ __forceinline__ void rope_rotate_pair(float x1, float x2, float4 cs, 
     y2 = rope_comb(x2, x1, cs.x, cs.z, cs.y, cs.w);
 }
 
+// ------------------------------------------------------------------ token masks
+
+// The tokens of a page that are attended to: the first n of it, or any set.
+struct FirstTokens {
+    int n;
+    __device__ __forceinline__ bool operator()(int t) const { return t < n; }
+    __device__ __forceinline__ bool all() const { return n >= kPage; }
+};
+
+struct TokenSet {
+    uint32_t bits;
+    __device__ __forceinline__ bool operator()(int t) const { return (bits >> t) & 1u; }
+    __device__ __forceinline__ bool all() const { return bits == (1u << kPage) - 1; }
+};
+
+// What becomes of a page's scores besides the softmax: nothing.
+struct NoScores {
+    __device__ __forceinline__ void operator()(int, int, float, float) const {}
+};
+
 // ------------------------------------------------------------------ SIMT policy
 
 struct SimtWarp {
@@ -188,8 +208,9 @@ struct SimtWarp {
         l[0] = l[1] = 0.f;
     }
 
-    __device__ __forceinline__ void page(const uint8_t *st, int nvalid)
+    __device__ __forceinline__ void page(const uint8_t *st, FirstTokens keep)
     {
+        const int nvalid = keep.n;
         const int dg = lane & 7, tg = lane >> 3;
         // ---- partial dot products: tokens 4tg..4tg+3, dims 8dg..8dg+7, 4 heads
         float v[16];  // index i*4 + h
@@ -374,7 +395,10 @@ struct MmaWarp {
         l[0] = l[1] = 0.f;
     }
 
-    __device__ __forceinline__ void page(const uint8_t *st, int nvalid)
+    // The page at `st`, its tokens in `keep`; `emit(t, h, x0, x1)` gets the scores (log2
+    // domain) of token t and heads h, h + 1, from the lanes that hold real heads.
+    template <class Keep, class Emit = NoScores>
+    __device__ __forceinline__ void page(const uint8_t *st, Keep keep, const Emit &emit = Emit())
     {
         const int gid = lane >> 2, tig = lane & 3;
         const uint32_t kbase = smem_addr(st);
@@ -403,10 +427,16 @@ struct MmaWarp {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             x[i] = s[i] * c;
-        if (gid >= nvalid)
+        if (!keep(gid))
             x[0] = x[1] = -INFINITY;
-        if (gid + 8 >= nvalid)
+        if (!keep(gid + 8))
             x[2] = x[3] = -INFINITY;
+        if (tig < 2) {
+            if (keep(gid))
+                emit(gid, 2 * tig, x[0], x[1]);
+            if (keep(gid + 8))
+                emit(gid + 8, 2 * tig, x[2], x[3]);
+        }
         float pm0 = fmaxf(x[0], x[2]), pm1 = fmaxf(x[1], x[3]);
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) {
@@ -427,16 +457,15 @@ struct MmaWarp {
         // ---- O^T = alpha * O^T + V^T . P^T
         const int mi = lane >> 3, r = lane & 7;
         const int tok = r + ((mi >> 1) ? 8 : 0);
-        const bool partial = nvalid < kPage;
+        const bool partial = !keep.all();
         // token masks of this lane's A-fragment halves: a0/a1 tokens 2tig, 2tig+1; a2/a3 +8
-        const uint32_t mlo = (2 * tig < nvalid ? 0x0000ffffu : 0u) | (2 * tig + 1 < nvalid ? 0xffff0000u : 0u);
-        const uint32_t mhi =
-            (2 * tig + 8 < nvalid ? 0x0000ffffu : 0u) | (2 * tig + 9 < nvalid ? 0xffff0000u : 0u);
+        const uint32_t mlo = (keep(2 * tig) ? 0x0000ffffu : 0u) | (keep(2 * tig + 1) ? 0xffff0000u : 0u);
+        const uint32_t mhi = (keep(2 * tig + 8) ? 0x0000ffffu : 0u) | (keep(2 * tig + 9) ? 0xffff0000u : 0u);
 #pragma unroll
         for (int mt = 0; mt < 4; ++mt) {
             uint32_t a[4];
             ldsm_x4_trans(vbase + swz(tok, 2 * mt + (mi & 1)), a);
-            if (partial) {  // zero V of slots past the sequence end (their bytes are arbitrary)
+            if (partial) {  // zero V of slots not attended to (their bytes are arbitrary)
                 a[0] &= mlo;
                 a[1] &= mlo;
                 a[2] &= mhi;
@@ -479,6 +508,18 @@ struct MmaWarp {
 };
 
 
+
+// One page through a policy; the SIMT policy takes whole page beginnings and keeps no scores.
+template <class Warp, class Keep, class Emit>
+__device__ __forceinline__ void update_page(Warp &w, const uint8_t *stage, Keep keep, const Emit &emit)
+{
+    w.page(stage, keep, emit);
+}
+
+__device__ __forceinline__ void update_page(SimtWarp &w, const uint8_t *stage, FirstTokens keep, const NoScores &)
+{
+    w.page(stage, keep);
+}
 
 // ------------------------------------------------------------------ page streaming
 
@@ -542,15 +583,16 @@ __device__ __forceinline__ void issue_prologue(const CUtensorMap *tmap, uint8_t 
     issue_copies<STAGES>(tmap, my_stages, my_bars, my_page, 0, min(STAGES, nmine), g, lane, policy);
 }
 
-// How many of a warp's first min(stages, nmine) pages (pages j0 + warp + 4k of the
-// sequence) hold only positions below L - 2.  A decode launch may copy those before
+// How many of a warp's first min(stages, nmine) list entries (j0 + warp + 4k) are pages
+// that hold only positions below L - 2.  A decode launch may copy those before
 // its dependency wait: the previous decode step of the same layer wrote position
 // L - 2 and the append of this step (fused or a separate kernel just before) writes
 // L - 1, so the pages holding either are copied only after the wait.
-__device__ __forceinline__ int copies_before_wait(int L, int j0, int warp, int nmine, int stages)
+template <class List>
+__device__ __forceinline__ int copies_before_wait(const List &list, int L, int j0, int warp, int nmine, int stages)
 {
-    const int jsafe = max(L - 2, 0) / kPage;  // first page holding position L - 2 or later
-    const int n = jsafe > j0 + warp ? (jsafe - j0 - warp + kWarps - 1) / kWarps : 0;
+    const int isafe = list.before(max(L - 2, 0) / kPage);  // first entry holding position L - 2 or later
+    const int n = isafe > j0 + warp ? (isafe - j0 - warp + kWarps - 1) / kWarps : 0;
     return min(n, min(stages, nmine));
 }
 
@@ -558,26 +600,28 @@ struct NoPatch {
     __device__ __forceinline__ void operator()(uint8_t *, int) const {}
 };
 
-// Consume this warp's pages j0 + warp + k*kWarps (k < nmine): wait for the stage,
-// let `patch(stage, j)` edit it, run the policy's page update, refill the stage
+// Consume this warp's pages j0 + warp + k*kWarps (k < nmine) of a page list: wait for the
+// stage, let `patch(stage, j)` edit it, run the policy's page update on the tokens of
+// the page that the list keeps, its scores going to `emit_of(j)`, refill the stage
 // with page k + STAGES.  Returns false if a bounded wait gave up (after giving
 // the copies still in flight a bounded chance to land).  The first wait polls at
 // most `first_limit` times (a testing aid can make it give up at once); the others,
 // and the drain of copies in flight, kWaitLimit times.
-template <int STAGES, class Warp, class Patch>
-__device__ __forceinline__ bool consume_pages(const CUtensorMap *tmap, uint8_t *my_stages, uint64_t *my_bars, Warp &w,
-                                              int my_page, int nmine, int j0, int warp, int lane, int L, int g,
-                                              uint64_t policy, const Patch &patch, uint32_t first_limit = kWaitLimit)
+template <int STAGES, class Warp, class List, class Patch, class EmitOf>
+__device__ __forceinline__ bool consume_list(const CUtensorMap *tmap, uint8_t *my_stages, uint64_t *my_bars, Warp &w,
+                                             int my_page, int nmine, int j0, int warp, int lane, const List &list,
+                                             int g, uint64_t policy, const Patch &patch, const EmitOf &emit_of,
+                                             uint32_t first_limit = kWaitLimit)
 {
     int k = 0;
     for (; k < nmine; ++k) {
         const int s = k % STAGES;
         if (!mbar_wait_warp(&my_bars[s], (uint32_t)((k / STAGES) & 1), k == 0 ? first_limit : kWaitLimit))
             break;
-        const int j = j0 + warp + k * kWarps;
+        const int j = list.logical(j0 + warp + k * kWarps);
         uint8_t *stage = my_stages + s * kStageBytes;
         patch(stage, j);
-        w.page(stage, min(kPage, L - j * kPage));
+        update_page(w, stage, list.tokens(j), emit_of(j));
         __syncwarp();
         if (k + STAGES < nmine) {
             const int pk = __shfl_sync(kFull, my_page, k + STAGES);
@@ -595,6 +639,22 @@ __device__ __forceinline__ bool consume_pages(const CUtensorMap *tmap, uint8_t *
     }
     return true;
 }
+
+// The list of a sequence of length L whose every page is visited.
+struct WholeSequence {
+    int L;
+    __device__ __forceinline__ bool ok() const { return true; }
+    __device__ __forceinline__ int count() const { return (L + kPage - 1) / kPage; }
+    __device__ __forceinline__ int logical(int i) const { return i; }
+    __device__ __forceinline__ int before(int j) const { return j; }
+    __device__ __forceinline__ FirstTokens tokens(int j) const { return {min(kPage, L - j * kPage)}; }
+    __device__ __forceinline__ int row(int b, int) const { return b; }
+    __device__ __forceinline__ int first_slot() const { return 0; }
+};
+
+struct EmitNothing {
+    __device__ __forceinline__ NoScores operator()(int) const { return {}; }
+};
 
 // Combine the kWarps warps' (m, l, o) states stored at `state` (kStateFloats per
 // warp) for query head hl of the group and output dims 2dp, 2dp+1.

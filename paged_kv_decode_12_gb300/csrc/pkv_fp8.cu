@@ -86,26 +86,26 @@ constexpr int kAppendThreads = kHkv * 32;  // one warp per KV head
 // V rows; then the 32 query rows are rotated in place (BF16, as the BF16 path).
 __global__ void __launch_bounds__(kAppendThreads)
 append_rope_fp8_kernel(uint8_t *__restrict__ slab, int num_pages, const uint16_t *__restrict__ k_new,
-                       const uint16_t *__restrict__ v_new, uint16_t *__restrict__ q, const int32_t *__restrict__ bt,
-                       int max_blocks, const int32_t *__restrict__ pos,
-                       const float4 *__restrict__ rope, int max_pos, int32_t *__restrict__ err)
+                       const uint16_t *__restrict__ v_new, const uint16_t *q, uint16_t *q_out,
+                       const int32_t *__restrict__ bt, int max_blocks, const int32_t *__restrict__ pos,
+                       const int32_t *__restrict__ slots, const float4 *__restrict__ rope, int max_pos, int32_t *__restrict__ err)
 {
     grid_dependency_wait();  // launched with programmatic dependent launch: see append_rope_kernel
     allow_dependent_launch();
     const int b = blockIdx.x;
-    const int p = pos[b];
-    if (p < 0 || p >= min(max_pos, max_blocks * kPage)) {
+    const int p = pos[b], at = slots[b];  // the rotation's position, the token's place in the cache
+    if (p < 0 || p >= max_pos || at < 0 || at >= (int64_t)max_blocks * kPage) {
         if (threadIdx.x == 0 && err)
             atomicOr(err, PKV_DEVERR_LENGTH);
         return;
     }
-    const int page = bt[(size_t)b * max_blocks + p / kPage];
+    const int page = bt[(size_t)b * max_blocks + at / kPage];
     if (page < 0 || page >= num_pages) {
         if (threadIdx.x == 0 && err)
             atomicOr(err, PKV_DEVERR_PAGE_RANGE);
         return;
     }
-    const int slot = p % kPage;
+    const int slot = at % kPage;
     const int h = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *page_base = slab + (size_t)page * kFp8PageBytes;
     const float4 *rope_row = rope + (size_t)p * (kD / 2);
@@ -116,15 +116,16 @@ append_rope_fp8_kernel(uint8_t *__restrict__ slab, int num_pages, const uint16_t
     // query rows: 32 rows x 32 pairs, one pair per thread and pass
     for (int item = threadIdx.x; item < kHq * (kD / 2); item += kAppendThreads) {
         const int r = item / (kD / 2), i = item % (kD / 2);
-        uint16_t *row = q + ((size_t)b * kHq + r) * kD;
+        const uint16_t *row = q + ((size_t)b * kHq + r) * kD;
+        uint16_t *to = q_out + ((size_t)b * kHq + r) * kD;
         const float4 cs = rope_row[i];
         const float x1 = __uint_as_float((uint32_t)row[i] << 16);
         const float x2 = __uint_as_float((uint32_t)row[i + kD / 2] << 16);
         float y1, y2;
         rope_rotate_pair(x1, x2, cs, y1, y2);
         const __nv_bfloat16 b1 = __float2bfloat16_rn(y1), b2 = __float2bfloat16_rn(y2);
-        row[i] = *reinterpret_cast<const uint16_t *>(&b1);
-        row[i + kD / 2] = *reinterpret_cast<const uint16_t *>(&b2);
+        to[i] = *reinterpret_cast<const uint16_t *>(&b1);
+        to[i + kD / 2] = *reinterpret_cast<const uint16_t *>(&b2);
     }
 }
 
@@ -272,7 +273,7 @@ decode_split_fp8_kernel(const __grid_constant__ CUtensorMap tmap, Fp8SplitArgs a
             }
             const int j = j0 + warp + k * kWarps;
             uint8_t *stage = my_stages + s * kFp8Unit;
-            w.page(stage, min(kPage, L - j * kPage));
+            w.page(stage, FirstTokens{min(kPage, L - j * kPage)});
             __syncwarp();
             if (k + STAGES < nmine) {
                 const int pk = __shfl_sync(kFull, my_page, k + STAGES);
@@ -315,13 +316,13 @@ constexpr int kFp8Stages = 4;  // 35 KiB of shared memory: six CTAs per SM
 
 // ------------------------------------------------------------------ launchers
 
-int fp8_append_rope(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, uint16_t *q,
-                    const int32_t *bt, int max_blocks, const int32_t *pos, int B, const float *rope,
-                    int max_pos, int32_t *err, cudaStream_t s)
+int fp8_append_rope(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, const uint16_t *q,
+                    uint16_t *q_out, const int32_t *bt, int max_blocks, const int32_t *pos, const int32_t *slots, int B,
+                    const float *rope, int max_pos, int32_t *err, cudaStream_t s)
 {
     return launch_kernel(append_rope_fp8_kernel, dim3(B), dim3(kAppendThreads), 0, s, true,
-                         reinterpret_cast<uint8_t *>(pool->slab), pool->num_pages, k_new, v_new, q, bt, max_blocks,
-                         pos, reinterpret_cast<const float4 *>(rope), max_pos, err);
+                         reinterpret_cast<uint8_t *>(pool->slab), pool->num_pages, k_new, v_new, q, q_out, bt,
+                         max_blocks, pos, slots, reinterpret_cast<const float4 *>(rope), max_pos, err);
 }
 
 int fp8_prefill_append(const pkv_pool *pool, const uint16_t *k, const uint16_t *v, const int32_t *bt_rows,

@@ -218,7 +218,8 @@ struct Fp8MmaWarp {
     }
 
     // unit: the stage -- K code rows, V code rows (64 bytes each), K scales[16], V scales[16]
-    __device__ __forceinline__ void page(const uint8_t *unit, int nvalid)
+    template <class Keep, class Emit = NoScores>
+    __device__ __forceinline__ void page(const uint8_t *unit, Keep keep, const Emit &emit = Emit())
     {
         const uint8_t *codes = unit;
         const float *scales = reinterpret_cast<const float *>(unit + kFp8UnitCodes);
@@ -243,20 +244,26 @@ struct Fp8MmaWarp {
         const float skh00 = sk0 * hf[0], skh01 = sk0 * hf[1], skh10 = sk1 * hf[0], skh11 = sk1 * hf[1];
         float z[4] = {fmaf(s[0], skh00, -m[0]), fmaf(s[1], skh01, -m[1]), fmaf(s[2], skh10, -m[0]),
                       fmaf(s[3], skh11, -m[1])};
-        if (gid >= nvalid) {
+        if (!keep(gid)) {
             z[0] = z[1] = -INFINITY;
             sv0 = 0.f;
         }
-        if (gid + 8 >= nvalid) {
+        if (!keep(gid + 8)) {
             z[2] = z[3] = -INFINITY;
             sv1 = 0.f;
+        }
+        if (tig < 2) {
+            if (keep(gid))
+                emit(gid, 2 * tig, s[0] * skh00, s[1] * skh01);
+            if (keep(gid + 8))
+                emit(gid + 8, 2 * tig, s[2] * skh10, s[3] * skh11);
         }
         float al0 = 1.f, al1 = 1.f;
         if (__any_sync(kFull, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > kDeferLog2)) {
             float x[4] = {s[0] * skh00, s[1] * skh01, s[2] * skh10, s[3] * skh11};
-            if (gid >= nvalid)
+            if (!keep(gid))
                 x[0] = x[1] = -INFINITY;
-            if (gid + 8 >= nvalid)
+            if (!keep(gid + 8))
                 x[2] = x[3] = -INFINITY;
             float pm0 = fmaxf(x[0], x[2]), pm1 = fmaxf(x[1], x[3]);
 #pragma unroll
@@ -318,11 +325,9 @@ struct Fp8MmaWarp {
             e4m3x4_to_f16x2(w0[i], a[i][0], a[i][1]);  // dim 8gid+2i | 8gid+2i+1, tokens 2tig, 2tig+1
             e4m3x4_to_f16x2(w1[i], a[i][2], a[i][3]);  // same dims, tokens 2tig+8, 2tig+9
         }
-        if (nvalid < kPage) {  // zero V of slots past the sequence end (their bytes are arbitrary)
-            const uint32_t mlo =
-                (2 * tig < nvalid ? 0x0000ffffu : 0u) | (2 * tig + 1 < nvalid ? 0xffff0000u : 0u);
-            const uint32_t mhi =
-                (2 * tig + 8 < nvalid ? 0x0000ffffu : 0u) | (2 * tig + 9 < nvalid ? 0xffff0000u : 0u);
+        if (!keep.all()) {  // zero V of slots not attended to (their bytes are arbitrary)
+            const uint32_t mlo = (keep(2 * tig) ? 0x0000ffffu : 0u) | (keep(2 * tig + 1) ? 0xffff0000u : 0u);
+            const uint32_t mhi = (keep(2 * tig + 8) ? 0x0000ffffu : 0u) | (keep(2 * tig + 9) ? 0xffff0000u : 0u);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 a[i][0] &= mlo;

@@ -459,16 +459,124 @@ def pkv_pool_kv_format(pool) -> int:
     return st
 
 
+# ---------------------------------------------------------------------------- long contexts
+
+EXPORTED = EXPORTED + (
+    "pkv_decode_window", "pkv_decode_step_window", "pkv_decode_window_workspace_bytes", "pkv_decode_shared",
+    "pkv_decode_shared_workspace_bytes", "pkv_decode_scored", "pkv_decode_scored_workspace_bytes", "pkv_evict",
+    "pkv_evict_workspace_bytes", "pkv_append_rope_at",
+)
+
+_lib_fp8 = lib
+
+
+def lib():  # noqa: F811 -- extends the loader with the long-context signatures
+    L = _lib_fp8()
+    if not getattr(L, "_pkv_long_bound", False):
+        f, z, i64 = ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+        L.pkv_decode_window.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, f, _i32, _i32, _i32, _vp, z, _vp, _vp, _vp,
+                                        _i32]
+        L.pkv_decode_step_window.argtypes = [_vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _i32, f, _i32, _i32, _i32,
+                                             _vp, z, _vp, _vp, _vp, _i32]
+        L.pkv_decode_window_workspace_bytes.argtypes = [_i32] * 5
+        L.pkv_decode_shared.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp, _i32, _i32, f, _i32, _i32, _vp, z,
+                                        _vp, _vp, _vp, _i32]
+        L.pkv_decode_shared_workspace_bytes.argtypes = [_i32] * 6
+        L.pkv_decode_scored.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, f, _vp, _vp, i64, _i32, _vp, z, _vp, _vp, _vp,
+                                        _i32]
+        L.pkv_decode_scored_workspace_bytes.argtypes = [_i32] * 3
+        L.pkv_evict.argtypes = [_vp, _vp, _i32, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, i64, _vp, i64, _vp, _vp,
+                                _vp, z, _vp, _vp]
+        L.pkv_evict_workspace_bytes.argtypes = [_i32] * 2
+        L.pkv_append_rope_at.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _i32, _vp, _i32, _vp, _vp]
+        for name in EXPORTED[-10:]:
+            getattr(L, name).restype = z if name.endswith("_workspace_bytes") else ctypes.c_int
+        L._pkv_long_bound = True
+    return L
+
+
+def pkv_decode_window_workspace_bytes(B: int, max_blocks: int, window: int, sinks: int, pages_per_chunk: int) -> int:
+    return int(lib().pkv_decode_window_workspace_bytes(B, max_blocks, window, sinks, pages_per_chunk))
+
+
+def pkv_decode_window(pool, q, bt_dev, max_blocks: int, seq_lens_dev, B: int, scale: float, window: int, sinks: int,
+                      pages_per_chunk: int, workspace, workspace_bytes: int, out, dev_err_flag=None, stream=None,
+                      options: int = PKV_DECODE_DEFAULT) -> None:
+    _check(lib().pkv_decode_window(pool, _ptr(q), _ptr(bt_dev), max_blocks, _ptr(seq_lens_dev), B, float(scale),
+                                   int(window), int(sinks), pages_per_chunk, _ptr(workspace), int(workspace_bytes),
+                                   _ptr(out), _ptr(dev_err_flag), _stream(stream), int(options)), "pkv_decode_window")
+
+
+def pkv_decode_step_window(pool, k_new, v_new, q, bt_dev, max_blocks: int, seq_lens_dev, B: int, rope_table,
+                           max_pos: int, scale: float, window: int, sinks: int, pages_per_chunk: int, workspace,
+                           workspace_bytes: int, out, dev_err_flag=None, stream=None,
+                           options: int = PKV_DECODE_DEFAULT) -> None:
+    _check(lib().pkv_decode_step_window(pool, _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(bt_dev), max_blocks,
+                                        _ptr(seq_lens_dev), B, _ptr(rope_table), max_pos, float(scale), int(window),
+                                        int(sinks), pages_per_chunk, _ptr(workspace), int(workspace_bytes), _ptr(out),
+                                        _ptr(dev_err_flag), _stream(stream), int(options)), "pkv_decode_step_window")
+
+
+def pkv_decode_shared_workspace_bytes(B: int, max_blocks: int, groups: int, max_prefix_pages: int,
+                                      pages_per_chunk: int, prefix_pages_per_chunk: int) -> int:
+    return int(lib().pkv_decode_shared_workspace_bytes(B, max_blocks, groups, max_prefix_pages, pages_per_chunk,
+                                                       prefix_pages_per_chunk))
+
+
+def pkv_decode_shared(pool, q, bt_dev, max_blocks: int, seq_lens_dev, B: int, group_starts_dev, prefix_pages_dev,
+                      groups: int, max_prefix_pages: int, scale: float, pages_per_chunk: int,
+                      prefix_pages_per_chunk: int, workspace, workspace_bytes: int, out, dev_err_flag=None,
+                      stream=None, options: int = PKV_DECODE_DEFAULT) -> None:
+    _check(lib().pkv_decode_shared(pool, _ptr(q), _ptr(bt_dev), max_blocks, _ptr(seq_lens_dev), B,
+                                   _ptr(group_starts_dev), _ptr(prefix_pages_dev), groups, max_prefix_pages,
+                                   float(scale), pages_per_chunk, prefix_pages_per_chunk, _ptr(workspace),
+                                   int(workspace_bytes), _ptr(out), _ptr(dev_err_flag), _stream(stream),
+                                   int(options)), "pkv_decode_shared")
+
+
+def pkv_decode_scored_workspace_bytes(B: int, max_blocks: int, pages_per_chunk: int) -> int:
+    return int(lib().pkv_decode_scored_workspace_bytes(B, max_blocks, pages_per_chunk))
+
+
+def pkv_decode_scored(pool, q, bt_dev, max_blocks: int, seq_lens_dev, B: int, scale: float, acc, acc_out,
+                      acc_stride: int, pages_per_chunk: int, workspace, workspace_bytes: int, out, dev_err_flag=None,
+                      stream=None, options: int = PKV_DECODE_DEFAULT) -> None:
+    _check(lib().pkv_decode_scored(pool, _ptr(q), _ptr(bt_dev), max_blocks, _ptr(seq_lens_dev), B, float(scale),
+                                   _ptr(acc), _ptr(acc_out), int(acc_stride), pages_per_chunk, _ptr(workspace),
+                                   int(workspace_bytes), _ptr(out), _ptr(dev_err_flag), _stream(stream),
+                                   int(options)), "pkv_decode_scored")
+
+
+def pkv_evict_workspace_bytes(B: int, keep: int) -> int:
+    return int(lib().pkv_evict_workspace_bytes(B, keep))
+
+
+def pkv_evict(pool, bt_src_dev, src_blocks: int, seq_lens_dev, B: int, bt_dst_dev, dst_blocks: int, keep: int,
+              recent: int, sinks: int, acc, acc_stride: int, acc_out, acc_out_stride: int, kept, seq_lens_out,
+              workspace, workspace_bytes: int, dev_err_flag=None, stream=None) -> None:
+    _check(lib().pkv_evict(pool, _ptr(bt_src_dev), src_blocks, _ptr(seq_lens_dev), B, _ptr(bt_dst_dev), dst_blocks,
+                           int(keep), int(recent), int(sinks), _ptr(acc), int(acc_stride), _ptr(acc_out),
+                           int(acc_out_stride), _ptr(kept), _ptr(seq_lens_out), _ptr(workspace), int(workspace_bytes),
+                           _ptr(dev_err_flag), _stream(stream)), "pkv_evict")
+
+
+def pkv_append_rope_at(pool, k_new, v_new, q, q_out, bt_dev, max_blocks: int, pos_dev, slots_dev, B: int, rope_table,
+                       max_pos: int, dev_err_flag=None, stream=None) -> None:
+    _check(lib().pkv_append_rope_at(pool, _ptr(k_new), _ptr(v_new), _ptr(q), _ptr(q_out), _ptr(bt_dev), max_blocks,
+                                    _ptr(pos_dev), _ptr(slots_dev), B, _ptr(rope_table), max_pos, _ptr(dev_err_flag),
+                                    _stream(stream)), "pkv_append_rope_at")
+
+
 # ---------------------------------------------------------------------------- read-bandwidth probes
 
 # every symbol include/pkv_probe.h declares (a measurement aid, not the decode path)
 EXPORTED_PROBE = ("pkv_probe_read_ldg", "pkv_probe_read_bulk")
 
-_lib_fp8 = lib
+_lib_long = lib
 
 
 def lib():  # noqa: F811 -- extends the loader with the probe signatures
-    L = _lib_fp8()
+    L = _lib_long()
     if not getattr(L, "_pkv_probe_bound", False):
         for name in EXPORTED_PROBE:
             getattr(L, name).argtypes = [_vp, ctypes.c_size_t, _vp, _i32, _vp]
