@@ -17,7 +17,7 @@ namespace pkv {
 namespace {
 
 struct ScoredPages {
-    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false;
+    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
     float *scores;  // [B][8][tokens][4]
     float *lse;     // [B][32] log2 of the sum of 2^score
     int tokens;     // per (sequence, KV head): 16 * max_blocks

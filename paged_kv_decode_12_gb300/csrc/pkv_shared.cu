@@ -1,43 +1,780 @@
 // pkv_shared.cu -- decode attention for groups of sequences that share a prefix.
 #include "pkv_step.cuh"
+#include "pkv_tc.cuh"
 
 namespace pkv {
 namespace {
 
-// Every page of the sequence, the prefix's through the table row of the group's first
-// sequence.
-struct SharedPages {
-    static constexpr bool kIdentity = false, kSortable = false, kLateWait = false;
-    const int32_t *starts, *prefix_pages;
-    int groups, max_prefix;
+constexpr int kTilePages = 8;                       // pages of one key tile: 128 tokens
+constexpr int kHalf = kTilePages * kPage / 2;       // its halves
+constexpr int kRowTile = 128;                       // query rows of one tensor-core tile
+constexpr int kTileSeqs = kRowTile / kGroup;        // 32 sequences x the 4 heads of a KV head
 
-    struct List : WholeSequence {
-        int lead, prefix;  // the group's first sequence, its prefix pages (-1: no such group)
-        __device__ __forceinline__ int row(int b, int j) const { return j < prefix ? lead : b; }
+// The groups of a call: group i is sequences starts[i] .. starts[i + 1] - 1, its prefix
+// prefix_pages[i] pages in chunks of chunk_pages.
+struct Groups {
+    const int32_t *starts, *prefix_pages;
+    int groups, max_prefix, chunk_pages, B;
+
+    struct Group {
+        int s0, n, prefix;
+        bool ok;
+    };
+    // Group i, not ok if its bounds leave the batch or its prefix the announced range.
+    __device__ __forceinline__ Group at(int i) const
+    {
+        Group x;
+        x.s0 = starts[i];
+        const int s1 = starts[i + 1];
+        x.prefix = prefix_pages[i];
+        x.ok = x.s0 >= 0 && s1 <= B && x.s0 < s1 && x.prefix >= 0 && x.prefix <= max_prefix;
+        x.n = x.ok ? s1 - x.s0 : 0;
+        return x;
+    }
+    __device__ __forceinline__ int chunks(int prefix) const { return (prefix + chunk_pages - 1) / chunk_pages; }
+};
+
+// The pages of a sequence behind its group's prefix; the prefix's partials come first.  MERGE:
+// the units wait for the prefix's partials and merge; else merge_kernel does.
+template <bool MERGE>
+struct OwnPages {
+    static constexpr bool kIdentity = false, kSortable = false, kLateWait = MERGE, kPublish = !MERGE, kLoops = true;
+    Groups gr;
+
+    struct List {
+        int L, prefix, slots;  // prefix < 0: the sequence is in no valid group
         __device__ __forceinline__ bool ok() const { return prefix >= 0 && (int64_t)prefix * kPage <= L; }
+        __device__ __forceinline__ int count() const { return (L + kPage - 1) / kPage - prefix; }
+        __device__ __forceinline__ int logical(int i) const { return i + prefix; }
+        __device__ __forceinline__ int before(int j) const { return max(j - prefix, 0); }
+        __device__ __forceinline__ FirstTokens tokens(int j) const { return {min(kPage, L - j * kPage)}; }
+        __device__ __forceinline__ int row(int b, int) const { return b; }
+        __device__ __forceinline__ int first_slot() const { return slots; }
     };
 
+    // (the whole warp looks for the group of b)
     __device__ __forceinline__ List list(int b, int L) const
     {
-        List x;
-        x.L = L;
-        x.lead = 0;
-        x.prefix = -1;
-        for (int i = threadIdx.x & 31; i < groups; i += 32) {
-            const int s0 = starts[i], s1 = starts[i + 1], p = prefix_pages[i];
-            if (s0 >= 0 && s0 <= b && b < s1 && p >= 0 && p <= max_prefix) {
-                x.lead = s0;
-                x.prefix = p;
-            }
+        int prefix = -1;
+        for (int i = threadIdx.x & 31; i < gr.groups; i += 32) {
+            const Groups::Group x = gr.at(i);
+            if (x.ok && x.s0 <= b && b < x.s0 + x.n)
+                prefix = x.prefix;
         }
-        x.prefix = __reduce_max_sync(kFull, x.prefix);
-        x.lead = __reduce_max_sync(kFull, x.lead);
-        return x;
+        prefix = __reduce_max_sync(kFull, prefix);
+        return {L, prefix, prefix > 0 ? gr.chunks(prefix) : 0};
     }
     __device__ __forceinline__ EmitNothing emit(int, int) const { return {}; }
     __device__ __forceinline__ void skipped(int, int, int, int) const {}
     __device__ __forceinline__ void norm(int, int, float, float) const {}
 };
+
+// ------------------------------------------------------------------ the prefix on tensor cores
+
+constexpr int kStageSize = kTilePages * kStageBytes;           // 32 KiB: 8 x (K rows, V rows)
+constexpr int kRawSize = kTilePages * kFp8Unit;                // 17 KiB: FP8 units as they lie in the pages
+constexpr int kRaws = 3;                                       // of them in flight
+constexpr int kLoader = 8, kIssuer = 9, kConverter = 11;       // warps: 2 x 4 softmax, loader, two issuers, (FP8) four
+constexpr int kConverters = 4;                                 // converters
+constexpr int kScales = 2 * kTilePages * kPage;                // row scales of a tile: K's, then V's
+constexpr int kCols = 512;                                     // tensor memory, all of it
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;        // + 128 / 64 / 32 for the second tile
+
+// FP8 pages leave room for three stages beside the raw units.
+constexpr int stages_of(bool fp8) { return fp8 ? 3 : 4; }
+constexpr int prefix_threads(bool fp8) { return (kConverter + (fp8 ? kConverters : 0)) * 32; }
+
+struct PrefixBars {
+    uint64_t full[4], empty[4];              // a stage holds its pages / both tiles are done with it
+    uint64_t raw_full[kRaws], raw_empty[kRaws];  // the same of the raw units
+    uint64_t s_full[2][2], p_full[2][2];     // [row tile][half]: scores are in tensor memory / weights are
+    uint64_t o_step[2];                      // one more product of weights and values is done
+    uint64_t q_full[2], o_full[2];           // once an item: the queries are in / its last product is done
+    uint32_t tmem;
+    int stop;                                // a wait gave up
+    int bad[4], raw_bad[kRaws];              // the tile has a bad page id
+    uint64_t drained[2];
+    // FP8: a stage's row scales, [K (times scale log2 e), V][half][64] in the order of S's columns
+    float scales[3][kScales];
+};
+
+struct PrefixArgs {
+    Groups gr;
+    int num_pages;
+    const uint16_t *q;   // [B][32][64]
+    const int32_t *bt;
+    int max_blocks;
+    float scale_log2;
+    float2 *part_ml;
+    float *part_o;
+    int max_chunks;
+    int32_t *err;
+};
+
+// A work item: two tiles of 128 query rows of one KV head, each with its run of key tiles.
+struct Item {
+    int g;              // KV head
+    int lead;           // the sequence whose table row holds the prefix
+    int s0[2], ns[2];   // each tile's sequences (ns <= 32; 0: no such tile)
+    int chunk[2];       // each tile's chunk
+    int j0[2], np[2];   // its pages
+    bool shared;        // both tiles go through the same pages
+    __device__ __forceinline__ int tiles(int s) const { return (np[s] + kTilePages - 1) / kTilePages; }
+    // the place in the loader's order of tile s's j-th key tile: the pages of a shared run are
+    // loaded once, two runs of their own alternate as long as both last (the first is no shorter)
+    __device__ __forceinline__ int order(int s, int j) const
+    {
+        return shared ? j : j < tiles(1) ? 2 * j + s : tiles(1) + j;
+    }
+    __device__ __forceinline__ int loads() const { return shared ? tiles(0) : tiles(0) + tiles(1); }
+};
+
+// Item `it` of the call (the whole warp): the row tiles of a group are paired and each pair goes
+// through every chunk; an odd last row tile takes two chunks at a time.  Pairs that read the
+// same pages are neighbours, so that the pages come from L2.
+__device__ __forceinline__ bool find_item(const Groups &gr, int it, Item &x)
+{
+    const int lane = threadIdx.x & 31;
+    int64_t base = 0;
+    for (int i0 = 0; i0 < gr.groups; i0 += 32) {
+        Groups::Group gp = {0, 0, 0, false};
+        if (i0 + lane < gr.groups)
+            gp = gr.at(i0 + lane);
+        const int tiles = (gp.n + kTileSeqs - 1) / kTileSeqs;
+        const int chunks = gp.ok ? gr.chunks(gp.prefix) : 0;
+        const int64_t mine = (int64_t)kHkv * ((int64_t)(tiles / 2) * chunks + (tiles & 1) * ((chunks + 1) / 2));
+        int64_t end = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, end, off);
+            if (lane >= off)
+                end += y;
+        }
+        end += base;
+        const unsigned hit = __ballot_sync(kFull, it < end);
+        if (hit) {
+            const int src = __ffs(hit) - 1;
+            const int local = it - (int)__shfl_sync(kFull, end - mine, src);
+            const int s0 = __shfl_sync(kFull, gp.s0, src), n = __shfl_sync(kFull, gp.n, src);
+            const int prefix = __shfl_sync(kFull, gp.prefix, src);
+            const int nt = (n + kTileSeqs - 1) / kTileSeqs, nc = gr.chunks(prefix), pairs = nt / 2;
+            const int paired = kHkv * pairs * nc;
+            x.lead = s0;
+            int rt[2];
+            x.shared = local < paired;
+            if (x.shared) {
+                rt[0] = 2 * (local % pairs);
+                rt[1] = rt[0] + 1;
+                x.g = local / pairs % kHkv;
+                x.chunk[0] = x.chunk[1] = local / pairs / kHkv;
+            } else {
+                rt[0] = rt[1] = nt - 1;
+                x.g = (local - paired) % kHkv;
+                x.chunk[0] = (local - paired) / kHkv * 2;
+                x.chunk[1] = x.chunk[0] + 1;
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                x.j0[s] = x.chunk[s] * gr.chunk_pages;
+                x.np[s] = max(min(prefix - x.j0[s], gr.chunk_pages), 0);
+                x.s0[s] = s0 + rt[s] * kTileSeqs;
+                x.ns[s] = x.np[s] > 0 ? min(kTileSeqs, n - rt[s] * kTileSeqs) : 0;
+            }
+            return true;
+        }
+        base = __shfl_sync(kFull, end, 31);
+    }
+    return false;
+}
+
+// Loader: the pages of every item's key tiles into the ring of stages (FP8: of raw units).  A
+// tile that the chunk does not fill repeats the chunk's last page (its weights are masked); a
+// bad page id is replaced by page 0 and the tile marked.
+template <bool FP8>
+__device__ __forceinline__ void prefix_loader(const CUtensorMap *tmap, const PrefixArgs &a, uint8_t *ring, PrefixBars &bars)
+{
+    constexpr int kRing = FP8 ? kRaws : stages_of(false), kSize = FP8 ? kRawSize : kStageSize;
+    uint64_t *full = FP8 ? bars.raw_full : bars.full, *empty = FP8 ? bars.raw_empty : bars.empty;
+    int *marks = FP8 ? bars.raw_bad : bars.bad;
+    const int lane = threadIdx.x & 31;
+    uint64_t policy;  // pages are read by several CTAs: no eviction hint
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+    Item x;
+    int seq = 0;
+    bool go = true;
+    for (int it = blockIdx.x; go && find_item(a.gr, it, x); it += gridDim.x) {
+        const int32_t *row = a.bt + (size_t)x.lead * a.max_blocks;
+        const int most = x.tiles(0);
+        int ids[2] = {0, 0};  // lane l: the id of page l of the current run of 4 key tiles
+        unsigned bad[2] = {0, 0};
+        for (int j = 0; j < most && go; ++j) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                if ((s == 1 && x.shared) || j >= x.tiles(s) || !go)
+                    continue;
+                if (j % 4 == 0) {
+                    ids[s] = row[x.j0[s] + min(j * kTilePages + lane, x.np[s] - 1)];
+                    const bool out = ids[s] < 0 || ids[s] >= a.num_pages;
+                    bad[s] = __ballot_sync(kFull, out);
+                    if (out)
+                        ids[s] = 0;
+                }
+                const int st = seq % kRing;
+                if (seq >= kRing && !tc::wait_warp(&empty[st], (seq / kRing - 1) & 1, &bars.stop)) {
+                    go = false;
+                    continue;
+                }
+                const int id = __shfl_sync(kFull, ids[s], j % 4 * kTilePages + lane % kTilePages);
+                if (lane == 0) {
+                    marks[st] = (bad[s] >> (j % 4 * kTilePages)) & ((1u << kTilePages) - 1);
+                    mbar_arrive_expect_tx(&full[st], kSize);
+                }
+                __syncwarp();
+                if (lane < kTilePages) {
+                    if (FP8)
+                        fp8::tma_load_unit(ring + st * kSize + lane * kFp8Unit, tmap, &full[st], x.g, id, policy);
+                    else
+                        tma_load_page_head(ring + st * kSize + lane * kStageBytes, tmap, &full[st], x.g, id, policy);
+                }
+                ++seq;
+            }
+        }
+    }
+    if (bars.stop)  // let the copies in flight land (bounded)
+        for (int i = max(seq - kRing, 0); i < seq; ++i)
+            (void)mbar_wait_warp(&full[i % kRing], (i / kRing) & 1);
+}
+
+// Two E4M3 codes as BF16 (exact: 4 significant bits, exponents in range; NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t h)
+{
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16x2(f.x, f.y);
+}
+
+__device__ __forceinline__ void bf16_of_e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    uint32_t a, b;
+    fp8::e4m3x4_to_f16x2(w, a, b);
+    lo = bf16x2_of_f16x2(a);
+    hi = bf16x2_of_f16x2(b);
+}
+
+// Converters (FP8; 128 threads): raw units into a stage of the BF16 layout.  The codes become
+// BF16 as they are; the row scales go to the scores and the weights instead of the rows, so
+// that nothing is rounded here.
+__device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint8_t *raws, uint8_t *stages, PrefixBars &bars)
+{
+    constexpr int kRing = stages_of(true);
+    const int t = threadIdx.x - kConverter * 32, lane = threadIdx.x & 31;
+    Item x;
+    int seq = 0;
+    for (int it = blockIdx.x; find_item(a.gr, it, x); it += gridDim.x) {
+        const int n = x.loads();
+        for (int i = 0; i < n; ++i, ++seq) {
+            const int rs = seq % kRaws, st = seq % kRing;
+            if (!tc::wait_warp(&bars.raw_full[rs], (seq / kRaws) & 1, &bars.stop) ||
+                (seq >= kRing && !tc::wait_warp(&bars.empty[st], (seq / kRing - 1) & 1, &bars.stop)))
+                return;
+            const uint8_t *raw = raws + rs * kRawSize;
+            uint8_t *dst = stages + st * kStageSize;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // K: 16 codes of a row, two chunks of 8 values
+                const int u = t + 128 * k, page = u / 64, row = u % 64 / 4, part = u % 4;
+                const uint4 c = *reinterpret_cast<const uint4 *>(raw + page * kFp8Unit + row * kD + part * 16);
+                uint4 lo, hi;
+                bf16_of_e4m3x4(c.x, lo.x, lo.y);
+                bf16_of_e4m3x4(c.y, lo.z, lo.w);
+                bf16_of_e4m3x4(c.z, hi.x, hi.y);
+                bf16_of_e4m3x4(c.w, hi.z, hi.w);
+                *reinterpret_cast<uint4 *>(dst + page * kStageBytes + swz(row, 2 * part)) = lo;
+                *reinterpret_cast<uint4 *>(dst + page * kStageBytes + swz(row, 2 * part + 1)) = hi;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // V: 8 dims of the tokens 2 pair, 2 pair + 1, codes alternating
+                const int u = t + 128 * k, page = u / 64, pair = u % 64 / 8, at = u % 8, chunk = at ^ ((2 * pair) & 7);
+                const uint4 c = *reinterpret_cast<const uint4 *>(raw + page * kFp8Unit + fp8::kFp8Tile + pair * 2 * kD + at * 16);
+                uint4 even, odd;
+                bf16_of_e4m3x4(__byte_perm(c.x, c.y, 0x6420), even.x, even.y);
+                bf16_of_e4m3x4(__byte_perm(c.z, c.w, 0x6420), even.z, even.w);
+                bf16_of_e4m3x4(__byte_perm(c.x, c.y, 0x7531), odd.x, odd.y);
+                bf16_of_e4m3x4(__byte_perm(c.z, c.w, 0x7531), odd.z, odd.w);
+                uint8_t *v = dst + page * kStageBytes + kTileBytes;
+                *reinterpret_cast<uint4 *>(v + swz(2 * pair, chunk)) = even;
+                *reinterpret_cast<uint4 *>(v + swz(2 * pair + 1, chunk)) = odd;
+            }
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {  // thread = (page, slot)
+                const int page = t / kPage, slot = t % kPage;
+                const float f = reinterpret_cast<const float *>(raw + page * kFp8Unit + kFp8UnitCodes)[kv * kPage + slot];
+                bars.scales[st][kv * 128 + slot / 8 * 64 + page * 8 + slot % 8] = kv ? f : f * a.scale_log2;
+            }
+            if (t == 0)
+                bars.bad[st] = bars.raw_bad[rs];
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(&bars.raw_empty[rs]);
+                tc::mbar_arrive(&bars.full[st]);
+            }
+        }
+    }
+}
+
+// Issuer (a converged warp, one elected thread of which issues): the matrix products of every
+// item.  A key tile goes through in two halves of 64 tokens (slots 0..7 and 8..15 of its 8
+// pages), each with scores of its own in tensor memory: while the softmax of one half runs, the
+// other half's weights meet the values and its columns take the next tile's scores.
+__device__ __forceinline__ void issue_scores(uint32_t k, uint32_t s, uint32_t q, uint64_t *done)
+{
+    // S[128 x 64] = Q K^T: columns 8 p + i are slot 8 h + i of page p (page stride 4 KiB)
+    constexpr uint32_t kIdesc = tc::instr_desc(64, true, false), kHi = tc::smem_desc_hi(kStageBytes);
+    const uint32_t lo = tc::smem_desc_lo(k, kStageBytes);
+    if (tc::elect()) {
+        tc::mma_ts<false>(s, q, lo, kHi, kIdesc);
+#pragma unroll
+        for (int i = 1; i < kD / 16; ++i)
+            tc::mma_ts<true>(s, q + i * 8, lo + i * 2, kHi, kIdesc);
+        tc::commit(done);
+    }
+    __syncwarp();
+}
+
+template <bool FIRST>
+__device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p, uint64_t *free_stage, int uses,
+                                             uint64_t *done, uint64_t *last)
+{
+    // O[128 x 64] += P V: 16 columns of P are 8 slots of two pages
+    constexpr uint32_t kIdesc = tc::instr_desc(64, true, true), kHi = tc::smem_desc_hi(kStageBytes);
+    const uint32_t lo = tc::smem_desc_lo(v, kStageBytes);
+    if (tc::elect()) {
+        tc::mma_ts<!FIRST>(o, p, lo, kHi, kIdesc);
+#pragma unroll
+        for (int i = 1; i < kHalf / 16; ++i)
+            tc::mma_ts<true>(o, p + i * 8, lo + i * (2 * kStageBytes / 16), kHi, kIdesc);
+        tc::commit(done);
+        if (last)
+            tc::commit(last);
+        if (free_stage) {
+            tc::commit(free_stage);
+            if (uses > 1)
+                tc::commit(free_stage);
+        }
+    }
+    __syncwarp();
+}
+
+// Each row tile has an issuer warp of its own, so that one's waits pass while the other's
+// products run: the tensor cores take only a few instructions ahead.
+template <int kStages>
+__device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stages, PrefixBars &bars, uint32_t tmem, int s)
+{
+    const uint32_t base = smem_addr(stages);
+    const uint32_t ts = tmem + kColS + s * 128, to = tmem + kColO + s * 64, tq = tmem + kColQ + s * 32;
+    Item x;
+    int loaded = 0;  // key tiles of earlier items
+    int done = 0;    // of them, this row tile's
+    int items = 0;   // earlier items with such a row tile
+    const auto scores = [&](int j, int h) {
+        const int seq = loaded + x.order(s, j), st = seq % kStages;
+        if (h == 0) {
+            if (!tc::wait_warp(&bars.full[st], (seq / kStages) & 1, &bars.stop))
+                return false;
+            tc::fence_after();
+        }
+        issue_scores(base + st * kStageSize + h * 1024, ts + h * kHalf, tq, &bars.s_full[s][h]);
+        return true;
+    };
+    const auto output = [&](int j, int h, int nt) {
+        if (!tc::wait_warp(&bars.p_full[s][h], (done + j) & 1, &bars.stop))
+            return false;
+        tc::fence_after();
+        const int st = (loaded + x.order(s, j)) % kStages;
+        const uint32_t v = base + st * kStageSize + kTileBytes + h * 1024, p = ts + h * kHalf;
+        uint64_t *empty = h == 1 ? &bars.empty[st] : nullptr;
+        uint64_t *last = h == 1 && j + 1 == nt ? &bars.o_full[s] : nullptr;
+        const int uses = x.shared ? 1 : 2;  // a stage is free after two arrivals
+        if (j == 0 && h == 0)
+            issue_output<true>(v, to, p, empty, uses, &bars.o_step[s], last);
+        else
+            issue_output<false>(v, to, p, empty, uses, &bars.o_step[s], last);
+        return true;
+    };
+    for (int it = blockIdx.x; find_item(a.gr, it, x); it += gridDim.x) {
+        const int nt = x.tiles(s);
+        if (nt) {
+            bool go = tc::wait_warp(&bars.q_full[s], items & 1, &bars.stop);
+            tc::fence_after();
+            go = go && scores(0, 0) && scores(0, 1);
+            for (int j = 0; j < nt && go; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (go) {
+                        go = output(j, h, nt);
+                        if (go && j + 1 < nt)
+                            go = scores(j + 1, h);
+                    }
+            if (!go) {  // let the products in flight end (bounded)
+                if (tc::elect())
+                    tc::commit(&bars.drained[s]);
+                __syncwarp();
+                (void)mbar_wait_warp(&bars.drained[s], 0);
+                return;
+            }
+            ++items;
+        }
+        loaded += x.loads();
+        done += nt;
+    }
+}
+
+// What turns 64 scores into exponents and weights into the second product's operand: one
+// factor, or (FP8) a factor and a scale for every column.
+struct OneFactor {
+    float c;
+    __device__ __forceinline__ float2 factor(int) const { return make_float2(c, c); }
+    __device__ __forceinline__ float2 weight(int, float2 e) const { return e; }
+};
+
+struct RowScales {
+    const float2 *k, *v;  // 32 pairs of columns
+    __device__ __forceinline__ float2 factor(int i) const { return k[i]; }
+    __device__ __forceinline__ float2 weight(int i, float2 e) const { return tc::mul2(e, v[i]); }
+};
+
+// 32 scores of one query row (columns 32 k ..) as weights 2^(S c - m): their sum, and the weights
+// in pairs rounded to BF16 for the second product.  MASK: columns of pages from `pages` on weigh
+// nothing.  Four chains of sums, so that no chain's latency is the time of the whole.
+template <bool MASK, class Scale>
+__device__ __forceinline__ float make_weights(uint32_t ts, int k, const Scale &sc, int pages, float m, uint32_t (&pk)[16])
+{
+    uint32_t w[32];
+    tc::ld32(ts + k * 32, w);
+    float2 sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sum[i] = make_float2(0.f, 0.f);
+    const float2 m2 = make_float2(-m, -m);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 x =
+            tc::fma2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i), m2);
+        float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        if (MASK && !(k * 4 + i / 4 < pages))
+            e = make_float2(0.f, 0.f);
+        sum[i % 4] = tc::add2(sum[i % 4], e);
+        const float2 p = sc.weight(k * 16 + i, e);
+        pk[i] = pack_bf16x2(p.x, p.y);
+    }
+    const float2 s = tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3]));
+    return s.x + s.y;
+}
+
+// Their maximum, times the factors.
+template <bool MASK, class Scale>
+__device__ __forceinline__ float max_score(uint32_t ts, int k, const Scale &sc, int pages)
+{
+    uint32_t w[32];
+    tc::ld32(ts + k * 32, w);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 x = tc::mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i));
+        if (!MASK || k * 4 + i / 4 < pages)
+            mx = tc::max3(mx, x.x, x.y);
+    }
+    return mx;
+}
+
+// The reference m of a row's softmax is its first half tile's maximum, and it stays until a
+// half tile's weights sum to 2^64 or more: FP32 and BF16 hold 2^127, so m, l and O remain a
+// valid log-sum-exp triple that far above m, and no maximum is taken on the way.  (Moving m for
+// every score 2^8 above it, as narrower types need, made most half tiles of 32 rows rescale O.)
+constexpr float kMostWeight = 18446744073709551616.f;
+
+// Half a key tile's scores of one query row become weights, in place: P is the first half of
+// S's columns.  MASK: only the first `pages` pages of the tile count.  Returns false if a wait
+// gave up.
+template <bool MASK, class Scale>
+__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, const Scale &sc, int pages, int before,
+                                             uint64_t *o_step, bool first, volatile int *stop, float &m, float &l)
+{
+    uint32_t p0[16], p1[16];
+    float s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
+    const bool move = first || !(s < kMostWeight);
+    if (__any_sync(kFull, move)) {
+        const float top = fmaxf(max_score<MASK>(ts, 0, sc, pages), max_score<MASK>(ts, 1, sc, pages));
+        const float mn = move ? (first ? top : fmaxf(top, m)) : m;
+        const float f = first ? 0.f : ex2_approx(m - mn);  // 1 where the reference stays
+        m = mn;
+        l *= f;
+        s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
+        // Once the product before this one is done, nothing else touches O.  (These scores came
+        // after the product before that, so the wait is one phase behind at most.)
+        if (!first) {
+            if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
+                return false;
+            tc::fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t o[16];
+                tc::ld16(to + k * 16, o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tc::st16(to + k * 16, o);
+            }
+        }
+    }
+    l += s;
+    tc::st16(ts, p0);  // columns 2i, 2i + 1 of S are column i of P
+    tc::st16(ts + 16, p1);
+    tc::wait_st();
+    return true;
+}
+
+// Softmax warps of row tile s: thread = query row (sequence r / 4 of the tile, head r % 4).
+template <bool FP8>
+__device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &bars, uint32_t tmem, int s)
+{
+    constexpr int kStages = stages_of(FP8);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int r = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + kColS + s * 128, to = tmem + lanes + kColO + s * 64,
+                   tq = tmem + lanes + kColQ + s * 32;
+    Item x;
+    int loaded = 0, done = 0, items = 0;
+    for (int it = blockIdx.x; find_item(a.gr, it, x); it += gridDim.x) {
+        const int nt = x.tiles(s);
+        if (nt == 0) {
+            loaded += x.loads();
+            continue;
+        }
+        const bool live = r / kGroup < x.ns[s];
+        const int b = x.s0[s] + r / kGroup, h = x.g * kGroup + r % kGroup;
+        {  // the query row: 64 values, two to a column
+            uint32_t w[32];
+            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((size_t)b * kHq + h) * kD);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+                w[4 * i] = v.x;
+                w[4 * i + 1] = v.y;
+                w[4 * i + 2] = v.z;
+                w[4 * i + 3] = v.w;
+            }
+            tc::st32(tq, w);
+            tc::wait_st();
+            tc::fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(&bars.q_full[s]);
+        }
+        float m = 0.f, l = 0.f;
+        int bad = 0;
+        for (int j = 0; j < nt; ++j) {
+            const int pages = x.np[s] - j * kTilePages;
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                if (!tc::wait_warp(&bars.s_full[s][hf], (done + j) & 1, &bars.stop))
+                    return;
+                tc::fence_after();
+                const int before = 2 * (done + j) + hf;  // products of this row tile so far
+                const bool first = j == 0 && hf == 0;
+                const int seq = loaded + x.order(s, j), st = seq % kStages;
+                const auto half = [&](const auto &sc) {
+                    return pages >= kTilePages
+                               ? softmax_half<false>(ts + hf * kHalf, to, sc, kTilePages, before, &bars.o_step[s], first,
+                                                     &bars.stop, m, l)
+                               : softmax_half<true>(ts + hf * kHalf, to, sc, pages, before, &bars.o_step[s], first,
+                                                    &bars.stop, m, l);
+                };
+                bool go;
+                if constexpr (FP8) {
+                    // the scales are the converters' writes (the stage is full long since)
+                    if (hf == 0 && !tc::wait_warp(&bars.full[st], (seq / kStages) & 1, &bars.stop))
+                        return;
+                    const float2 *sc = reinterpret_cast<const float2 *>(bars.scales[st]) + hf * 32;
+                    go = half(RowScales{sc, sc + 64});
+                } else {
+                    go = half(OneFactor{a.scale_log2});
+                }
+                if (!go)
+                    return;
+                if (hf == 0)
+                    bad |= *(volatile int *)&bars.bad[st];
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&bars.p_full[s][hf]);
+            }
+        }
+        if (!tc::wait_warp(&bars.o_full[s], items & 1, &bars.stop))
+            return;
+        tc::fence_after();
+        // the chunk's partial; with a bad page id it is empty
+        const size_t idx = ((size_t)b * kHq + h) * a.max_chunks + x.chunk[s];
+#pragma unroll
+        for (int q2 = 0; q2 < 2; ++q2) {
+            uint32_t w[32];
+            tc::ld32(to + q2 * 32, w);
+            if (live) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    reinterpret_cast<float4 *>(a.part_o + idx * kD)[q2 * 8 + i] =
+                        bad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                            : make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
+                                          __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3]));
+            }
+        }
+        if (live)
+            a.part_ml[idx] = bad ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
+        if (bad && r == 0 && a.err)
+            atomicOr(a.err, PKV_DEVERR_PAGE_RANGE);
+        loaded += x.loads();
+        done += nt;
+        ++items;
+    }
+}
+
+template <bool FP8>
+__global__ void __launch_bounds__(prefix_threads(FP8), 1)
+prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
+{
+    constexpr int kStages = stages_of(FP8);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *raws = stages + kStages * kStageSize;
+    PrefixBars &bars = *reinterpret_cast<PrefixBars *>(raws + (FP8 ? kRaws * kRawSize : 0));
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&bars.full[i], FP8 ? kConverters : 1);
+            mbar_init(&bars.empty[i], 2);
+        }
+        for (int i = 0; i < kRaws; ++i) {
+            mbar_init(&bars.raw_full[i], 1);
+            mbar_init(&bars.raw_empty[i], kConverters);
+        }
+        for (int s = 0; s < 2; ++s) {
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(&bars.s_full[s][h], 1);
+                mbar_init(&bars.p_full[s][h], 4);
+            }
+            mbar_init(&bars.q_full[s], 4);
+            mbar_init(&bars.o_step[s], 1);
+            mbar_init(&bars.o_full[s], 1);
+            mbar_init(&bars.drained[s], 1);
+        }
+        bars.stop = 0;
+        fence_barrier_init();
+    }
+    if (warp == kIssuer)
+        tc::alloc<kCols>(&bars.tmem);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = bars.tmem;
+    grid_dependency_wait();
+    allow_dependent_launch();  // the sequences' own pages need nothing of this kernel until they merge
+    if (warp == kLoader)
+        prefix_loader<FP8>(&tmap, a, FP8 ? raws : stages, bars);
+    else if (FP8 && warp >= kConverter)
+        prefix_converter(a, raws, stages, bars);
+    else if (warp >= kIssuer)
+        prefix_issuer<kStages>(a, stages, bars, tmem, warp - kIssuer);
+    else
+        prefix_softmax<FP8>(a, bars, tmem, warp >> 2);
+    __syncthreads();
+    if (threadIdx.x == 0 && bars.stop && a.err)
+        atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+    if (warp == kIssuer)
+        tc::dealloc<kCols>(tmem);
+}
+
+constexpr int kSms = 152;
+
+// Pages per prefix chunk where the caller leaves it to the library: the chunk count whose waves
+// of work items (two row tiles each, one CTA per SM) take the fewest key tiles in all, an item
+// costing about two key tiles besides its own and each chunk a little merging.
+int default_prefix_chunk(int B, int groups, int max_prefix)
+{
+    const int tiles = (max_prefix + kTilePages - 1) / kTilePages;
+    const int64_t row_tiles = (B + kTileSeqs - 1) / kTileSeqs + (groups - 1);
+    int best = tiles;
+    double best_cost = 1e30;
+    for (int chunks = 1; chunks <= tiles && chunks <= 64; ++chunks) {
+        const int per = (tiles + chunks - 1) / chunks;
+        const int64_t items = (kHkv * row_tiles * ((tiles + per - 1) / per) + 1) / 2;
+        const double cost = (double)((items + kSms - 1) / kSms) * (per + 2) + 0.1 * chunks;
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = per;
+        }
+    }
+    return best * kTilePages;
+}
+
+// What a call's host-side arguments settle.
+struct SharedPlan {
+    int own_ppc, prefix_chunk, prefix_slots, max_chunks;
+    int64_t max_items;
+    bool merge_apart;
+};
+
+SharedPlan shared_plan(int B, int max_blocks, int groups, int max_prefix, int ppc, int prefix_ppc)
+{
+    SharedPlan p;
+    p.own_ppc = ppc ? ppc : default_chunk(B, max_blocks);
+    p.prefix_chunk = kTilePages;
+    p.prefix_slots = 0;
+    p.max_items = 0;
+    if (max_prefix > 0) {
+        const int whole = (max_prefix + kTilePages - 1) / kTilePages * kTilePages;
+        p.prefix_chunk = prefix_ppc ? (int)std::min<int64_t>(whole, ((int64_t)prefix_ppc + kTilePages - 1) / kTilePages * kTilePages)
+                                    : default_prefix_chunk(B, groups, max_prefix);
+        p.prefix_slots = (max_prefix + p.prefix_chunk - 1) / p.prefix_chunk;
+        // sum over groups of ceil(n / 64) row-tile pairs, each in every chunk
+        p.max_items = (int64_t)kHkv * ((B + (int64_t)(2 * kTileSeqs - 1) * groups) / (2 * kTileSeqs)) * p.prefix_slots;
+    }
+    p.max_chunks = p.prefix_slots + (max_blocks + p.own_ppc - 1) / p.own_ppc;
+    p.merge_apart = p.max_items > 0 && B * kHkv > kSms;
+    return p;
+}
+
+template <bool FP8>
+int launch_prefix(const pkv_pool *pool, const PrefixArgs &a, int64_t max_items, cudaStream_t s, bool pdl)
+{
+    const CUtensorMap *tmap = pool_tensor_map(pool);
+    if (!tmap)
+        return PKV_ERR_CUDA;
+    constexpr int smem =
+        1024 + stages_of(FP8) * kStageSize + (FP8 ? kRaws * kRawSize : 0) + (int)sizeof(PrefixBars);
+    static PerDeviceOnce attr;
+    if (const int st = ensure_smem_attr(attr, prefix_kernel<FP8>, smem); st != PKV_OK)
+        return st;
+    const dim3 grid((unsigned)std::min<int64_t>(max_items, kSms));
+    return launch_kernel(prefix_kernel<FP8>, grid, dim3(prefix_threads(FP8)), smem, s, pdl, *tmap, a);
+}
+
+// The partials of one (sequence, KV head): the prefix's chunks, then its own.
+__global__ void __launch_bounds__(kThreads) merge_kernel(StepArgs a, Groups gr)
+{
+    const int g = blockIdx.x, b = blockIdx.y;
+    const int L = a.seq_lens[b];
+    const auto list = OwnPages<false>{gr}.list(b, L);
+    grid_dependency_wait();
+    allow_dependent_launch();
+    if (!length_ok(a, L) || !list.ok())
+        return;  // zeros, written by the units' kernel
+    const int n = list.first_slot() + max(1, (list.count() + a.pages_per_chunk - 1) / a.pages_per_chunk);
+    const int h = g * kGroup + (threadIdx.x >> 5), dp = threadIdx.x & 31;
+    const size_t base = ((size_t)b * kHq + h) * a.max_chunks;
+    float Mx, ls, r0, r1;
+    merge_partials(a.part_ml + base, reinterpret_cast<const float2 *>(a.part_o + base * kD) + dp, n, Mx, ls, r0, r1);
+    reinterpret_cast<uint32_t *>(a.out + ((size_t)b * kHq + h) * kD)[dp] = finish_pair(r0, r1, ls);
+}
 
 bool shared_args_ok(int B, int max_blocks, int groups, int max_prefix_pages, int pages_per_chunk,
                     int prefix_pages_per_chunk)
@@ -56,8 +793,9 @@ extern "C" size_t pkv_decode_shared_workspace_bytes(int B, int max_blocks, int g
     using namespace pkv;
     if (!shared_args_ok(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk))
         return 0;
-    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks);
-    return workspace_layout(B, (max_blocks + ppc - 1) / ppc).total();
+    return workspace_layout(
+               B, shared_plan(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk).max_chunks)
+        .total();
 }
 
 extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
@@ -80,8 +818,10 @@ extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const 
     if (workspace_bytes < pkv_decode_shared_workspace_bytes(B, max_blocks, groups, max_prefix_pages, pages_per_chunk,
                                                             prefix_pages_per_chunk))
         return PKV_ERR_WORKSPACE_TOO_SMALL;
-    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks);
-    const SharedPages sel = {group_starts_dev, prefix_pages_dev, groups, max_prefix_pages};
+    const SharedPlan plan =
+        shared_plan(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk);
+    cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    const Groups gr = {group_starts_dev, prefix_pages_dev, groups, max_prefix_pages, plan.prefix_chunk, B};
     StepArgs a = {};
     a.q = const_cast<uint16_t *>(q);
     a.bt = bt_dev;
@@ -90,6 +830,38 @@ extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const 
     a.scale_log2 = scale * kLog2e;
     a.out = out;
     a.err = dev_err_flag;
-    return launch_fused<false>(pool, a, sel, B, max_blocks, max_blocks, 0, ppc, workspace,
-                               static_cast<cudaStream_t>(cuda_stream), options);
+    // both launches check the options; the first is the one that must not run if they are refused
+    if (const int st = check_options<OwnPages<true>>(pool, B, max_blocks, plan.own_ppc, options); st != PKV_OK)
+        return st;
+    const bool pdl = take_pdl_permission(pool, !(options & PKV_STEP_NO_PDL));
+    if (plan.max_items > 0) {
+        const WorkspaceLayout ws = workspace_layout(B, plan.max_chunks);
+        PrefixArgs p;
+        p.gr = gr;
+        p.num_pages = pool->num_pages;
+        p.q = q;
+        p.bt = bt_dev;
+        p.max_blocks = max_blocks;
+        p.scale_log2 = a.scale_log2;
+        p.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + ws.ml_offset());
+        p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.o_offset());
+        p.max_chunks = plan.max_chunks;
+        p.err = dev_err_flag;
+        if (const int st = pool->kv_format == PKV_KV_FP8 ? launch_prefix<true>(pool, p, plan.max_items, s, pdl)
+                                                         : launch_prefix<false>(pool, p, plan.max_items, s, pdl);
+            st != PKV_OK)
+            return st;
+    }
+    // The second launch begins beside the first.  A few units wait for it and merge; many would
+    // keep each other from starting, so they only publish, and a third launch merges.
+    // (With no first launch the second waits for what came before the call.)
+    const int first = plan.max_items > 0 ? options : options | PKV_STEP_NO_PDL;
+    if (!plan.merge_apart)
+        return launch_fused<false>(pool, a, OwnPages<true>{gr}, B, max_blocks, max_blocks, plan.prefix_slots, plan.own_ppc,
+                                   workspace, s, first, true);
+    if (const int st = launch_fused<false>(pool, a, OwnPages<false>{gr}, B, max_blocks, max_blocks, plan.prefix_slots,
+                                           plan.own_ppc, workspace, s, first, true);
+        st != PKV_OK)
+        return st;
+    return launch_kernel(merge_kernel, dim3(kHkv, B), dim3(kThreads), 0, s, !(options & PKV_STEP_NO_PDL), a, gr);
 }

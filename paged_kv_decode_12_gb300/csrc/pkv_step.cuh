@@ -36,11 +36,16 @@ using namespace dev;
 //   kSortable    the list depends on L alone, so that units can be dispatched by size
 //   kLateWait    the dependency wait comes before the partials are published instead of
 //                before the query rows are read
+//   kPublish     units only write their partials, for another kernel to merge; the grid ends
+//                after the kernel that it follows, because its first CTA waits for it
+//   kLoops       a CTA goes on to chunk c + gridDim.z: the grid need not have a CTA for every
+//                chunk of the table's width, which with wide tables and short sequences would
+//                be mostly CTAs with nothing to do
 // `emit(b, g)` makes what takes the units' scores, `skipped(b, g, j0, jn)` is told of a
 // unit that a bad page id keeps from being computed, `norm(b, h, M, l)` takes the
 // finished softmax statistics of one head.
 struct AllPages {
-    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false;
+    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
     __device__ __forceinline__ WholeSequence list(int, int L) const { return {L}; }
     __device__ __forceinline__ EmitNothing emit(int, int) const { return {}; }
     __device__ __forceinline__ void skipped(int, int, int, int) const {}
@@ -64,7 +69,7 @@ struct StepArgs {
     float2 *part_ml;         // [B][32][max_chunks]
     float *part_o;           // [B][32][max_chunks][64]
     int max_chunks;          // partials per (sequence, head)
-    int unit_chunks;         // chunks per (sequence, KV head) in the grid
+    int unit_chunks;         // CTAs per (sequence, KV head) in the grid
     uint16_t *out;           // [B][32][64]
     int32_t *err;
     int sorted;              // units dispatched largest first (PKV_STEP_SORTED)
@@ -328,58 +333,12 @@ __device__ __forceinline__ void write_zero_unit(const StepArgs &a, int b, int g)
 // Chunk counts up to which the merging unit holds every partial in registers.
 constexpr int kMergeRegs = 8;
 
-// Unit epilogue, all threads: combine the warps' states through `state`, then
-// write the output (single partial) or publish the chunk partial and take a ticket;
-// the unit drawing the last ticket merges every chunk of (b, g) in chunk order, behind
-// the `first` partials that another kernel wrote, writes the output (and, WRITE_Q, the
-// rotated query rows), and resets the counter.
-template <bool WRITE_Q, class Sel, class Warp>
-__device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, Warp &w, float *state, int *ticket,
-                                            const uint16_t *q_rot, int b, int g, int c, int nunits, int first)
+// The log-sum-exp merge, in chunk order, of a head's partials (ml_row, and o_col one dim pair).
+__device__ __forceinline__ void merge_partials(const float2 *ml_row, const float2 *o_col, int nchunks, float &Mx, float &ls,
+                                               float &r0, float &r1)
 {
-    const int nchunks = first + nunits;
-    const int tid = threadIdx.x, warp = tid >> 5;
-    __syncthreads();
-    w.store_state(state + warp * kStateFloats);
-    __syncthreads();
-    const int hl = tid >> 5, dp = tid & 31, h = g * kGroup + hl;
-    float M, lsum, o0, o1;
-    combine_warps(state, hl, dp, M, lsum, o0, o1);
-    uint32_t *out_row = reinterpret_cast<uint32_t *>(a.out + ((size_t)b * kHq + h) * kD);
-    uint32_t *q_row = reinterpret_cast<uint32_t *>(a.q + ((size_t)b * kHq + h) * kD);
-    const uint32_t q_word = reinterpret_cast<const uint32_t *>(q_rot + hl * kD)[dp];
-    if (nchunks == 1) {
-        out_row[dp] = finish_pair(o0, o1, lsum);
-        if (dp == 0)
-            sel.norm(b, h, M, lsum);
-        if (WRITE_Q)
-            q_row[dp] = q_word;
-        if (Sel::kLateWait) {
-            grid_dependency_wait();  // this grid ends after the kernel it follows
-            allow_dependent_launch();
-        }
-        return;
-    }
-    const size_t base = ((size_t)b * kHq + h) * a.max_chunks;
-    reinterpret_cast<float2 *>(a.part_o + (base + first + c) * kD)[dp] = make_float2(o0, o1);
-    if (dp == 0)
-        a.part_ml[base + first + c] = make_float2(M, lsum);
-    if (Sel::kLateWait) {
-        grid_dependency_wait();  // the other kernel's partials
-        allow_dependent_launch();
-    }
-    // publish: the CTA barrier orders every thread's partial stores before thread 0's
-    // release-acquire ticket; the acquire side plus the barrier orders the merging
-    // unit's loads after every other unit's partial stores
-    __syncthreads();
-    if (tid == 0)
-        *ticket = ticket_acq_rel(&a.counters[b * kHkv + g]);
-    __syncthreads();
-    if (*ticket != nunits - 1)
-        return;
-    float ls = 0.f, r0 = 0.f, r1 = 0.f, Mx = -INFINITY;
-    const float2 *ml_row = a.part_ml + base;
-    const float2 *o_col = reinterpret_cast<const float2 *>(a.part_o + base * kD) + dp;
+    ls = r0 = r1 = 0.f;
+    Mx = -INFINITY;
     if (nchunks <= kMergeRegs) {
         // every partial loaded before the first use: one memory round trip at the end of
         // the sequence's critical path; the arithmetic below is the general loop's
@@ -405,9 +364,11 @@ __device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, W
                 }
         }
     } else {
+#pragma unroll 4
         for (int cc = 0; cc < nchunks; ++cc)
             Mx = fmaxf(Mx, __ldcg(ml_row + cc).x);
         if (Mx != -INFINITY) {
+#pragma unroll 4
             for (int cc = 0; cc < nchunks; ++cc) {
                 const float2 ml = __ldcg(ml_row + cc);
                 const float f = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - Mx);
@@ -418,6 +379,61 @@ __device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, W
             }
         }
     }
+}
+
+// Unit epilogue, all threads: combine the warps' states through `state`, then
+// write the output (single partial) or publish the chunk partial and take a ticket;
+// the unit drawing the last ticket merges every chunk of (b, g) in chunk order, behind
+// the `first` partials that another kernel wrote, writes the output (and, WRITE_Q, the
+// rotated query rows), and resets the counter.
+template <bool WRITE_Q, class Sel, class Warp>
+__device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, Warp &w, float *state, int *ticket,
+                                            const uint16_t *q_rot, int b, int g, int c, int nunits, int first)
+{
+    const int nchunks = first + nunits;
+    const int tid = threadIdx.x, warp = tid >> 5;
+    __syncthreads();
+    w.store_state(state + warp * kStateFloats);
+    __syncthreads();
+    const int hl = tid >> 5, dp = tid & 31, h = g * kGroup + hl;
+    float M, lsum, o0, o1;
+    combine_warps(state, hl, dp, M, lsum, o0, o1);
+    uint32_t *out_row = reinterpret_cast<uint32_t *>(a.out + ((size_t)b * kHq + h) * kD);
+    uint32_t *q_row = reinterpret_cast<uint32_t *>(a.q + ((size_t)b * kHq + h) * kD);
+    const uint32_t q_word = reinterpret_cast<const uint32_t *>(q_rot + hl * kD)[dp];
+    if (!Sel::kPublish && nchunks == 1) {
+        out_row[dp] = finish_pair(o0, o1, lsum);
+        if (dp == 0)
+            sel.norm(b, h, M, lsum);
+        if (WRITE_Q)
+            q_row[dp] = q_word;
+        if (Sel::kLateWait) {
+            grid_dependency_wait();  // this grid ends after the kernel it follows
+            allow_dependent_launch();
+        }
+        return;
+    }
+    const size_t base = ((size_t)b * kHq + h) * a.max_chunks;
+    reinterpret_cast<float2 *>(a.part_o + (base + first + c) * kD)[dp] = make_float2(o0, o1);
+    if (dp == 0)
+        a.part_ml[base + first + c] = make_float2(M, lsum);
+    if (Sel::kPublish)
+        return;
+    if (Sel::kLateWait) {
+        grid_dependency_wait();  // the other kernel's partials
+        allow_dependent_launch();
+    }
+    // publish: the CTA barrier orders every thread's partial stores before thread 0's
+    // release-acquire ticket; the acquire side plus the barrier orders the merging
+    // unit's loads after every other unit's partial stores
+    __syncthreads();
+    if (tid == 0)
+        *ticket = ticket_acq_rel(&a.counters[b * kHkv + g]);
+    __syncthreads();
+    if (*ticket != nunits - 1)
+        return;
+    float ls, r0, r1, Mx;
+    merge_partials(a.part_ml + base, reinterpret_cast<const float2 *>(a.part_o + base * kD) + dp, nchunks, Mx, ls, r0, r1);
     out_row[dp] = finish_pair(r0, r1, ls);
     if (dp == 0)
         sel.norm(b, h, Mx, ls);
@@ -490,60 +506,38 @@ struct Timeline {  // compiled out
 
 constexpr int kGridExtraBytes = kGroup * kD * 2 + 2 * kD * 2 + 16;  // rotated q rows, new K/V rows, ticket
 
-template <class Warp, int STAGES, bool APPEND, class Sel>
-__global__ void __launch_bounds__(kThreads)
-    decode_step_kernel(const __grid_constant__ CUtensorMap tmap, StepArgs a, Sel sel)
+// All threads, between two units of a CTA: the first one's shared memory is read and its barriers
+// (all of whose phases are complete) are free to be initialised again; what threads wrote there
+// comes before the next copies.
+__device__ __forceinline__ void rearm_barriers(uint64_t *my_bars, int stages, int lane)
 {
-    extern __shared__ uint8_t smem_raw[];
-    SmemLayout<STAGES> sm(smem_raw);
+    fence_proxy_async_smem();
+    __syncthreads();
+    if (lane == 0)
+        for (int s = 0; s < stages; ++s)
+            mbar_inval(&my_bars[s]);
+    __syncwarp();
+}
+
+// One work unit (all threads): chunk c of the nchunks of (sequence b, KV head g).  Lane k of a warp
+// holds in `my_page` the warp's k-th table entry if the list is the identity and `prefetched`.
+template <class Warp, int STAGES, bool APPEND, class Sel, class List>
+__device__ __forceinline__ void decode_unit(const CUtensorMap &tmap, const StepArgs &a, const Sel &sel, const List &list,
+                                            SmemLayout<STAGES> &sm, int b, int g, int c, int nchunks, int L, int my_page,
+                                            bool prefetched, Timeline &tl)
+{
     uint16_t *q_rot = reinterpret_cast<uint16_t *>(sm.extra);  // [4][64] query rows (rotated when APPEND)
     uint16_t *new_kv = q_rot + kGroup * kD;                     // [2][64] rotated key row, value row
     int *ticket = reinterpret_cast<int *>(new_kv + 2 * kD);
-    Timeline tl;
-    tl.begin();
-
-    int g = blockIdx.x, b = blockIdx.y, c = blockIdx.z;
-    if constexpr (Sel::kSortable) {
-        if (a.sorted) {
-            const int lin = blockIdx.x + kHkv * (blockIdx.y + gridDim.y * blockIdx.z);
-            if (!sorted_unit(a, sel, gridDim.y, lin, reinterpret_cast<int *>(sm.scratch), b, g, c)) {
-                tl.none();
-                return;
-            }
-        }
-    }
-    tl.stamp(1);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int j0 = c * a.pages_per_chunk;
-    // the length and this chunk's table entries are fetched together (one round trip):
-    // entries inside the table row are always readable, whatever the length turns out to be
-    const int jcap = min(a.max_blocks - j0, a.pages_per_chunk);
-    const int ncap = warp < jcap ? (jcap - warp + kWarps - 1) / kWarps : 0;
-    int my_page = 0;
-    if (Sel::kIdentity && lane < ncap)
-        my_page = a.bt[(size_t)b * a.max_blocks + j0 + warp + lane * kWarps];
-    const int L = a.seq_lens[b];
-    const auto list = sel.list(b, L);
-    if (!length_ok(a, L) || !list.ok()) {
-        if (c == 0) {
-            grid_dependency_wait();
-            write_zero_unit(a, b, g);
-        }
-        tl.none();
-        return;
-    }
-    const int npages = (L + kPage - 1) / kPage;
-    const int nlist = list.count();
-    const int nchunks = Sel::kIdentity ? (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk
-                                       : max(1, (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk);
-    if (c >= nchunks) {
-        tl.none();
-        return;
-    }
+    int tid = threadIdx.x;
+    if (Sel::kLoops)  // keeps what depends on it from being held in registers across the loop's units
+        asm volatile("" : "+r"(tid));
+    const int warp = tid >> 5, lane = tid & 31;
+    const int npages = (L + kPage - 1) / kPage, j0 = c * a.pages_per_chunk, nlist = list.count();
     const bool last_chunk = c == nchunks - 1;
     const int jn = min(nlist - j0, a.pages_per_chunk);
     const int nmine = warp < jn ? (jn - warp + kWarps - 1) / kWarps : 0;
-    if (!Sel::kIdentity && lane < nmine) {
+    if (!prefetched && lane < nmine) {
         const int j = list.logical(j0 + warp + lane * kWarps);
         my_page = a.bt[(size_t)list.row(b, j) * a.max_blocks + j];
     }
@@ -555,12 +549,13 @@ __global__ void __launch_bounds__(kThreads)
     const uint64_t policy = l2_evict_first_policy();
     const int nfirst = min(STAGES, nmine);
     const int nearly = any_bad ? 0 : copies_before_wait(list, L, j0, warp, nmine, STAGES);
-    if (!any_bad) {
+    if (Sel::kLoops || !any_bad)
         init_warp_barriers<STAGES>(my_bars, lane);
+    if (!any_bad) {
         issue_copies<STAGES>(&tmap, my_stages, my_bars, my_page, 0, nearly, g, lane, policy);
     }
 
-    if (!Sel::kLateWait)
+    if (!Sel::kLateWait && !Sel::kPublish)
         grid_dependency_wait();  // q, k_new, v_new, recently written pages and every output follow it
     tl.stamp(2);
     if (!any_bad)  // the pages holding positions L - 2 and L - 1
@@ -591,12 +586,89 @@ __global__ void __launch_bounds__(kThreads)
             atomicOr(a.err, PKV_DEVERR_TIMEOUT);
     }
     tl.stamp(3);
-    if (!Sel::kLateWait)
+    if (!Sel::kLateWait && !Sel::kPublish)
         allow_dependent_launch();
     // the stages are free now: they hold the combine area
     finish_unit<APPEND>(a, sel, w, reinterpret_cast<float *>(sm.stages), ticket, q_rot, b, g, c, nchunks,
                         list.first_slot());
     tl.end(b, c, jn);
+}
+
+// CTAs per SM the register budget of a looping kernel is set for: as many as its ring's shared
+// memory lets in (the others have none).
+constexpr int loop_ctas_per_sm(bool loops, int stages) { return !loops ? 0 : stages == 2 ? 6 : stages == 3 ? 4 : 3; }
+
+// The end of a publishing kernel's CTA: the first one waits for the kernel before.
+template <class Sel>
+__device__ __forceinline__ void publish_end()
+{
+    if constexpr (Sel::kPublish) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0)
+            grid_dependency_wait();
+        allow_dependent_launch();
+    }
+}
+
+template <class Warp, int STAGES, bool APPEND, class Sel>
+__device__ __forceinline__ void decode_cta(const CUtensorMap &tmap, const StepArgs &a, const Sel &sel, uint8_t *smem_raw)
+{
+    SmemLayout<STAGES> sm(smem_raw);
+    Timeline tl;
+    tl.begin();
+
+    int g = blockIdx.x, b = blockIdx.y, c = blockIdx.z;
+    if constexpr (Sel::kSortable) {
+        if (a.sorted) {
+            const int lin = blockIdx.x + kHkv * (blockIdx.y + gridDim.y * blockIdx.z);
+            if (!sorted_unit(a, sel, gridDim.y, lin, reinterpret_cast<int *>(sm.scratch), b, g, c)) {
+                tl.none();
+                return;
+            }
+        }
+    }
+    tl.stamp(1);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int j0 = c * a.pages_per_chunk;
+    // the length and this chunk's table entries are fetched together (one round trip):
+    // entries inside the table row are always readable, whatever the length turns out to be
+    const int jcap = min(a.max_blocks - j0, a.pages_per_chunk);
+    const int ncap = warp < jcap ? (jcap - warp + kWarps - 1) / kWarps : 0;
+    int my_page = 0;
+    if (Sel::kIdentity && lane < ncap)
+        my_page = a.bt[(size_t)b * a.max_blocks + j0 + warp + lane * kWarps];
+    const int L = a.seq_lens[b];
+    const auto list = sel.list(b, L);
+    if (!length_ok(a, L) || !list.ok()) {
+        if (c == 0) {
+            if (!Sel::kPublish)
+                grid_dependency_wait();
+            write_zero_unit(a, b, g);
+        }
+        tl.none();
+        return;
+    }
+    const int nlist = list.count();
+    const int nchunks = Sel::kIdentity ? (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk
+                                       : max(1, (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk);
+    if (c >= nchunks) {
+        tl.none();
+        return;
+    }
+    for (bool first = true;; first = false) {
+        decode_unit<Warp, STAGES, APPEND>(tmap, a, sel, list, sm, b, g, c, nchunks, L, my_page, Sel::kIdentity && first, tl);
+        if (!Sel::kLoops || (c += gridDim.z) >= nchunks)
+            break;
+        rearm_barriers(sm.bars + warp * STAGES, STAGES, lane);
+    }
+}
+
+template <class Warp, int STAGES, bool APPEND, class Sel>
+__global__ void __launch_bounds__(kThreads, loop_ctas_per_sm(Sel::kLoops, STAGES))
+    decode_step_kernel(const __grid_constant__ CUtensorMap tmap, StepArgs a, Sel sel)
+{
+    extern __shared__ uint8_t smem_raw[];
+    decode_cta<Warp, STAGES, APPEND>(tmap, a, sel, smem_raw);
+    publish_end<Sel>();
 }
 
 // ------------------------------------------------------------------ FP8 pages, grid schedule
@@ -657,49 +729,24 @@ __device__ __forceinline__ void put_new_token_fp8(uint8_t *unit, int slot, const
 // CTAs per SM the register budget is set for.  The 3-stage ring takes 27.5 KB of shared
 // memory per CTA, so seven CTAs fit (at most 72 registers, a few spilled) and keep 7 x 4 x 3
 // units of 2176 B in flight per SM; the other rings keep six (80 registers, none spilled).
+// (The looping kernels hold more across their units and keep one CTA less.)
 constexpr int fp8_ctas_per_sm(int stages) { return stages == 3 ? 7 : 6; }
 
-template <int STAGES, bool APPEND, class Sel>
-__global__ void __launch_bounds__(kThreads, fp8_ctas_per_sm(STAGES))
-    decode_step_fp8_kernel(const __grid_constant__ CUtensorMap tmap, StepArgs a, Sel sel)
+// decode_unit over FP8 pages.
+template <int STAGES, bool APPEND, class Sel, class List>
+__device__ __forceinline__ void decode_unit_fp8(const CUtensorMap &tmap, const StepArgs &a, const Sel &sel,
+                                                const List &list, Fp8StepSmem<STAGES> &sm, int b, int g, int c, int nchunks,
+                                                int L, int my_page, bool prefetched)
 {
-    extern __shared__ uint8_t smem_raw[];
-    Fp8StepSmem<STAGES> sm(smem_raw);
-
-    int g = blockIdx.x, b = blockIdx.y, c = blockIdx.z;
-    if constexpr (Sel::kSortable) {
-        if (a.sorted) {
-            const int lin = blockIdx.x + kHkv * (blockIdx.y + gridDim.y * blockIdx.z);
-            if (!sorted_unit(a, sel, gridDim.y, lin, sm.sort_scratch, b, g, c))
-                return;
-        }
-    }
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int j0 = c * a.pages_per_chunk;
-    const int jcap = min(a.max_blocks - j0, a.pages_per_chunk);
-    const int ncap = warp < jcap ? (jcap - warp + kWarps - 1) / kWarps : 0;
-    int my_page = 0;
-    if (Sel::kIdentity && lane < ncap)
-        my_page = a.bt[(size_t)b * a.max_blocks + j0 + warp + lane * kWarps];
-    const int L = a.seq_lens[b];
-    const auto list = sel.list(b, L);
-    if (!length_ok(a, L) || !list.ok()) {
-        if (c == 0) {
-            grid_dependency_wait();
-            write_zero_unit(a, b, g);
-        }
-        return;
-    }
-    const int npages = (L + kPage - 1) / kPage;
-    const int nlist = list.count();
-    const int nchunks = Sel::kIdentity ? (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk
-                                       : max(1, (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk);
-    if (c >= nchunks)
-        return;
+    int tid = threadIdx.x;
+    if (Sel::kLoops)  // keeps what depends on it from being held in registers across the loop's units
+        asm volatile("" : "+r"(tid));
+    const int warp = tid >> 5, lane = tid & 31;
+    const int npages = (L + kPage - 1) / kPage, j0 = c * a.pages_per_chunk, nlist = list.count();
     const bool last_chunk = c == nchunks - 1;
     const int jn = min(nlist - j0, a.pages_per_chunk);
     const int nmine = warp < jn ? (jn - warp + kWarps - 1) / kWarps : 0;
-    if (!Sel::kIdentity && lane < nmine) {
+    if (!prefetched && lane < nmine) {
         const int j = list.logical(j0 + warp + lane * kWarps);
         my_page = a.bt[(size_t)list.row(b, j) * a.max_blocks + j];
     }
@@ -718,12 +765,12 @@ __global__ void __launch_bounds__(kThreads, fp8_ctas_per_sm(STAGES))
                 fp8::fp8_issue(&tmap, my_stages + k * kFp8Unit, &my_bars[k], g, pk, policy);
         }
     };
-    if (!any_bad) {
+    if (Sel::kLoops || !any_bad)
         init_warp_barriers<STAGES>(my_bars, lane);
+    if (!any_bad)
         issue(0, nearly);
-    }
 
-    if (!Sel::kLateWait)
+    if (!Sel::kLateWait && !Sel::kPublish)
         grid_dependency_wait();  // q, k_new, v_new, recently written pages and every output follow it
     if (!any_bad)  // the pages holding positions L - 2 and L - 1
         issue(nearly, nfirst);
@@ -795,11 +842,63 @@ __global__ void __launch_bounds__(kThreads, fp8_ctas_per_sm(STAGES))
                 atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         }
     }
-    if (!Sel::kLateWait)
+    if (!Sel::kLateWait && !Sel::kPublish)
         allow_dependent_launch();
     // the stages are free now: they hold the combine area
     finish_unit<APPEND>(a, sel, w, reinterpret_cast<float *>(sm.stages), sm.ticket, sm.q_rot, b, g, c, nchunks,
                         list.first_slot());
+}
+
+template <int STAGES, bool APPEND, class Sel>
+__device__ __forceinline__ void decode_cta_fp8(const CUtensorMap &tmap, const StepArgs &a, const Sel &sel, uint8_t *smem_raw)
+{
+    Fp8StepSmem<STAGES> sm(smem_raw);
+
+    int g = blockIdx.x, b = blockIdx.y, c = blockIdx.z;
+    if constexpr (Sel::kSortable) {
+        if (a.sorted) {
+            const int lin = blockIdx.x + kHkv * (blockIdx.y + gridDim.y * blockIdx.z);
+            if (!sorted_unit(a, sel, gridDim.y, lin, sm.sort_scratch, b, g, c))
+                return;
+        }
+    }
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int j0 = c * a.pages_per_chunk;
+    const int jcap = min(a.max_blocks - j0, a.pages_per_chunk);
+    const int ncap = warp < jcap ? (jcap - warp + kWarps - 1) / kWarps : 0;
+    int my_page = 0;
+    if (Sel::kIdentity && lane < ncap)
+        my_page = a.bt[(size_t)b * a.max_blocks + j0 + warp + lane * kWarps];
+    const int L = a.seq_lens[b];
+    const auto list = sel.list(b, L);
+    if (!length_ok(a, L) || !list.ok()) {
+        if (c == 0) {
+            if (!Sel::kPublish)
+                grid_dependency_wait();
+            write_zero_unit(a, b, g);
+        }
+        return;
+    }
+    const int nlist = list.count();
+    const int nchunks = Sel::kIdentity ? (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk
+                                       : max(1, (nlist + a.pages_per_chunk - 1) / a.pages_per_chunk);
+    if (c >= nchunks)
+        return;
+    for (bool first = true;; first = false) {
+        decode_unit_fp8<STAGES, APPEND>(tmap, a, sel, list, sm, b, g, c, nchunks, L, my_page, Sel::kIdentity && first);
+        if (!Sel::kLoops || (c += gridDim.z) >= nchunks)
+            break;
+        rearm_barriers(sm.bars + warp * STAGES, STAGES, lane);
+    }
+}
+
+template <int STAGES, bool APPEND, class Sel>
+__global__ void __launch_bounds__(kThreads, fp8_ctas_per_sm(STAGES) - (Sel::kLoops ? 1 : 0))
+    decode_step_fp8_kernel(const __grid_constant__ CUtensorMap tmap, StepArgs a, Sel sel)
+{
+    extern __shared__ uint8_t smem_raw[];
+    decode_cta_fp8<STAGES, APPEND>(tmap, a, sel, smem_raw);
+    publish_end<Sel>();
 }
 
 // ------------------------------------------------------------------ launch
@@ -883,13 +982,11 @@ int launch_grid_depth(const CUtensorMap *tmap, const StepArgs &a, const Sel &sel
 constexpr int kGridOptions = 0xff | PKV_STEP_NO_PDL | PKV_STEP_GRID | PKV_STEP_RING_MASK | PKV_STEP_SORTED |
                              PKV_STEP_TEST_EXPIRE_WAIT;
 
-// Validates the options, fills the launch-dependent fields of `a` and launches the
-// kernel for the pool's format.  `max_blocks` is the table's width, `list_pages` the most
-// entries a list of the selection has, `first_slots` the most partials that another
-// kernel puts before a sequence's own.
-template <bool APPEND, class Sel>
-int launch_fused(const pkv_pool *pool, StepArgs &a, const Sel &sel, int B, int max_blocks, int list_pages,
-                 int first_slots, int pages_per_chunk, void *workspace, cudaStream_t s, int options, bool pdl_chain = false)
+constexpr int kLoopCtas = 152 * 16;
+
+// The options of a call on `pool` whose lists have at most `list_pages` entries.
+template <class Sel>
+int check_options(const pkv_pool *pool, int B, int list_pages, int pages_per_chunk, int options)
 {
     const int variant = options & 0xff;
     if (variant < PKV_DECODE_DEFAULT || variant > PKV_DECODE_MMA || (options & ~kGridOptions))
@@ -903,10 +1000,28 @@ int launch_fused(const pkv_pool *pool, StepArgs &a, const Sel &sel, int B, int m
         return PKV_ERR_UNSUPPORTED;  // FP8 pages and selections of pages: the MMA policy only
     if ((options & PKV_STEP_SORTED) && !Sel::kSortable)
         return PKV_ERR_UNSUPPORTED;
-    a.unit_chunks = (list_pages + pages_per_chunk - 1) / pages_per_chunk;
-    if (a.unit_chunks > 65535)  // the chunk index is gridDim.z
+    if ((list_pages + pages_per_chunk - 1) / pages_per_chunk > 65535)  // the chunk index is gridDim.z
         return PKV_ERR_INVALID_ARG;
-    const int max_chunks = first_slots + a.unit_chunks;
+    return PKV_OK;
+}
+
+// Validates the options, fills the launch-dependent fields of `a` and launches the
+// kernel for the pool's format.  `max_blocks` is the table's width, `list_pages` the most
+// entries a list of the selection has, `first_slots` the most partials that another
+// kernel puts before a sequence's own.  follows: the kernel just before on the stream is
+// the call's own and has waited for everything before it.
+template <bool APPEND, class Sel>
+int launch_fused(const pkv_pool *pool, StepArgs &a, const Sel &sel, int B, int max_blocks, int list_pages,
+                 int first_slots, int pages_per_chunk, void *workspace, cudaStream_t s, int options, bool follows = false)
+{
+    if (const int st = check_options<Sel>(pool, B, list_pages, pages_per_chunk, options); st != PKV_OK)
+        return st;
+    const int variant = options & 0xff, ring = (options & PKV_STEP_RING_MASK) >> 12;
+    const int unit_chunks = (list_pages + pages_per_chunk - 1) / pages_per_chunk;
+    const int max_chunks = first_slots + unit_chunks;
+    a.unit_chunks = unit_chunks;
+    if (Sel::kLoops)  // as many CTAs as fill the GPU about twice
+        a.unit_chunks = (int)std::min<int64_t>(unit_chunks, std::max<int64_t>(1, kLoopCtas / ((int64_t)B * kHkv)));
     const CUtensorMap *tmap = pool_tensor_map(pool);
     if (!tmap)
         return PKV_ERR_CUDA;
@@ -922,8 +1037,8 @@ int launch_fused(const pkv_pool *pool, StepArgs &a, const Sel &sel, int B, int m
     a.max_chunks = max_chunks;
     a.sorted = (options & PKV_STEP_SORTED) ? 1 : 0;
     a.expire_seq = (options & PKV_STEP_TEST_EXPIRE_WAIT) ? 0 : -1;
-    // (pdl_chain: the kernel just before is the call's own and has waited for everything else)
-    const bool pdl = pdl_chain ? !(options & PKV_STEP_NO_PDL) : take_pdl_permission(pool, !(options & PKV_STEP_NO_PDL));
+    const bool wanted = !(options & PKV_STEP_NO_PDL);
+    const bool pdl = follows ? wanted : take_pdl_permission(pool, wanted);
     const int depth = ring ? ring : default_ring(pages_per_chunk);
     if (pool->kv_format == PKV_KV_FP8)
         return launch_fp8_depth<APPEND>(tmap, a, sel, B, s, pdl, depth);

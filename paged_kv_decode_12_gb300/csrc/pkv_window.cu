@@ -17,7 +17,7 @@ namespace pkv {
 namespace {
 
 struct WindowPages {
-    static constexpr bool kIdentity = false, kSortable = true, kLateWait = false;
+    static constexpr bool kIdentity = false, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
     int window, sinks;
 
     struct List {

@@ -96,14 +96,16 @@ def weights(q, K):
     return e / e.sum(-1, keepdims=True), s
 
 
-def attend(q, K, V, kv):
+def attend(q, K, V, kv, rounding=None):
     """(output [32][64], what the kernels may be off by, weights, what those may be off by).
 
     The output is rounded once to BF16 (2^-8 relative).  The weights are rounded once for the
     second product: to BF16 (2^-8) or, on FP8 pages, to FP16 (2^-11) with a step of 2^-24 where
     they are small, in units of the largest V scale.  The scores are FP32 sums of 64 products
     (2^-18 of the products' absolute sum covers any order and a truncating adder); on FP8 pages a
-    query entry below 2^-10 of its row's largest is off by at most 2^-17 of that largest."""
+    query entry below 2^-10 of its row's largest is off by at most 2^-17 of that largest.
+    ``rounding``: the weights' rounding where a kernel has another than its pages' (a shared prefix
+    of FP8 pages: BF16)."""
     p, s = weights(q, K)
     Kr, Vr = np.repeat(K, GROUP, 0), np.repeat(V, GROUP, 0)
     ds = SCALE * 2.0 ** -18 * np.einsum("hd,hnd->hn", np.abs(q), np.abs(Kr))
@@ -112,7 +114,7 @@ def attend(q, K, V, kv):
     ds = ds + 2.0 ** -20 * (1 + np.abs(s))
     dp = p * 2 * np.max(ds, axis=-1, keepdims=True) + 2.0 ** -126
     out = np.einsum("hn,hnd->hd", p, Vr)
-    rounding = 2.0 ** -8 if kv == "bf16" else 2.0 ** -11
+    rounding = rounding or (2.0 ** -8 if kv == "bf16" else 2.0 ** -11)
     off = np.einsum("hn,hnd->hd", p * rounding + dp, np.abs(Vr))
     if kv == "fp8":
         off = off + 2.0 ** -24 * np.abs(Vr).max((1, 2))[:, None] * p.shape[1]

@@ -240,7 +240,7 @@ def test_shared(kv, case):
     outs = [run_shared(c, bt, lens, starts, prefix, q, *a)[0] for a in ((0, 0), (2, 8), (128, 16), (1, 10000))]
     for b, L in enumerate(lens):
         K, V = c.rows(view[b], range(int(L)))
-        want, off, _, _ = lh.attend(qf[b], K, V, kv)
+        want, off, _, _ = lh.attend(qf[b], K, V, kv, 2.0 ** -8)
         for o in outs:
             close(o[b], want, off, (b, L))
     c.close()
@@ -278,7 +278,7 @@ def test_shared_device_checks(kv):
         assert not out[b].any(), b
     for b in (0, 5):
         K, V = c.rows(view[b], range(int(lens[b])))
-        close(out[b], *lh.attend(qf[b], K, V, kv)[:2])
+        close(out[b], *lh.attend(qf[b], K, V, kv, 2.0 ** -8)[:2])
     # sequences that are in no group; starts that run outside the batch
     for bad in ([0, 2, 4, 5, 5], [1, 2, 4, 5, 6], [-3, 2, 4, 5, 6]):
         out, bits = run_shared(c, bt, lens, np.array(bad, np.int32), prefix, q, 128, 8, ok=False)
@@ -290,7 +290,7 @@ def test_shared_device_checks(kv):
     assert bits == pkv.PKV_DEVERR_PAGE_RANGE
     for b in (2, 3, 4):
         K, V = c.rows(view[b], range(int(lens[b])))
-        close(out[b], *lh.attend(qf[b], K, V, kv)[:2])
+        close(out[b], *lh.attend(qf[b], K, V, kv, 2.0 ** -8)[:2])
     c.close()
 
 
