@@ -125,22 +125,32 @@ def lib():
 # ---------------------------------------------------------------------------- marshalling
 
 def _ptr(x):
-    """Device/host pointer from a tensor, an int address or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return ctypes.c_void_p(x)
-    return ctypes.c_void_p(x.data_ptr())
+    """Device/host pointer (an address, as the c_void_p arguments take it) from a tensor, an int
+    address or None."""
+    if x is None or isinstance(x, int):
+        return x
+    return x.data_ptr()
+
+
+_torch = None
 
 
 def _stream(stream):
     if stream is None:
-        import torch
+        global _torch
+        if _torch is None:
+            import torch
 
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            _torch = torch
+        # the raw handle of torch.cuda.current_stream(), without making its Stream object where
+        # torch can (a few microseconds of every call)
+        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None or not _torch.cuda.is_initialized():
+            return _torch.cuda.current_stream().cuda_stream
+        return raw(_torch._C._cuda_getDevice())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check(status: int, what: str) -> int:
