@@ -108,7 +108,7 @@ extern "C" size_t pkv_decode_scored_workspace_bytes(int B, int max_blocks, int p
     using namespace pkv;
     if (!scored_args_ok(B, max_blocks, pages_per_chunk))
         return 0;
-    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks);
+    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks, 2);
     return scored_workspace(B, max_blocks, (max_blocks + ppc - 1) / ppc).total();
 }
 
@@ -129,7 +129,7 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
         return PKV_ERR_INVALID_ARG;
     if (workspace_bytes < pkv_decode_scored_workspace_bytes(B, max_blocks, pages_per_chunk))
         return PKV_ERR_WORKSPACE_TOO_SMALL;
-    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks);
+    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks, 2);
     const ScoredWorkspace w = scored_workspace(B, max_blocks, (max_blocks + ppc - 1) / ppc);
     char *base = static_cast<char *>(workspace);
     ScoredPages sel;
@@ -145,6 +145,11 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     a.out = out;
     a.err = dev_err_flag;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+    // Largest units first where there are several waves of them and the library chooses: 64
+    // sequences up to 16384 tokens (FP8) 85 us instead of 93; with up to 2048 tokens, two waves,
+    // the order costs more than it gives (18.8 us instead of 17.2).
+    if (pages_per_chunk == 0 && B <= kMaxSortedBatch && (int64_t)B * kHkv * ((max_blocks + ppc - 1) / ppc) > 4 * 152 * 6)
+        options |= PKV_STEP_SORTED;
     if (const int st = launch_fused<false>(pool, a, sel, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
         st != PKV_OK)
         return st;

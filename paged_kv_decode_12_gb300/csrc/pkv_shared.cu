@@ -726,7 +726,7 @@ struct SharedPlan {
 SharedPlan shared_plan(int B, int max_blocks, int groups, int max_prefix, int ppc, int prefix_ppc)
 {
     SharedPlan p;
-    p.own_ppc = ppc ? ppc : default_chunk(B, max_blocks);
+    p.own_ppc = ppc ? ppc : default_chunk(B, max_blocks, 2);
     p.prefix_chunk = kTilePages;
     p.prefix_slots = 0;
     p.max_items = 0;

@@ -908,12 +908,18 @@ __global__ void __launch_bounds__(kThreads, fp8_ctas_per_sm(STAGES) - (Sel::kLoo
 // for 128-page chunks and for 16- to 32-page chunks of ragged batches respectively.
 int default_ring(int pages_per_chunk) { return pages_per_chunk >= 64 ? 3 : 2; }
 
-// Pages per unit where the caller leaves it to the library.
-inline int default_chunk(int B, int list_pages)
+// Pages per unit where the caller leaves it to the library: as many units as the GPU holds at
+// once (6 CTAs on each of 152 SMs) if every list is full, and at least 8 pages, two a warp.
+// `spread`: how many times that where lists are bounded only by the table's width, most of them
+// being much shorter.  Measured (us): a window of 2000 tokens, 16
+// sequences 20 pages 12.5, 48 pages 14.0, 4 pages 19; a window of 1000, 64 sequences 24 pages
+// 24.0, 48 pages 21.6, all 65 pages 20.3; scored, 64 sequences up to 2048 tokens 24 pages 19.4,
+// 36 pages 17.2, 128 pages over 20.
+inline int default_chunk(int B, int list_pages, int spread)
 {
-    const int64_t units = (int64_t)B * kHkv * list_pages;
-    const int64_t ppc = (units / (152 * 12) + kWarps - 1) / kWarps * kWarps;
-    return (int)std::min<int64_t>(std::max<int64_t>(ppc, kWarps), kMaxPagesPerChunk);
+    const int64_t pages = (int64_t)B * kHkv * list_pages, units = 152 * 6 * spread;
+    const int64_t ppc = ((pages + units - 1) / units + kWarps - 1) / kWarps * kWarps;
+    return (int)std::min<int64_t>(std::max<int64_t>(ppc, 2 * kWarps), kMaxPagesPerChunk);
 }
 
 template <class Warp, int STAGES, bool APPEND, class Sel>
@@ -1039,7 +1045,8 @@ int launch_fused(const pkv_pool *pool, StepArgs &a, const Sel &sel, int B, int m
     a.expire_seq = (options & PKV_STEP_TEST_EXPIRE_WAIT) ? 0 : -1;
     const bool wanted = !(options & PKV_STEP_NO_PDL);
     const bool pdl = follows ? wanted : take_pdl_permission(pool, wanted);
-    const int depth = ring ? ring : default_ring(pages_per_chunk);
+    // (selections of pages: 2 stages were the fastest or within 1 % of it at every size)
+    const int depth = ring ? ring : std::is_same_v<Sel, AllPages> ? default_ring(pages_per_chunk) : 2;
     if (pool->kv_format == PKV_KV_FP8)
         return launch_fp8_depth<APPEND>(tmap, a, sel, B, s, pdl, depth);
     if constexpr (std::is_same_v<Sel, AllPages>) {

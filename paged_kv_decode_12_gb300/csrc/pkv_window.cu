@@ -75,7 +75,7 @@ extern "C" size_t pkv_decode_window_workspace_bytes(int B, int max_blocks, int w
     if (!window_args_ok(B, max_blocks, window, sinks, pages_per_chunk))
         return 0;
     const int list = window_list_pages(max_blocks, window, sinks);
-    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, list);
+    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, list, 1);
     return workspace_layout(B, (list + ppc - 1) / ppc).total();
 }
 
@@ -99,7 +99,7 @@ int decode_window(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v
     if (align & 15u)
         return PKV_ERR_INVALID_ARG;
     const int list = window_list_pages(max_blocks, window, sinks);
-    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, list);
+    const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, list, 1);
     if (list > ppc || append) {
         if (!workspace)
             return PKV_ERR_INVALID_ARG;

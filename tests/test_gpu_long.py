@@ -434,6 +434,8 @@ EVICTS = [
     ([100, 33, 64], 32, 20, 12, "odd"), ([200, 150], 1, 0, 0, "real"), ([200, 150, 1], 33, 1, 0, "odd"),
     ([1500, 1024, 1025, 2047], 700, 100, 4, "ties"), ([2600, 40], 1500, 0, 5, "real"), ([64, 65], 64, 10, 10, "odd"),
     ([300, 5], 299, 5, 5, "real"),
+    # rows longer than the 8192 and 32768 weights that are held in registers
+    ([9000, 8193, 20], 3000, 100, 4, "real"), ([33000, 32769], 5000, 500, 3, "ties"), ([16384], 4096, 0, 0, "odd"),
 ]
 
 
