@@ -23,14 +23,14 @@ namespace {
 
 using namespace dev;
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
-
 // Ascending unsigned order = ascending float order; both zeros are one value, NaN is least.
+// No float has the keys kNone (no token) and kStays (a token that is not up for choice).
+constexpr uint32_t kNone = 0u, kNan = 1u, kStays = 0xffffffffu;
+
 __device__ __forceinline__ uint32_t order_key(float x)
 {
     if (x != x)
-        return 0u;
+        return kNan;
     const uint32_t u = __float_as_uint(x + 0.f);
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
@@ -40,62 +40,26 @@ __device__ __forceinline__ bool evict_length_ok(int L, int src_blocks, int dst_b
     return L >= 0 && L <= src_blocks * kPage && min(L, keep) <= dst_blocks * kPage;
 }
 
-// The keys of tokens lo .. hi-1 of a row, PER of them a thread in registers (token i * 1024 +
-// thread), or, for rows longer than that (PER = 0), read again in every pass.
-template <int PER>
-struct RowKeys {
-    int tiles;
-    uint32_t k[PER];
-    __device__ __forceinline__ RowKeys(const float *w, int lo, int hi) : tiles((hi + kSelThreads - 1) / kSelThreads)
-    {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int t = i * kSelThreads + threadIdx.x;
-            k[i] = t >= lo && t < hi ? order_key(w[t]) : 0u;
-        }
-    }
-    // how many of this thread's keys are at least each of three values (none of them 0)
-    __device__ __forceinline__ void count(const uint32_t (&v)[3], int (&n)[3]) const
-    {
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            if (i >= tiles)
-                break;
-#pragma unroll
-            for (int c = 0; c < 3; ++c)
-                n[c] += k[i] >= v[c];
-        }
-    }
-};
-
-template <>
-struct RowKeys<0> {
-    const float *w;
-    int lo, hi;
-    __device__ __forceinline__ RowKeys(const float *w_, int lo_, int hi_) : w(w_), lo(lo_), hi(hi_) {}
-    __device__ __forceinline__ void count(const uint32_t (&v)[3], int (&n)[3]) const
-    {
-        for (int t = lo + threadIdx.x; t < hi; t += kSelThreads) {
-            const uint32_t k = order_key(w[t]);
-#pragma unroll
-            for (int c = 0; c < 3; ++c)
-                n[c] += k >= v[c];
-        }
-    }
-};
-
-// One CTA per (sequence, KV head).  Two bits of the least kept key at a time, from the top: the
-// largest prefix of which at least `need` keys are not below.  Counting keys held in registers
-// against three candidates takes no atomics (a histogram's bins would be few and crowded: weights
-// share their exponents) and one barrier a step.
-template <int PER>
-__global__ void __launch_bounds__(kSelThreads, PER > 0 && PER <= 8 ? 2 : 1)
+// One CTA of WARPS warps per (sequence, KV head); warp v has the row's tokens 32 v per .. and on,
+// `per` times 32 of them.  PER > 0: their keys (at most PER a thread) stay in registers; PER = 0,
+// for rows longer than that: they are read again in every step.
+//
+// The least kept key is found bit by bit, from the top: a bit is set if at least `keep` keys are
+// not below.  Counting takes no atomics (a histogram's bins would be few and crowded: weights
+// share their exponents) and one barrier a step; once no more keys than threads begin with the
+// bits found, they are gathered, one a thread, for the steps left.  The kept tokens' ranks then
+// take one more barrier: every warp counts its own first.  What bounds it is the number of
+// instructions, so few warps with many keys each (512 rows of 6000 weights: 62 us with 32 warps
+// of 8 keys that all counted to the end).
+template <int WARPS, int PER>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 4 : 1)
 select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_blocks, int keep, int recent, int sinks,
               const float *acc, int64_t acc_stride, float *acc_out, int64_t acc_out_stride, int32_t *__restrict__ kept,
               int32_t *__restrict__ err)
 {
-    __shared__ int sums[2][3][kSelWarps];
-    __shared__ int tile_sums[2][kSelWarps];
+    constexpr int kThreadsHere = WARPS * 32;
+    __shared__ int sums[2][32], tie_sums[32], gathered;
+    __shared__ uint32_t few[kThreadsHere];
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
@@ -111,71 +75,140 @@ select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_bloc
         L = 0;
     }
     const int n = min(L, keep);
-    // of the tokens lo .. hi-1 the `need` heaviest stay; all others stay
-    const int lo = L > keep ? sinks : L, hi = L > keep ? L - recent : L;
-    const int need = L > keep ? keep - sinks - recent : 0;
-    const RowKeys<PER> keys(w, lo, hi);
-    uint32_t bar = 0;     // the key of the least token kept
-    int ties = 0;         // how many of that key are kept
-    if (need > 0) {
-        // keys of NaN are 0 and count like any other: a value of 0 is reached by all hi - lo
-        int above = 0;    // keys above every key that begins with bar's bits so far
-        for (int shift = 30, step = 0; shift >= 0; shift -= 2, step ^= 1) {
-            const uint32_t v[3] = {bar | 1u << shift, bar | 2u << shift, bar | 3u << shift};
-            int c[3] = {0, 0, 0};
-            keys.count(v, c);
+    const int per = (L + kThreadsHere - 1) / kThreadsHere, t0 = warp * per * 32 + lane;
+    // every weight is read, whether it matters or not, so that a thread's reads are in flight at once
+    const auto weight = [&](int i) { return w[max(min(t0 + i * 32, L - 1), 0)]; };
+    const auto key = [&](int i, float x) {
+        const int t = t0 + i * 32;
+        return i >= per || t >= L ? kNone : L <= keep || t < sinks || t >= L - recent ? kStays : order_key(x);
+    };
+    uint32_t held[PER > 0 ? PER : 1];
+    if constexpr (PER > 0) {
 #pragma unroll
-            for (int i = 0; i < 3; ++i) {
-                const int s = __reduce_add_sync(kFull, c[i]);
-                if (lane == 0)
-                    sums[step][i][warp] = s;
-            }
+        for (int i0 = 0; i0 < PER; i0 += 8) {
+#pragma unroll
+            for (int i = i0; i < i0 + 8; ++i)
+                held[i] = i0 < per ? __float_as_uint(weight(i)) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            held[i] = key(i, __uint_as_float(held[i]));
+    }
+    // f(i, key) of this thread's tokens (and of some behind them, eight to a branch)
+    const auto each = [&](const auto &f) {
+        if constexpr (PER > 0) {
+#pragma unroll
+            for (int i0 = 0; i0 < PER; i0 += 8)
+                if (i0 < per)
+#pragma unroll
+                    for (int i = i0; i < i0 + 8; ++i)
+                        f(i, held[i]);
+        } else {
+#pragma unroll 4
+            for (int i = 0; i < per; ++i)
+                f(i, key(i, weight(i)));
+        }
+    };
+    // kept: keys above `bar`, and the first `ties` tokens of that key
+    uint32_t bar = kNone;
+    int ties = 0;
+    if (L > keep) {
+        int above = 0, reach = L;  // keys above those that begin with bar's bits; keys not below bar
+        int bit = 31, buf = 0;
+        const auto total_of = [&](int c) {
+            c = __reduce_add_sync(kFull, c);
+            if (lane == 0)
+                sums[buf][warp] = c;
             __syncthreads();
-            int total[3];
-#pragma unroll
-            for (int i = 0; i < 3; ++i)
-                total[i] = __reduce_add_sync(kFull, sums[step][i][lane]);
-            // the largest of the four continuations that `need` keys reach
-            const int pick = total[2] >= need ? 3 : total[1] >= need ? 2 : total[0] >= need ? 1 : 0;
-            if (pick < 3)
-                above = total[pick];
-            bar |= (uint32_t)pick << shift;
+            const int total = __reduce_add_sync(kFull, lane < WARPS ? sums[buf][lane] : 0);
+            buf ^= 1;
+            return total;
+        };
+        const auto settle = [&](uint32_t with, int total) {
+            if (total >= keep) {
+                bar = with;
+                reach = total;
+            } else {
+                above = total;
+            }
+        };
+        for (; bit >= 0 && reach > keep && reach - above > kThreadsHere; --bit) {
+            const uint32_t with = bar | 1u << bit;
+            int c = 0;
+            each([&](int, uint32_t k) { c += k >= with; });
+            settle(with, total_of(c));
         }
-        ties = need - above;
-    }
-    // the kept tokens in order: ranks within tiles of kSelThreads tokens
-    int done = 0, tied = 0;
-    for (int i = 0; i * kSelThreads < L; ++i) {
-        const int t = i * kSelThreads + tid;
-        const float x = t < L ? w[t] : 0.f;
-        const bool middle = t >= lo && t < hi;
-        const uint32_t k = order_key(x);
-        const bool tie = middle && need > 0 && k == bar;
-        const bool sure = t < L && (!middle || (need > 0 && k > bar));
-        // (ties, sure ones) of each warp, packed in one word: tiles have 1024 tokens
-        const uint32_t bt_ = __ballot_sync(kFull, tie), bs = __ballot_sync(kFull, sure);
-        if (lane == 0)
-            tile_sums[i & 1][warp] = __popc(bt_) << 16 | __popc(bs);
+        if (bit >= 0 && reach > keep) {
+            if (tid == 0)
+                gathered = 0;
+            __syncthreads();
+            const int free_bits = bit + 1;
+            each([&](int, uint32_t k) {
+                if (k != kNone && (free_bits == 32 || (k >> free_bits) == (bar >> free_bits)))
+                    few[atomicAdd(&gathered, 1)] = k;
+            });
+            __syncthreads();
+            const uint32_t mine = tid < gathered ? few[tid] : kNone;
+            const int beyond = above;
+            for (; bit >= 0 && reach > keep; --bit) {
+                const uint32_t with = bar | 1u << bit;
+                settle(with, beyond + total_of(mine >= with));
+            }
+        }
+        ties = keep - above;
+        if (reach == keep) {  // every key from bar on is kept
+            bar -= 1;
+            ties = 0;
+        }
         __syncthreads();
-        const int v = tile_sums[i & 1][lane];
-        const int total = __reduce_add_sync(kFull, v), before = __reduce_add_sync(kFull, lane < warp ? v : 0);
-        const uint32_t lower = (1u << lane) - 1;
-        const int ties_before = tied + (before >> 16) + __popc(bt_ & lower);
-        const int sure_before = (before & 0xffff) + __popc(bs & lower);
-        const int taken_before = min(ties_before, ties) - min(tied, ties);
-        if (sure || (tie && ties_before < ties)) {
-            const int at = done + sure_before + taken_before;
-            k_out[at] = t;
-            w_out[at] = x;
-        }
-        const int tied_now = tied + (total >> 16);
-        done += (total & 0xffff) + min(tied_now, ties) - min(tied, ties);
-        tied = tied_now;
     }
-    __syncthreads();  // with weights in place, the last reads come before the zeros
-    for (int i = n + tid; i < keep; i += kSelThreads)
+    int sure = 0, tied = 0;  // of this thread, then of the warps before
+    each([&](int, uint32_t k) {
+        sure += k > bar;
+        tied += k == bar;
+    });
+    sure = __reduce_add_sync(kFull, sure);
+    tied = __reduce_add_sync(kFull, tied);
+    if (lane == 0) {
+        sums[0][warp] = sure;
+        tie_sums[warp] = tied;
+    }
+    __syncthreads();
+    sure = __reduce_add_sync(kFull, lane < warp ? sums[0][lane] : 0);
+    tied = __reduce_add_sync(kFull, lane < warp ? tie_sums[lane] : 0);
+    const uint32_t lower = (1u << lane) - 1;
+    each([&](int i, uint32_t k) {
+        const bool s = k > bar, e = k == bar;
+        const uint32_t bs = __ballot_sync(kFull, s), be = __ballot_sync(kFull, e);
+        const int before = tied + __popc(be & lower);  // ties before this token
+        if (s || (e && before < ties))
+            k_out[sure + __popc(bs & lower) + min(before, ties)] = t0 + i * 32;
+        sure += __popc(bs);
+        tied += __popc(be);
+    });
+    __syncthreads();
+    // the kept weights, four a thread at a time: all of them are read before any is written, and
+    // none comes from further forward than it goes to, so this may be done in place
+    constexpr int kGroup4 = 4 * WARPS * 32;
+    for (int i0 = 0; i0 < n; i0 += kGroup4) {
+        float x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q * WARPS * 32 + tid;
+            x[q] = i < n ? w[k_out[i]] : 0.f;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = i0 + q * WARPS * 32 + tid;
+            if (i < n)
+                w_out[i] = x[q];
+        }
+    }
+    __syncthreads();
+    for (int i = n + tid; i < keep; i += WARPS * 32)
         k_out[i] = -1;
-    for (int64_t i = n + tid; i < acc_out_stride; i += kSelThreads)
+    for (int64_t i = n + tid; i < acc_out_stride; i += WARPS * 32)
         w_out[i] = 0.f;
 }
 
@@ -392,11 +425,11 @@ extern "C" int pkv_evict(const pkv_pool *pool, const int32_t *bt_src_dev, int sr
     // rows written here are read by later launches: the next decode launch on the pool may
     // not copy pages before its dependency wait
     pool->serialize_next_launch = true;
-    const int longest = src_blocks * kPage;
-    const auto select = longest <= 8 * kSelThreads    ? select_kernel<8>
-                        : longest <= 32 * kSelThreads ? select_kernel<32>
-                                                      : select_kernel<0>;
-    if (const int st = launch_kernel(select, dim3(kHkv, B), dim3(kSelThreads), 0, s, true, seq_lens_dev, src_blocks,
+    const int longest = src_blocks * kPage, threads = longest <= 8 * 32 * 32 ? 8 * 32 : 32 * 32;
+    const auto select = longest <= 8 * 32 * 32    ? select_kernel<8, 32>
+                        : longest <= 32 * 32 * 32 ? select_kernel<32, 32>
+                                                  : select_kernel<32, 0>;
+    if (const int st = launch_kernel(select, dim3(kHkv, B), dim3(threads), 0, s, true, seq_lens_dev, src_blocks,
                                      dst_blocks, keep, recent, sinks, acc, acc_stride, acc_out, acc_out_stride, kept,
                                      dev_err_flag);
         st != PKV_OK)
