@@ -76,6 +76,8 @@ constexpr int kRawSize = kTilePages * kFp8Unit;                // 17 KiB: FP8 un
 constexpr int kRaws = 3;                                       // of them in flight
 constexpr int kLoader = 8, kIssuer = 9, kConverter = 11;       // warps: 2 x 4 softmax, loader, two issuers, (FP8) four
 constexpr int kConverters = 4;                                 // converters
+constexpr int kOutRow = 32 * 4 + 16;                           // half an output row, padded to other banks
+constexpr int kOutSize = 2 * kRowTile * kOutRow;               // 36 KiB: of every row
 constexpr int kScales = 2 * kTilePages * kPage;                // row scales of a tile: K's, then V's
 constexpr int kCols = 512;                                     // tensor memory, all of it
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;        // + 128 / 64 / 32 for the second tile
@@ -111,81 +113,113 @@ struct PrefixArgs {
     int32_t *err;
 };
 
-// A work item: two tiles of 128 query rows of one KV head, each with its run of key tiles.
-struct Item {
-    int g;              // KV head
-    int lead;           // the sequence whose table row holds the prefix
-    int s0[2], ns[2];   // each tile's sequences (ns <= 32; 0: no such tile)
-    int chunk[2];       // each tile's chunk
-    int j0[2], np[2];   // its pages
-    bool shared;        // both tiles go through the same pages
-    __device__ __forceinline__ int tiles(int s) const { return (np[s] + kTilePages - 1) / kTilePages; }
-    // the place in the loader's order of tile s's j-th key tile: the pages of a shared run are
-    // loaded once, two runs of their own alternate as long as both last (the first is no shorter)
-    __device__ __forceinline__ int order(int s, int j) const
-    {
-        return shared ? j : j < tiles(1) ? 2 * j + s : tiles(1) + j;
-    }
-    __device__ __forceinline__ int loads() const { return shared ? tiles(0) : tiles(0) + tiles(1); }
+// Two values, picked without an address (an indexed array would live in memory).
+struct Two {
+    int v0, v1;
+    __device__ __forceinline__ int operator[](int s) const { return s ? v1 : v0; }
 };
 
-// Item `it` of the call (the whole warp): the row tiles of a group are paired and each pair goes
+// A work item: two tiles of 128 query rows of one KV head, each with its run of key tiles.
+struct Item {
+    int g;       // KV head
+    int lead;    // the sequence whose table row holds the prefix
+    Two s0, ns;  // each tile's sequences (ns <= 32; 0: no such tile)
+    Two chunk;   // each tile's chunk
+    Two j0, np;  // its pages
+    Two nt;      // its key tiles
+    bool shared; // both tiles go through the same pages
+    __device__ __forceinline__ int tiles(int s) const { return nt[s]; }
+    // the place in the loader's order of tile s's j-th key tile: the pages of a shared run are
+    // loaded once, two runs of their own alternate as long as both last (the first is no shorter)
+    __device__ __forceinline__ int order(int s, int j) const { return shared ? j : j < nt.v1 ? 2 * j + s : nt.v1 + j; }
+    __device__ __forceinline__ int loads() const { return shared ? nt.v0 : nt.v0 + nt.v1; }
+};
+
+// The items of the call, as a warp looks them up: lane i holds group i (of the first 32; more
+// are read again for every item).  The row tiles of a group are paired and each pair goes
 // through every chunk; an odd last row tile takes two chunks at a time.  Pairs that read the
 // same pages are neighbours, so that the pages come from L2.
-__device__ __forceinline__ bool find_item(const Groups &gr, int it, Item &x)
-{
-    const int lane = threadIdx.x & 31;
-    int64_t base = 0;
-    for (int i0 = 0; i0 < gr.groups; i0 += 32) {
-        Groups::Group gp = {0, 0, 0, false};
-        if (i0 + lane < gr.groups)
-            gp = gr.at(i0 + lane);
-        const int tiles = (gp.n + kTileSeqs - 1) / kTileSeqs;
-        const int chunks = gp.ok ? gr.chunks(gp.prefix) : 0;
-        const int64_t mine = (int64_t)kHkv * ((int64_t)(tiles / 2) * chunks + (tiles & 1) * ((chunks + 1) / 2));
-        int64_t end = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(kFull, end, off);
-            if (lane >= off)
-                end += y;
+struct Items {
+    const Groups &gr;
+    struct Lane {
+        int s0, n, prefix, chunks, items;
+    } own;
+
+    __device__ __forceinline__ explicit Items(const Groups &g) : gr(g), own(group(0)) {}
+
+    __device__ __forceinline__ Lane group(int i0) const
+    {
+        const int i = i0 + (threadIdx.x & 31);
+        Lane x = {0, 0, 0, 0, 0};
+        if (i < gr.groups) {
+            const Groups::Group gp = gr.at(i);
+            const int tiles = (gp.n + kTileSeqs - 1) / kTileSeqs;
+            x.s0 = gp.s0;
+            x.n = gp.n;
+            x.prefix = gp.prefix;
+            x.chunks = gp.ok ? gr.chunks(gp.prefix) : 0;
+            // (at most 8 x 2^11 row tiles x 2^17 chunks)
+            x.items = kHkv * (tiles / 2 * x.chunks + (tiles & 1) * ((x.chunks + 1) / 2));
         }
-        end += base;
-        const unsigned hit = __ballot_sync(kFull, it < end);
-        if (hit) {
-            const int src = __ffs(hit) - 1;
-            const int local = it - (int)__shfl_sync(kFull, end - mine, src);
+        return x;
+    }
+
+    // Item `it` (the whole warp); false past the last.
+    __device__ __forceinline__ bool find(int it, Item &x) const
+    {
+        const int lane = threadIdx.x & 31;
+        int local = it;
+        for (int i0 = 0; i0 < gr.groups; i0 += 32) {
+            const Lane gp = i0 == 0 ? own : group(i0);
+            int src = 0;
+            if (gr.groups > 1) {
+                int end = gp.items;
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1) {
+                    const int y = __shfl_up_sync(kFull, end, off);
+                    if (lane >= off)
+                        end += y;
+                }
+                const unsigned hit = __ballot_sync(kFull, local < end);
+                if (!hit) {
+                    local -= __shfl_sync(kFull, end, 31);
+                    continue;
+                }
+                src = __ffs(hit) - 1;
+                local -= __shfl_sync(kFull, end - gp.items, src);
+            } else if (local >= __shfl_sync(kFull, gp.items, 0)) {
+                return false;
+            }
             const int s0 = __shfl_sync(kFull, gp.s0, src), n = __shfl_sync(kFull, gp.n, src);
-            const int prefix = __shfl_sync(kFull, gp.prefix, src);
-            const int nt = (n + kTileSeqs - 1) / kTileSeqs, nc = gr.chunks(prefix), pairs = nt / 2;
+            const int prefix = __shfl_sync(kFull, gp.prefix, src), nc = __shfl_sync(kFull, gp.chunks, src);
+            const int nt = (n + kTileSeqs - 1) / kTileSeqs, pairs = nt / 2;
             const int paired = kHkv * pairs * nc;
             x.lead = s0;
-            int rt[2];
             x.shared = local < paired;
+            int r0, r1;
             if (x.shared) {
-                rt[0] = 2 * (local % pairs);
-                rt[1] = rt[0] + 1;
-                x.g = local / pairs % kHkv;
-                x.chunk[0] = x.chunk[1] = local / pairs / kHkv;
+                const int q = pairs > 1 ? local / pairs : local;
+                r0 = 2 * (local - q * pairs);
+                r1 = r0 + 1;
+                x.g = q & (kHkv - 1);
+                x.chunk.v0 = x.chunk.v1 = (unsigned)q / kHkv;
             } else {
-                rt[0] = rt[1] = nt - 1;
-                x.g = (local - paired) % kHkv;
-                x.chunk[0] = (local - paired) / kHkv * 2;
-                x.chunk[1] = x.chunk[0] + 1;
+                const unsigned l = local - paired;
+                r0 = r1 = nt - 1;
+                x.g = l & (kHkv - 1);
+                x.chunk.v0 = l / kHkv * 2;
+                x.chunk.v1 = x.chunk.v0 + 1;
             }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                x.j0[s] = x.chunk[s] * gr.chunk_pages;
-                x.np[s] = max(min(prefix - x.j0[s], gr.chunk_pages), 0);
-                x.s0[s] = s0 + rt[s] * kTileSeqs;
-                x.ns[s] = x.np[s] > 0 ? min(kTileSeqs, n - rt[s] * kTileSeqs) : 0;
-            }
+            x.j0 = {x.chunk.v0 * gr.chunk_pages, x.chunk.v1 * gr.chunk_pages};
+            x.np = {max(min(prefix - x.j0.v0, gr.chunk_pages), 0), max(min(prefix - x.j0.v1, gr.chunk_pages), 0)};
+            x.nt = {(x.np.v0 + kTilePages - 1) / kTilePages, (x.np.v1 + kTilePages - 1) / kTilePages};
+            x.s0 = {s0 + r0 * kTileSeqs, s0 + r1 * kTileSeqs};
+            x.ns = {x.np.v0 > 0 ? min(kTileSeqs, n - r0 * kTileSeqs) : 0, x.np.v1 > 0 ? min(kTileSeqs, n - r1 * kTileSeqs) : 0};
             return true;
         }
-        base = __shfl_sync(kFull, end, 31);
+        return false;
     }
-    return false;
-}
+};
 
 // Loader: the pages of every item's key tiles into the ring of stages (FP8: of raw units).  A
 // tile that the chunk does not fill repeats the chunk's last page (its weights are masked); a
@@ -202,7 +236,8 @@ __device__ __forceinline__ void prefix_loader(const CUtensorMap *tmap, const Pre
     Item x;
     int seq = 0;
     bool go = true;
-    for (int it = blockIdx.x; go && find_item(a.gr, it, x); it += gridDim.x) {
+    const Items items(a.gr);
+    for (int it = blockIdx.x; go && items.find(it, x); it += gridDim.x) {
         const int32_t *row = a.bt + (size_t)x.lead * a.max_blocks;
         const int most = x.tiles(0);
         int ids[2] = {0, 0};  // lane l: the id of page l of the current run of 4 key tiles
@@ -267,9 +302,10 @@ __device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint
 {
     constexpr int kRing = stages_of(true);
     const int t = threadIdx.x - kConverter * 32, lane = threadIdx.x & 31;
+    const Items items(a.gr);
     Item x;
     int seq = 0;
-    for (int it = blockIdx.x; find_item(a.gr, it, x); it += gridDim.x) {
+    for (int it = blockIdx.x; items.find(it, x); it += gridDim.x) {
         const int n = x.loads();
         for (int i = 0; i < n; ++i, ++seq) {
             const int rs = seq % kRaws, st = seq % kRing;
@@ -374,7 +410,7 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
     Item x;
     int loaded = 0;  // key tiles of earlier items
     int done = 0;    // of them, this row tile's
-    int items = 0;   // earlier items with such a row tile
+    int used = 0;    // earlier items with such a row tile
     const auto scores = [&](int j, int h) {
         const int seq = loaded + x.order(s, j), st = seq % kStages;
         if (h == 0) {
@@ -400,10 +436,11 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
             issue_output<false>(v, to, p, empty, uses, &bars.o_step[s], last);
         return true;
     };
-    for (int it = blockIdx.x; find_item(a.gr, it, x); it += gridDim.x) {
+    const Items items(a.gr);
+    for (int it = blockIdx.x; items.find(it, x); it += gridDim.x) {
         const int nt = x.tiles(s);
         if (nt) {
-            bool go = tc::wait_warp(&bars.q_full[s], items & 1, &bars.stop);
+            bool go = tc::wait_warp(&bars.q_full[s], used & 1, &bars.stop);
             tc::fence_after();
             go = go && scores(0, 0) && scores(0, 1);
             for (int j = 0; j < nt && go; ++j)
@@ -421,7 +458,7 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
                 (void)mbar_wait_warp(&bars.drained[s], 0);
                 return;
             }
-            ++items;
+            ++used;
         }
         loaded += x.loads();
         done += nt;
@@ -535,7 +572,7 @@ __device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, const Sca
 
 // Softmax warps of row tile s: thread = query row (sequence r / 4 of the tile, head r % 4).
 template <bool FP8>
-__device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &bars, uint32_t tmem, int s)
+__device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &bars, uint32_t tmem, int s, uint8_t *out)
 {
     constexpr int kStages = stages_of(FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -543,34 +580,51 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + kColS + s * 128, to = tmem + lanes + kColO + s * 64,
                    tq = tmem + lanes + kColQ + s * 32;
-    Item x;
-    int loaded = 0, done = 0, items = 0;
-    for (int it = blockIdx.x; find_item(a.gr, it, x); it += gridDim.x) {
-        const int nt = x.tiles(s);
-        if (nt == 0) {
-            loaded += x.loads();
-            continue;
+    const Items items(a.gr);
+    int it = blockIdx.x;
+    int loaded = 0, done = 0, used = 0;
+    // The next item with such a row tile, from item `it` on; `skipped` counts the key tiles of
+    // those without.
+    const auto next = [&](Item &x, int &skipped) {
+        skipped = 0;
+        for (; items.find(it, x); it += gridDim.x) {
+            if (x.tiles(s))
+                return true;
+            skipped += x.loads();
         }
+        return false;
+    };
+    // An item's query rows into tensor memory: 64 values, two to a column.  (Every product of the
+    // previous item with its queries is done when its last scores are there.)
+    const auto queries = [&](const Item &x) {
         const bool live = r / kGroup < x.ns[s];
         const int b = x.s0[s] + r / kGroup, h = x.g * kGroup + r % kGroup;
-        {  // the query row: 64 values, two to a column
-            uint32_t w[32];
-            const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((size_t)b * kHq + h) * kD);
+        uint32_t w[32];
+        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + ((size_t)b * kHq + h) * kD);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
-                w[4 * i] = v.x;
-                w[4 * i + 1] = v.y;
-                w[4 * i + 2] = v.z;
-                w[4 * i + 3] = v.w;
-            }
-            tc::st32(tq, w);
-            tc::wait_st();
-            tc::fence_before();
-            __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive(&bars.q_full[s]);
+        for (int i = 0; i < 8; ++i) {
+            const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
         }
+        tc::st32(tq, w);
+        tc::wait_st();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0)
+            tc::mbar_arrive(&bars.q_full[s]);
+    };
+    Item x, y;
+    int skipped;
+    bool more = next(x, skipped);
+    if (more)
+        queries(x);
+    while (more) {
+        loaded += skipped;
+        const int nt = x.tiles(s);
+        const bool idle = (warp & 3) * 32 >= x.ns[s] * kGroup;  // no row of the warp is a query: it only keeps step
         float m = 0.f, l = 0.f;
         int bad = 0;
         for (int j = 0; j < nt; ++j) {
@@ -579,6 +633,11 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
             for (int hf = 0; hf < 2; ++hf) {
                 if (!tc::wait_warp(&bars.s_full[s][hf], (done + j) & 1, &bars.stop))
                     return;
+                if (idle) {
+                    if (lane == 0)
+                        tc::mbar_arrive(&bars.p_full[s][hf]);
+                    continue;
+                }
                 tc::fence_after();
                 const int before = 2 * (done + j) + hf;  // products of this row tile so far
                 const bool first = j == 0 && hf == 0;
@@ -610,31 +669,47 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
                     tc::mbar_arrive(&bars.p_full[s][hf]);
             }
         }
-        if (!tc::wait_warp(&bars.o_full[s], items & 1, &bars.stop))
+        // the next item's first scores are made while this one's last product and its output end
+        it += gridDim.x;
+        more = next(y, skipped);
+        if (more)
+            queries(y);
+        if (!tc::wait_warp(&bars.o_full[s], used & 1, &bars.stop))
             return;
         tc::fence_after();
-        // the chunk's partial; with a bad page id it is empty
-        const size_t idx = ((size_t)b * kHq + h) * a.max_chunks + x.chunk[s];
+        // The chunk's partial; with a bad page id it is empty.  A thread's row goes through shared
+        // memory, so that the warp writes whole lines: 128 bytes of four rows at once.
+        const int ns = x.ns[s] - (warp & 3) * 8;  // of the warp's 8 sequences, those there are
+        const size_t first = ((size_t)(x.s0[s] + (warp & 3) * 8) * kHq + x.g * kGroup) * a.max_chunks + x.chunk[s];
+        const size_t per_seq = (size_t)kHq * a.max_chunks;
+        float4 *own = reinterpret_cast<float4 *>(out + lane * kOutRow);
+        float4 *dst = reinterpret_cast<float4 *>(a.part_o + (first + (size_t)(lane / 8) * a.max_chunks) * kD) + lane % 8;
+        const float4 *line = reinterpret_cast<const float4 *>(out + lane / 8 * kOutRow) + lane % 8;
 #pragma unroll
         for (int q2 = 0; q2 < 2; ++q2) {
             uint32_t w[32];
             tc::ld32(to + q2 * 32, w);
-            if (live) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    reinterpret_cast<float4 *>(a.part_o + idx * kD)[q2 * 8 + i] =
-                        bad ? make_float4(0.f, 0.f, 0.f, 0.f)
-                            : make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
-                                          __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3]));
-            }
+            for (int i = 0; i < 8; ++i)
+                own[i] = bad ? make_float4(0.f, 0.f, 0.f, 0.f)
+                             : make_float4(__uint_as_float(w[4 * i]), __uint_as_float(w[4 * i + 1]),
+                                           __uint_as_float(w[4 * i + 2]), __uint_as_float(w[4 * i + 3]));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // sequence i, head lane / 8
+                if (i < ns)
+                    dst[i * per_seq * (kD / 4) + q2 * 8] = line[i * 4 * (kOutRow / 16)];
+            __syncwarp();
         }
-        if (live)
-            a.part_ml[idx] = bad ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
+        if (lane / kGroup < ns)
+            a.part_ml[first + lane / kGroup * per_seq + (size_t)(lane % kGroup) * a.max_chunks] =
+                bad ? make_float2(-INFINITY, 0.f) : make_float2(m, l);
         if (bad && r == 0 && a.err)
             atomicOr(a.err, PKV_DEVERR_PAGE_RANGE);
         loaded += x.loads();
         done += nt;
-        ++items;
+        ++used;
+        x = y;
     }
 }
 
@@ -644,8 +719,10 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
 {
     constexpr int kStages = stages_of(FP8);
     extern __shared__ uint8_t smem_raw[];
-    uint8_t *stages = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint8_t *raws = stages + kStages * kStageSize;
+    // (an offset, not a rounded address: the compiler keeps shared-memory instructions)
+    uint8_t *stages = smem_raw + (-smem_addr(smem_raw) & 1023u);
+    uint8_t *outs = stages + kStages * kStageSize;
+    uint8_t *raws = outs + kOutSize;
     PrefixBars &bars = *reinterpret_cast<PrefixBars *>(raws + (FP8 ? kRaws * kRawSize : 0));
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -685,7 +762,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
     else if (warp >= kIssuer)
         prefix_issuer<kStages>(a, stages, bars, tmem, warp - kIssuer);
     else
-        prefix_softmax<FP8>(a, bars, tmem, warp >> 2);
+        prefix_softmax<FP8>(a, bars, tmem, warp >> 2, outs + warp * (32 * kOutRow));
     __syncthreads();
     if (threadIdx.x == 0 && bars.stop && a.err)
         atomicOr(a.err, PKV_DEVERR_TIMEOUT);
@@ -696,8 +773,12 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
 constexpr int kSms = 152;
 
 // Pages per prefix chunk where the caller leaves it to the library: the chunk count whose waves
-// of work items (two row tiles each, one CTA per SM) take the fewest key tiles in all, an item
-// costing about two key tiles besides its own and each chunk a little merging.
+// of work items (two row tiles each, one CTA per SM) take the least time, in key tiles (1.05 us):
+// an item costs 3.3 besides its own, and every chunk 0.42 of merging and as much as 0.5 more with
+// the number of sequences (to 256).  Measured with chunks of 8 / 16 / 32 / 64 / 128 / 512 pages
+// (us): 256 sequences, 2048 pages 357 / 236 / 162 / 122 / 104 / 93; 64 sequences, 128 pages
+// 25 / 20 / 17 / 20 / 28; 16 sequences, 512 pages 21 / 14 / 14 / 17 / 25 / 65; 4 sequences, 32
+// pages 7.5 / 8.6 / 9.8.
 int default_prefix_chunk(int B, int groups, int max_prefix)
 {
     const int tiles = (max_prefix + kTilePages - 1) / kTilePages;
@@ -707,7 +788,7 @@ int default_prefix_chunk(int B, int groups, int max_prefix)
     for (int chunks = 1; chunks <= tiles && chunks <= 64; ++chunks) {
         const int per = (tiles + chunks - 1) / chunks;
         const int64_t items = (kHkv * row_tiles * ((tiles + per - 1) / per) + 1) / 2;
-        const double cost = (double)((items + kSms - 1) / kSms) * (per + 2) + 0.1 * chunks;
+        const double cost = (double)((items + kSms - 1) / kSms) * (per + 3.3) + (0.42 + 0.5 * B / 256) * chunks;
         if (cost < best_cost) {
             best_cost = cost;
             best = per;
@@ -750,7 +831,7 @@ int launch_prefix(const pkv_pool *pool, const PrefixArgs &a, int64_t max_items, 
     if (!tmap)
         return PKV_ERR_CUDA;
     constexpr int smem =
-        1024 + stages_of(FP8) * kStageSize + (FP8 ? kRaws * kRawSize : 0) + (int)sizeof(PrefixBars);
+        1024 + stages_of(FP8) * kStageSize + kOutSize + (FP8 ? kRaws * kRawSize : 0) + (int)sizeof(PrefixBars);
     static PerDeviceOnce attr;
     if (const int st = ensure_smem_attr(attr, prefix_kernel<FP8>, smem); st != PKV_OK)
         return st;
@@ -771,8 +852,8 @@ __global__ void __launch_bounds__(kThreads) merge_kernel(StepArgs a, Groups gr)
     const int n = list.first_slot() + max(1, (list.count() + a.pages_per_chunk - 1) / a.pages_per_chunk);
     const int h = g * kGroup + (threadIdx.x >> 5), dp = threadIdx.x & 31;
     const size_t base = ((size_t)b * kHq + h) * a.max_chunks;
-    float Mx, ls, r0, r1;
-    merge_partials(a.part_ml + base, reinterpret_cast<const float2 *>(a.part_o + base * kD) + dp, n, Mx, ls, r0, r1);
+    float ls, r0, r1;
+    merge_eights(a.part_ml + base, reinterpret_cast<const float2 *>(a.part_o + base * kD) + dp, n, ls, r0, r1);
     reinterpret_cast<uint32_t *>(a.out + ((size_t)b * kHq + h) * kD)[dp] = finish_pair(r0, r1, ls);
 }
 

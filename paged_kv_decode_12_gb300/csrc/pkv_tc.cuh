@@ -214,25 +214,30 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-// Bounded waits of one thread and of a whole warp (all of whose lanes get the same answer).
-// They give up after kWaitLimit polls, or as soon as another wait of the CTA has given up
-// (*stop set), and set *stop when they do.
-__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, volatile int *stop)
+// Bounded wait of a whole warp, all of whose lanes get the same answer.  It gives up after
+// kWaitLimit polls, or as soon as another wait of the CTA has given up (*stop set), and sets
+// *stop when it does.
+// One try of every lane and their common answer.
+__device__ __forceinline__ bool try_warp(uint64_t *bar, uint32_t parity)
 {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (mbar_try_wait(bar, parity))
-            return true;
-        if (*stop)
-            return false;
-    }
-    *stop = 1;
-    return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "vote.sync.all.pred q, p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 
 __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, volatile int *stop)
 {
+    if (try_warp(bar, parity))
+        return true;
     for (uint32_t i = 0; i < kWaitLimit; ++i) {
-        if (__all_sync(kFull, mbar_try_wait(bar, parity)))
+        if (try_warp(bar, parity))
             return true;
         if (__any_sync(kFull, *stop))
             return false;
