@@ -370,7 +370,9 @@ int pkv_prefill_append(const pkv_pool *pool, const uint16_t *k, const uint16_t *
  * limit does.  The unit then waits (bounded) for its copies in flight -- they are
  * copies of valid pages, so they land -- sets PKV_DEVERR_TIMEOUT in the error flag and
  * finishes: sequence 0's outputs are undefined, every other sequence's are computed as
- * usual, and the merge counters are left at zero.  No copy stalls and nothing faults. */
+ * usual, and the merge counters are left at zero.  No copy stalls and nothing faults.
+ * (pkv_decode_shared: the first wait for scores of the first prefix work item gives up as
+ * well; the outputs of the sequences whose prefix that CTA goes through are undefined.) */
 #define PKV_STEP_TEST_EXPIRE_WAIT 0x40000
 
 /* Bytes of device workspace pkv_decode_step needs: pkv_decode_workspace_bytes. */

@@ -111,6 +111,7 @@ struct PrefixArgs {
     float *part_o;
     int max_chunks;
     int32_t *err;
+    int expire;          // testing aid: the first wait for scores gives up at once (PKV_STEP_TEST_EXPIRE_WAIT)
 };
 
 // Two values, picked without an address (an indexed array would live in memory).
@@ -275,7 +276,7 @@ __device__ __forceinline__ void prefix_loader(const CUtensorMap *tmap, const Pre
             }
         }
     }
-    if (bars.stop)  // let the copies in flight land (bounded)
+    if (*(volatile int *)&bars.stop)  // let the copies in flight land (bounded)
         for (int i = max(seq - kRing, 0); i < seq; ++i)
             (void)mbar_wait_warp(&full[i % kRing], (i / kRing) & 1);
 }
@@ -631,6 +632,10 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
             const int pages = x.np[s] - j * kTilePages;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
+                if (a.expire && s == 0 && used == 0 && blockIdx.x == 0) {
+                    *(volatile int *)&bars.stop = 1;
+                    return;
+                }
                 if (!tc::wait_warp(&bars.s_full[s][hf], (done + j) & 1, &bars.stop))
                     return;
                 if (idle) {
@@ -911,6 +916,8 @@ extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const 
     a.scale_log2 = scale * kLog2e;
     a.out = out;
     a.err = dev_err_flag;
+    if (plan.max_items > INT32_MAX)
+        return PKV_ERR_INVALID_ARG;
     // both launches check the options; the first is the one that must not run if they are refused
     if (const int st = check_options<OwnPages<true>>(pool, B, max_blocks, plan.own_ppc, options); st != PKV_OK)
         return st;
@@ -928,6 +935,7 @@ extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const 
         p.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.o_offset());
         p.max_chunks = plan.max_chunks;
         p.err = dev_err_flag;
+        p.expire = (options & PKV_STEP_TEST_EXPIRE_WAIT) ? 1 : 0;
         if (const int st = pool->kv_format == PKV_KV_FP8 ? launch_prefix<true>(pool, p, plan.max_items, s, pdl)
                                                          : launch_prefix<false>(pool, p, plan.max_items, s, pdl);
             st != PKV_OK)

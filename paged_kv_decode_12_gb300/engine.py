@@ -27,6 +27,12 @@ step still appends one token to every sequence and attends over all of its pages
 only the barrier that made all micro-batches finish step s before any began step
 s + 1 is gone (a micro-batch's next step depends on its own sequences only).  The
 bytes written are those of the same steps run one by one.
+
+Long contexts: an engine with ``window=W`` (and ``sinks=S``) attends to the last W and the first
+S tokens in every step; ``attention_shared`` attends for groups of sequences behind a shared
+prefix, ``attention_scored`` also gathers every cached token's weight, and ``evict`` cuts the
+caches to a budget by those weights (``append`` with ``slots`` then puts a token behind a cut
+cache: its position is no longer its slot).
 """
 from __future__ import annotations
 
@@ -44,7 +50,11 @@ class DecodeEngine:
                  pages_per_chunk: int = 16, variant: int = pkv.PKV_DECODE_DEFAULT, max_pos: int = wl.MAX_CONTEXT,
                  theta: float = wl.ROPE_THETA, pool_seed: int = 0, device: str = "cuda", fused: bool = True,
                  pdl: bool = True, ring: int = 0, kv: str = "bf16", sorted_units: bool = False, chains: int = 1,
-                 split_merge: bool = False):
+                 split_merge: bool = False, window: int = 0, sinks: int = 0):
+        if window < 0 or sinks < 0 or (sinks and not window):
+            raise ValueError("window and sinks are token counts; sinks need a window (0: attend to everything)")
+        if window and split_merge:
+            raise ValueError("the two-kernel attention has no window")
         if kv not in ("bf16", "fp8"):
             raise ValueError(f"kv must be 'bf16' or 'fp8', not {kv!r}")
         if not 1 <= chains <= batch:
@@ -52,6 +62,7 @@ class DecodeEngine:
         if split_merge and fused:
             raise ValueError("split_merge selects the two-kernel attention of the separate path (fused=False)")
         self.kv = kv
+        self.window, self.sinks = window, sinks
         self.device = torch.device(device)
         self.layers, self.batch, self.max_blocks = layers, batch, max_blocks
         self.pages_per_chunk, self.variant, self.max_pos = pages_per_chunk, variant, max_pos
@@ -78,6 +89,7 @@ class DecodeEngine:
         self.attn_options = pkv.PKV_DECODE_SPLIT_MERGE | variant if split_merge else self.step_options
         self.bt = None
         self.bt_host = None
+        self._extra_ws = {}   # workspaces of the shared, scored and evict calls, by call and size
         self.chains = chains
         self.chain_bounds = chain_bounds(batch, chains)
         # each chain has its own stream and its own workspace (counters start at zero)
@@ -130,17 +142,31 @@ class DecodeEngine:
             pass
 
     # ------------------------------------------------------------------ step
-    def append(self, layer: int, k_new, v_new, q, pos_dev, stream=None, rows=None) -> None:
-        """pkv_append_rope of one layer (rows r0..r1-1 with ``rows=(r0, r1)``)."""
+    def append(self, layer: int, k_new, v_new, q, pos_dev, stream=None, rows=None, slots=None) -> None:
+        """pkv_append_rope of one layer (rows r0..r1-1 with ``rows=(r0, r1)``); with ``slots`` (int32
+        device tensor) the tokens go to those cache slots, rotated to their positions
+        (pkv_append_rope_at)."""
         r0, r1 = rows if rows is not None else (0, self.batch)
+        if slots is not None:
+            pkv.pkv_append_rope_at(self.pool, k_new[r0:r1], v_new[r0:r1], q[r0:r1], q[r0:r1], self.bt[layer, r0:r1],
+                                   self.max_blocks, pos_dev[r0:r1], slots[r0:r1], r1 - r0, self.rope, self.max_pos,
+                                   self.err, stream)
+            return
         pkv.pkv_append_rope(self.pool, k_new[r0:r1], v_new[r0:r1], q[r0:r1], self.bt[layer, r0:r1], self.max_blocks,
                             pos_dev[r0:r1], r1 - r0, self.rope, self.max_pos, self.err, stream)
 
     def attention(self, layer: int, q, seq_lens_dev, out, stream=None, variant=None, rows=None,
                   workspace=None) -> None:
         """pkv_decode_attention(_variant) of one layer with the engine's attention options
-        (or ``variant``); rows and workspace as for ``fused_layer``."""
+        (or ``variant``); rows and workspace as for ``fused_layer``.  With a window:
+        pkv_decode_window."""
         r0, r1 = rows if rows is not None else (0, self.batch)
+        if self.window:
+            pkv.pkv_decode_window(self.pool, q[r0:r1], self.bt[layer, r0:r1], self.max_blocks, seq_lens_dev[r0:r1],
+                                  r1 - r0, self.scale, self.window, self.sinks, self.pages_per_chunk,
+                                  self.workspace if workspace is None else workspace, self.ws_bytes, out[r0:r1],
+                                  self.err, stream, self.attn_options if variant is None else variant)
+            return
         pkv.pkv_decode_attention_variant(self.pool, q[r0:r1], self.bt[layer, r0:r1], self.max_blocks,
                                          seq_lens_dev[r0:r1], r1 - r0, self.scale, self.pages_per_chunk,
                                          self.workspace if workspace is None else workspace, self.ws_bytes,
@@ -152,6 +178,13 @@ class DecodeEngine:
         """Append + attention of one layer in one launch (positions are seq_lens - 1); with
         ``rows=(r0, r1)`` for the batch rows r0..r1-1 only (contiguous slices of every argument)."""
         r0, r1 = rows if rows is not None else (0, self.batch)
+        if self.window:
+            pkv.pkv_decode_step_window(self.pool, k_new[r0:r1], v_new[r0:r1], q[r0:r1], self.bt[layer, r0:r1],
+                                       self.max_blocks, seq_lens_dev[r0:r1], r1 - r0, self.rope, self.max_pos,
+                                       self.scale, self.window, self.sinks, self.pages_per_chunk,
+                                       self.step_ws if workspace is None else workspace, self.step_ws_bytes,
+                                       out[r0:r1], self.err, stream, self.step_options)
+            return
         pkv.pkv_decode_step(self.pool, k_new[r0:r1], v_new[r0:r1], q[r0:r1], self.bt[layer, r0:r1], self.max_blocks,
                             seq_lens_dev[r0:r1], r1 - r0, self.rope, self.max_pos, self.scale, self.pages_per_chunk,
                             self.step_ws if workspace is None else workspace, self.step_ws_bytes, out[r0:r1],
@@ -163,8 +196,8 @@ class DecodeEngine:
         contiguous rows; a layer's arrays are the layer-0 rows plus the tensors' layer stride."""
         r0, r1 = rows if rows is not None else (0, self.batch)
         ws = self.step_ws if workspace is None else workspace
-        if k_new.stride(0) != v_new.stride(0) or q.stride(0) != out.stride(0):
-            for layer in range(self.layers):  # layer strides the one call cannot express
+        if self.window or k_new.stride(0) != v_new.stride(0) or q.stride(0) != out.stride(0):
+            for layer in range(self.layers):  # (layer strides the one call cannot express)
                 self.fused_layer(layer, q[layer], k_new[layer], v_new[layer], seq_lens_dev, out[layer], stream,
                                  rows, ws)
             return
@@ -370,6 +403,62 @@ class DecodeEngine:
             sent[s].record(self._d2h)
         cur.wait_event(sent[steps - 1])
         cur.wait_event(ready[steps - 1])
+
+    # ------------------------------------------------------------------ long contexts
+    def _workspace(self, call: str, nbytes: int):
+        """The call's workspace of at least ``nbytes`` (zeroed when made, then kept: the calls leave
+        their merge counters at zero)."""
+        ws = self._extra_ws.get(call)
+        if ws is None or ws.numel() < nbytes:
+            ws = self._extra_ws[call] = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=self.device)
+        return ws
+
+    def attention_shared(self, layer: int, q, seq_lens_dev, group_starts_dev, prefix_pages_dev, max_prefix_pages: int,
+                         out, stream=None, prefix_pages_per_chunk: int = 0) -> None:
+        """pkv_decode_shared of one layer over the engine's batch: group i is rows group_starts[i] ..
+        group_starts[i + 1] - 1, behind the first prefix_pages[i] pages of its first row."""
+        groups = prefix_pages_dev.numel()
+        args = (self.batch, self.max_blocks, groups, max_prefix_pages, self.pages_per_chunk, prefix_pages_per_chunk)
+        nbytes = pkv.pkv_decode_shared_workspace_bytes(*args)
+        pkv.pkv_decode_shared(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, group_starts_dev,
+                              prefix_pages_dev, groups, max_prefix_pages, self.scale, self.pages_per_chunk,
+                              prefix_pages_per_chunk, self._workspace("shared", nbytes), nbytes, out, self.err, stream)
+
+    def attention_scored(self, layer: int, q, seq_lens_dev, acc, acc_out, out, stream=None) -> None:
+        """pkv_decode_scored of one layer: acc_out = acc + the weights (float32 [batch][8][n] with
+        n >= 16 * max_blocks, contiguous; they may be one tensor)."""
+        nbytes = pkv.pkv_decode_scored_workspace_bytes(self.batch, self.max_blocks, self.pages_per_chunk)
+        pkv.pkv_decode_scored(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, self.scale, acc,
+                              acc_out, acc.shape[-1], self.pages_per_chunk, self._workspace("scored", nbytes), nbytes,
+                              out, self.err, stream)
+
+    def evict(self, layer: int, seq_lens, acc, keep: int, recent: int, sinks: int = 0, stream=None) -> np.ndarray:
+        """Cut one layer's caches (lengths ``seq_lens``, host int32) to ``keep`` tokens per KV head by
+        ``acc`` (pkv_evict), in place in ``acc``: new pages are taken from the pool, the table's rows
+        are pointed at them, and the old pages given back (work on the stream so far still reads them;
+        later work on it comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the
+        table of all layers in step: each layer is cut by its own call with the same arguments."""
+        lens = np.asarray(seq_lens, dtype=np.int32)
+        after = np.minimum(lens, keep).astype(np.int32)
+        need = (after + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
+        ids = pkv.pkv_pool_alloc(self.pool, int(need.sum()))
+        dst = np.full((self.batch, self.max_blocks), -1, dtype=np.int32)
+        dst[np.arange(self.max_blocks)[None, :] < need[:, None]] = ids
+        dst_dev = torch.from_numpy(dst).to(self.device)
+        lens_dev = torch.from_numpy(lens).to(self.device)
+        nbytes = pkv.pkv_evict_workspace_bytes(self.batch, keep)
+        pkv.pkv_evict(self.pool, self.bt[layer], self.max_blocks, lens_dev, self.batch, dst_dev, self.max_blocks, keep,
+                      recent, sinks, acc, acc.shape[-1], acc, acc.shape[-1], None, lens_dev,
+                      self._workspace("evict", nbytes), nbytes, self.err, stream)
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        with torch.cuda.stream(s):
+            self.bt[layer].copy_(dst_dev)
+            for t in (dst_dev, lens_dev):
+                t.record_stream(s)
+        old = self.bt_host[layer]
+        pkv.pkv_pool_free(self.pool, old[old >= 0])
+        self.bt_host[layer] = dst
+        return after
 
     def check_errors(self):
         return pkv.pkv_check_device_error(self.err)
