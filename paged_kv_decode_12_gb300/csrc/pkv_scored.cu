@@ -4,23 +4,53 @@
 //     p[h][t] = softmax_t(scale * q[b][h] . K_t),   out[b][h] = sum_t p[h][t] V_t,
 //     acc_out[b][g][t] = acc[b][g][t] + sum_{h in group g} p[h][t],   t < seq_lens[b].
 //
-// A weight is known only when the whole sequence's maximum and sum are, so the work is
-// two launches.  The first is the grid kernel of pkv_step.cuh over every page, which
-// also stores the scores (log2 domain, FP32, the four heads of a token side by side)
-// and, from the unit that merges a (sequence, KV head), log2 of each head's sum.  The
-// second turns scores into weights and adds them, one (KV head, token) per thread.  It
-// re-reads 128 bytes per token where a second pass over the keys would read 1024 (BF16
-// pages) or 544 (FP8), and no atomics are involved: the sum has one order.
+// A weight is known only when the whole sequence's maximum and sum are.  The grid kernel of
+// pkv_step.cuh goes over every page and also stores the scores (log2 domain, FP32, the four heads
+// of a token side by side); the unit that finishes a (sequence, KV head) knows log2 of each head's
+// sum and turns the scores into weights.  For short rows it does so itself, while other units
+// stream their pages; a long row would keep one CTA busy behind all others, so there a second
+// launch does it, one (KV head, token) per thread.
+// Either way 128 bytes per token are re-read where a second pass over the keys would read 1024
+// (BF16 pages) or 544 (FP8), no atomics are involved, and the sum has one order.
 #include "pkv_step.cuh"
 
 namespace pkv {
 namespace {
 
+// acc_out[t] = acc[t] + the four heads' weights of token t, from its scores and log2 of the heads'
+// sums, for t = t0, t0 + STEP, ... < L: N of them, all read before any is written (acc and
+// acc_out may be one array, so the compiler may not reorder them itself).
+template <int N, int STEP>
+__device__ __forceinline__ void add_weights(const float4 *scores, float4 n, const float *acc, float *acc_out, int t0, int L)
+{
+    float4 s[N];
+    float a[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int t = t0 + i * STEP;
+        if (t < L) {
+            s[i] = __ldcg(scores + t);
+            a[i] = acc[t];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int t = t0 + i * STEP;
+        if (t < L)
+            acc_out[t] = a[i] + ((ex2_approx(s[i].x - n.x) + ex2_approx(s[i].y - n.y)) +
+                                 (ex2_approx(s[i].z - n.z) + ex2_approx(s[i].w - n.w)));
+    }
+}
+
+template <bool INLINE>
 struct ScoredPages {
     static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
     float *scores;  // [B][8][tokens][4]
     float *lse;     // [B][32] log2 of the sum of 2^score
     int tokens;     // per (sequence, KV head): 16 * max_blocks
+    const float *acc;
+    float *acc_out;
+    int64_t acc_stride;
 
     struct EmitOf {
         float *row;  // the (sequence, KV head)'s scores
@@ -47,9 +77,24 @@ struct ScoredPages {
         for (int t = threadIdx.x; t < jn * kPage; t += kThreads)
             p[t] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
     }
-    __device__ __forceinline__ void norm(int b, int h, float M, float l) const
+    __device__ __forceinline__ void finished(int b, int g, int L, float M, float l, float *scratch) const
     {
-        lse[b * kHq + h] = l > 0.f ? M + log2f(l) : INFINITY;  // nothing computed: every weight is 0
+        const int hl = threadIdx.x >> 5;
+        const float n = l > 0.f ? M + log2f(l) : INFINITY;  // nothing computed: every weight is 0
+        if (!INLINE) {
+            if ((threadIdx.x & 31) == 0)
+                lse[b * kHq + g * kGroup + hl] = n;
+            return;
+        }
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0)
+            scratch[hl] = n;
+        __syncthreads();
+        const float4 all = *reinterpret_cast<const float4 *>(scratch);
+        const float4 *x = reinterpret_cast<const float4 *>(row(b, g));
+        const size_t at = ((size_t)b * kHkv + g) * acc_stride;
+        for (int t0 = 0; t0 < L; t0 += 8 * kThreads)
+            add_weights<8, kThreads>(x, all, acc + at, acc_out + at, t0 + threadIdx.x, L);
     }
 };
 
@@ -69,15 +114,8 @@ accumulate_kernel(const float4 *__restrict__ scores, const float *__restrict__ l
     const float4 n = *reinterpret_cast<const float4 *>(lse + b * kHq + g * kGroup);
     const size_t row = (size_t)b * kHkv + g;
     const float4 *x = scores + row * ((size_t)max_blocks * kPage);
-#pragma unroll
-    for (int i = 0; i < kAccTokens / kAccThreads; ++i) {
-        const int t = t0 + i * kAccThreads + threadIdx.x;
-        if (t < L) {
-            const float4 s = __ldcg(x + t);
-            const float w = (ex2_approx(s.x - n.x) + ex2_approx(s.y - n.y)) + (ex2_approx(s.z - n.z) + ex2_approx(s.w - n.w));
-            acc_out[row * acc_stride + t] = acc[row * acc_stride + t] + w;
-        }
-    }
+    add_weights<kAccTokens / kAccThreads, kAccThreads>(x, n, acc + row * acc_stride, acc_out + row * acc_stride,
+                                                       t0 + threadIdx.x, L);
 }
 
 struct ScoredWorkspace {
@@ -132,10 +170,13 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     const int ppc = pages_per_chunk ? pages_per_chunk : default_chunk(B, max_blocks, 2);
     const ScoredWorkspace w = scored_workspace(B, max_blocks, (max_blocks + ppc - 1) / ppc);
     char *base = static_cast<char *>(workspace);
-    ScoredPages sel;
+    ScoredPages<true> sel;
     sel.scores = reinterpret_cast<float *>(base + w.attention);
     sel.lse = reinterpret_cast<float *>(base + w.attention + w.scores);
     sel.tokens = max_blocks * kPage;
+    sel.acc = acc;
+    sel.acc_out = acc_out;
+    sel.acc_stride = acc_stride;
     StepArgs a = {};
     a.q = const_cast<uint16_t *>(q);
     a.bt = bt_dev;
@@ -150,10 +191,16 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     // the order costs more than it gives (18.8 us instead of 17.2).
     if (pages_per_chunk == 0 && B <= kMaxSortedBatch && (int64_t)B * kHkv * ((max_blocks + ppc - 1) / ppc) > 4 * 152 * 6)
         options |= PKV_STEP_SORTED;
-    if (const int st = launch_fused<false>(pool, a, sel, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
+    // in the same launch: rows of 4096 tokens at most, or of 16384 where many units finish at
+    // different times (1 sequence of 1024 tokens 5.6 us instead of 7.0, 64 up to 16384 89 instead of
+    // 93; but 8 up to 8192 20 instead of 18)
+    if (sel.tokens <= (B * kHkv >= 3 * 152 ? 16384 : 4096))
+        return launch_fused<false>(pool, a, sel, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
+    const ScoredPages<false> apart = {sel.scores, sel.lse, sel.tokens, acc, acc_out, acc_stride};
+    if (const int st = launch_fused<false>(pool, a, apart, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
         st != PKV_OK)
         return st;
-    const dim3 grid((max_blocks * kPage + kAccTokens - 1) / kAccTokens, kHkv, B);
+    const dim3 grid((sel.tokens + kAccTokens - 1) / kAccTokens, kHkv, B);
     return launch_kernel(accumulate_kernel, grid, dim3(kAccThreads), 0, s, !(options & PKV_STEP_NO_PDL),
                          reinterpret_cast<const float4 *>(sel.scores), static_cast<const float *>(sel.lse), seq_lens_dev,
                          max_blocks, acc, acc_out, acc_stride);

@@ -66,7 +66,7 @@ struct OwnPages {
     }
     __device__ __forceinline__ EmitNothing emit(int, int) const { return {}; }
     __device__ __forceinline__ void skipped(int, int, int, int) const {}
-    __device__ __forceinline__ void norm(int, int, float, float) const {}
+    __device__ __forceinline__ void finished(int, int, int, float, float, float *) const {}
 };
 
 // ------------------------------------------------------------------ the prefix on tensor cores

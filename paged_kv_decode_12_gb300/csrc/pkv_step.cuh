@@ -42,14 +42,15 @@ using namespace dev;
 //                chunk of the table's width, which with wide tables and short sequences would
 //                be mostly CTAs with nothing to do
 // `emit(b, g)` makes what takes the units' scores, `skipped(b, g, j0, jn)` is told of a
-// unit that a bad page id keeps from being computed, `norm(b, h, M, l)` takes the
-// finished softmax statistics of one head.
+// unit that a bad page id keeps from being computed, `finished(b, g, L, M, l, scratch)` is
+// called by all threads of the unit that finishes a (sequence, KV head), each with its
+// head's softmax statistics; `scratch` is shared memory that the unit has done with.
 struct AllPages {
     static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
     __device__ __forceinline__ WholeSequence list(int, int L) const { return {L}; }
     __device__ __forceinline__ EmitNothing emit(int, int) const { return {}; }
     __device__ __forceinline__ void skipped(int, int, int, int) const {}
-    __device__ __forceinline__ void norm(int, int, float, float) const {}
+    __device__ __forceinline__ void finished(int, int, int, float, float, float *) const {}
 };
 
 struct StepArgs {
@@ -426,7 +427,7 @@ __device__ __forceinline__ void merge_eights(const float2 *ml_row, const float2 
 // rotated query rows), and resets the counter.
 template <bool WRITE_Q, class Sel, class Warp>
 __device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, Warp &w, float *state, int *ticket,
-                                            const uint16_t *q_rot, int b, int g, int c, int nunits, int first)
+                                            const uint16_t *q_rot, int b, int g, int c, int nunits, int first, int L)
 {
     const int nchunks = first + nunits;
     const int tid = threadIdx.x, warp = tid >> 5;
@@ -441,8 +442,7 @@ __device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, W
     const uint32_t q_word = reinterpret_cast<const uint32_t *>(q_rot + hl * kD)[dp];
     if (!Sel::kPublish && nchunks == 1) {
         out_row[dp] = finish_pair(o0, o1, lsum);
-        if (dp == 0)
-            sel.norm(b, h, M, lsum);
+        sel.finished(b, g, L, M, lsum, state);
         if (WRITE_Q)
             q_row[dp] = q_word;
         if (Sel::kLateWait) {
@@ -477,8 +477,7 @@ __device__ __forceinline__ void finish_unit(const StepArgs &a, const Sel &sel, W
     else
         merge_partials(ml_row, o_col, nchunks, Mx, ls, r0, r1);
     out_row[dp] = finish_pair(r0, r1, ls);
-    if (dp == 0)
-        sel.norm(b, h, Mx, ls);
+    sel.finished(b, g, L, Mx, ls, state);
     if (WRITE_Q)
         q_row[dp] = q_word;
     if (tid == 0)
@@ -632,7 +631,7 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmap, const StepA
         allow_dependent_launch();
     // the stages are free now: they hold the combine area
     finish_unit<APPEND>(a, sel, w, reinterpret_cast<float *>(sm.stages), ticket, q_rot, b, g, c, nchunks,
-                        list.first_slot());
+                        list.first_slot(), L);
     tl.end(b, c, jn);
 }
 
@@ -888,7 +887,7 @@ __device__ __forceinline__ void decode_unit_fp8(const CUtensorMap &tmap, const S
         allow_dependent_launch();
     // the stages are free now: they hold the combine area
     finish_unit<APPEND>(a, sel, w, reinterpret_cast<float *>(sm.stages), sm.ticket, sm.q_rot, b, g, c, nchunks,
-                        list.first_slot());
+                        list.first_slot(), L);
 }
 
 template <int STAGES, bool APPEND, class Sel>
@@ -951,16 +950,16 @@ __global__ void __launch_bounds__(kThreads, fp8_ctas_per_sm(STAGES) - (Sel::kLoo
 int default_ring(int pages_per_chunk) { return pages_per_chunk >= 64 ? 3 : 2; }
 
 // Pages per unit where the caller leaves it to the library: as many units as the GPU holds at
-// once (6 CTAs on each of 152 SMs) if every list is full, and at least 8 pages, two a warp.
-// `spread`: how many times that where lists are bounded only by the table's width, most of them
-// being much shorter.  Measured (us): a window of 2000 tokens, 16
-// sequences 20 pages 12.5, 48 pages 14.0, 4 pages 19; a window of 1000, 64 sequences 24 pages
-// 24.0, 48 pages 21.6, all 65 pages 20.3; scored, 64 sequences up to 2048 tokens 24 pages 19.4,
-// 36 pages 17.2, 128 pages over 20.
+// once (6 CTAs on each of 152 SMs), if every list is full, but whole lists before more units than
+// that, and at least 8 pages, two a warp.  `spread`: how many times that many units where lists
+// are bounded only by the table's width, most of them being much shorter.  Measured (us): a window
+// of 2000 tokens, 16 sequences 20 pages 9.7, 32 pages 11.0; a window of 1000, 64 sequences 24
+// pages 24.0, 48 pages 21.7, all 65 pages 20.3; a window of 300, 64 sequences 12 pages 11.3, all
+// 20 pages 8.0; scored, 64 sequences up to 2048 tokens 36 pages 16.1, 48 pages 17.1, 64 pages 17.5.
 inline int default_chunk(int B, int list_pages, int spread)
 {
-    const int64_t pages = (int64_t)B * kHkv * list_pages, units = 152 * 6 * spread;
-    const int64_t ppc = ((pages + units - 1) / units + kWarps - 1) / kWarps * kWarps;
+    const int64_t chunks = std::max<int64_t>(1, (int64_t)(152 * 6) * spread / ((int64_t)B * kHkv));
+    const int64_t ppc = ((list_pages + chunks - 1) / chunks + kWarps - 1) / kWarps * kWarps;
     return (int)std::min<int64_t>(std::max<int64_t>(ppc, 2 * kWarps), kMaxPagesPerChunk);
 }
 

@@ -50,7 +50,7 @@ struct WindowPages {
     }
     __device__ __forceinline__ EmitNothing emit(int, int) const { return {}; }
     __device__ __forceinline__ void skipped(int, int, int, int) const {}
-    __device__ __forceinline__ void norm(int, int, float, float) const {}
+    __device__ __forceinline__ void finished(int, int, int, float, float, float *) const {}
 };
 
 // The most pages a list can have: n tokens in a row touch at most (n + 14) / 16 + 1 pages.

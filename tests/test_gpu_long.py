@@ -353,6 +353,23 @@ def test_scored(kv, case):
 
 
 @pytest.mark.parametrize("kv", KV)
+def test_scored_over_a_wide_table_is_the_same(kv):
+    """Wide tables (here over 4096 tokens) add the weights in a launch of their own."""
+    c, bt, lens, rng = whole_case(kv, [300, 77, 1500, 1], 18)
+    q, _ = lh.query(rng, 4)
+    wide = np.full((4, 1025), -1, dtype=np.int32)
+    wide[:, :bt.shape[1]] = bt
+    got = []
+    for table in (bt, wide):
+        acc = torch.from_numpy(np.random.default_rng(1).random((4, HKV, 1025 * PS), dtype=np.float32)).cuda()
+        acc_out = torch.full_like(acc, -9.0)
+        out, _ = run_scored(c, table, lens, q, acc, acc_out, 8)
+        got.append((out, acc_out))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    c.close()
+
+
+@pytest.mark.parametrize("kv", KV)
 def test_scored_output_is_decode_attention(kv):
     c, bt, lens, rng = whole_case(kv, [300, 77, 16, 1], 8)
     q, _ = lh.query(rng, 4)
