@@ -1,4 +1,6 @@
 // pkv_shared.cu -- decode attention for groups of sequences that share a prefix.
+#include <cmath>
+
 #include "pkv_step.cuh"
 #include "pkv_tc.cuh"
 
@@ -778,22 +780,24 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
 constexpr int kSms = 152;
 
 // Pages per prefix chunk where the caller leaves it to the library: the chunk count whose waves
-// of work items (two row tiles each, one CTA per SM) take the least time, in key tiles (1.05 us):
-// an item costs 3.3 besides its own, and every chunk 0.42 of merging and as much as 0.5 more with
-// the number of sequences (to 256).  Measured with chunks of 8 / 16 / 32 / 64 / 128 / 512 pages
-// (us): 256 sequences, 2048 pages 357 / 236 / 162 / 122 / 104 / 93; 64 sequences, 128 pages
-// 25 / 20 / 17 / 20 / 28; 16 sequences, 512 pages 21 / 14 / 14 / 17 / 25 / 65; 4 sequences, 32
-// pages 7.5 / 8.6 / 9.8.
-int default_prefix_chunk(int B, int groups, int max_prefix)
+// of work items (two row tiles each, one CTA per SM) take the least time, in key tiles (BF16 pages
+// 1.05 us, FP8 pages, which are converted, 2.1 us): an item costs 3.3 (1.6) besides its own, and
+// every chunk 0.42 (0.12) of merging and as much as 0.5 (0.25) more with the number of sequences,
+// to 256.  Of several groups the others are taken to be half as long as the longest.  Measured
+// with chunks of 8 / 16 / 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 338 / 222 / 154
+// / 116 / 100 / 89; 64 sequences, 128 pages 24 / 20 / 16 / 18 / 27; 16 sequences, 512 pages 24 / 17
+// / 13 / 16 / 25 / 60, FP8 25 / 19 / 20 / 27 / 44 / 102; 4 sequences, 32 pages 7.3 / 8.4 / 9.5.
+int default_prefix_chunk(int B, int groups, int max_prefix, bool fp8)
 {
     const int tiles = (max_prefix + kTilePages - 1) / kTilePages;
-    const int64_t row_tiles = (B + kTileSeqs - 1) / kTileSeqs + (groups - 1);
+    const double row_tiles = (B + kTileSeqs - 1) / kTileSeqs + (groups - 1) / 2.0;
+    const double item = fp8 ? 1.6 : 3.3, chunk = fp8 ? 0.12 + 0.25 * B / 256 : 0.42 + 0.5 * B / 256;
     int best = tiles;
     double best_cost = 1e30;
     for (int chunks = 1; chunks <= tiles && chunks <= 64; ++chunks) {
         const int per = (tiles + chunks - 1) / chunks;
-        const int64_t items = (kHkv * row_tiles * ((tiles + per - 1) / per) + 1) / 2;
-        const double cost = (double)((items + kSms - 1) / kSms) * (per + 3.3) + (0.42 + 0.5 * B / 256) * chunks;
+        const double items = kHkv * row_tiles * ((tiles + per - 1) / per) / 2;
+        const double cost = std::ceil(items / kSms) * (per + item) + chunk * chunks;
         if (cost < best_cost) {
             best_cost = cost;
             best = per;
@@ -809,17 +813,18 @@ struct SharedPlan {
     bool merge_apart;
 };
 
-SharedPlan shared_plan(int B, int max_blocks, int groups, int max_prefix, int ppc, int prefix_ppc)
+SharedPlan shared_plan(int B, int max_blocks, int groups, int max_prefix, int ppc, int prefix_ppc, bool fp8)
 {
     SharedPlan p;
-    p.own_ppc = ppc ? ppc : default_chunk(B, max_blocks, 2);
+    // (32 pages at most: the width of the table says little about what is behind the prefixes)
+    p.own_ppc = ppc ? ppc : std::min(default_chunk(B, max_blocks, 2), 32);
     p.prefix_chunk = kTilePages;
     p.prefix_slots = 0;
     p.max_items = 0;
     if (max_prefix > 0) {
         const int whole = (max_prefix + kTilePages - 1) / kTilePages * kTilePages;
         p.prefix_chunk = prefix_ppc ? (int)std::min<int64_t>(whole, ((int64_t)prefix_ppc + kTilePages - 1) / kTilePages * kTilePages)
-                                    : default_prefix_chunk(B, groups, max_prefix);
+                                    : default_prefix_chunk(B, groups, max_prefix, fp8);
         p.prefix_slots = (max_prefix + p.prefix_chunk - 1) / p.prefix_chunk;
         // sum over groups of ceil(n / 64) row-tile pairs, each in every chunk
         p.max_items = (int64_t)kHkv * ((B + (int64_t)(2 * kTileSeqs - 1) * groups) / (2 * kTileSeqs)) * p.prefix_slots;
@@ -879,9 +884,14 @@ extern "C" size_t pkv_decode_shared_workspace_bytes(int B, int max_blocks, int g
     using namespace pkv;
     if (!shared_args_ok(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk))
         return 0;
-    return workspace_layout(
-               B, shared_plan(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk).max_chunks)
-        .total();
+    // (for either page format: the library's chunks differ)
+    size_t most = 0;
+    for (const bool fp8 : {false, true})
+        most = std::max(most, workspace_layout(B, shared_plan(B, max_blocks, groups, max_prefix_pages, pages_per_chunk,
+                                                              prefix_pages_per_chunk, fp8)
+                                                      .max_chunks)
+                                  .total());
+    return most;
 }
 
 extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
@@ -905,7 +915,8 @@ extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const 
                                                             prefix_pages_per_chunk))
         return PKV_ERR_WORKSPACE_TOO_SMALL;
     const SharedPlan plan =
-        shared_plan(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk);
+        shared_plan(B, max_blocks, groups, max_prefix_pages, pages_per_chunk, prefix_pages_per_chunk,
+                    pool->kv_format == PKV_KV_FP8);
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     const Groups gr = {group_starts_dev, prefix_pages_dev, groups, max_prefix_pages, plan.prefix_chunk, B};
     StepArgs a = {};
