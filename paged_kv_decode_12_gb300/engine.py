@@ -405,12 +405,29 @@ class DecodeEngine:
         cur.wait_event(ready[steps - 1])
 
     # ------------------------------------------------------------------ long contexts
-    def _workspace(self, call: str, nbytes: int):
-        """The call's workspace of at least ``nbytes`` (zeroed when made, then kept: the calls leave
-        their merge counters at zero)."""
+    def _on(self, stream):
+        return torch.cuda.current_stream(self.device) if stream is None else stream
+
+    def _acc_stride(self, *accs) -> int:
+        for acc in accs:
+            if (acc.dtype != torch.float32 or acc.shape != accs[0].shape or not acc.is_contiguous() or
+                    acc.dim() != 3 or acc.shape[:2] != (self.batch, wl.NUM_KV_HEADS)):
+                raise ValueError("weights: float32 [batch][8][n], contiguous")
+        return acc.shape[-1]
+
+    def _workspace(self, call: str, nbytes: int, stream):
+        """The call's workspace of at least ``nbytes`` (zeroed on its stream when made, then kept: the
+        calls leave their merge counters at zero).  Calls of one kind on two streams must not overlap."""
         ws = self._extra_ws.get(call)
         if ws is None or ws.numel() < nbytes:
-            ws = self._extra_ws[call] = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=self.device)
+            s = self._on(stream)
+            with torch.cuda.stream(s):
+                # (one made inside a capture would be zeroed by the graph's replays only)
+                if torch.cuda.is_current_stream_capturing():
+                    raise RuntimeError(f"make the {call} call once with these sizes before it is captured")
+                if ws is not None:
+                    ws.record_stream(s)
+                ws = self._extra_ws[call] = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=self.device)
         return ws
 
     def attention_shared(self, layer: int, q, seq_lens_dev, group_starts_dev, prefix_pages_dev, max_prefix_pages: int,
@@ -422,41 +439,56 @@ class DecodeEngine:
         nbytes = pkv.pkv_decode_shared_workspace_bytes(*args)
         pkv.pkv_decode_shared(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, group_starts_dev,
                               prefix_pages_dev, groups, max_prefix_pages, self.scale, self.pages_per_chunk,
-                              prefix_pages_per_chunk, self._workspace("shared", nbytes), nbytes, out, self.err, stream)
+                              prefix_pages_per_chunk, self._workspace("shared", nbytes, stream), nbytes, out, self.err,
+                              stream, self.step_options & ~pkv.PKV_STEP_SORTED)
 
     def attention_scored(self, layer: int, q, seq_lens_dev, acc, acc_out, out, stream=None) -> None:
         """pkv_decode_scored of one layer: acc_out = acc + the weights (float32 [batch][8][n] with
         n >= 16 * max_blocks, contiguous; they may be one tensor)."""
+        stride = self._acc_stride(acc, acc_out)
         nbytes = pkv.pkv_decode_scored_workspace_bytes(self.batch, self.max_blocks, self.pages_per_chunk)
         pkv.pkv_decode_scored(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, self.scale, acc,
-                              acc_out, acc.shape[-1], self.pages_per_chunk, self._workspace("scored", nbytes), nbytes,
-                              out, self.err, stream)
+                              acc_out, stride, self.pages_per_chunk, self._workspace("scored", nbytes, stream),
+                              nbytes, out, self.err, stream, self.step_options)
 
     def evict(self, layer: int, seq_lens, acc, keep: int, recent: int, sinks: int = 0, stream=None) -> np.ndarray:
         """Cut one layer's caches (lengths ``seq_lens``, host int32) to ``keep`` tokens per KV head by
         ``acc`` (pkv_evict), in place in ``acc``: new pages are taken from the pool, the table's rows
         are pointed at them, and the old pages given back (work on the stream so far still reads them;
         later work on it comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the
-        table of all layers in step: each layer is cut by its own call with the same arguments."""
+        table of all layers in step: each layer is cut by its own call with the same arguments.
+        A row names all of its sequence's pages; rows may share some (a prefix), and no longer do
+        after it.  Cannot be captured."""
         lens = np.asarray(seq_lens, dtype=np.int32)
+        if lens.shape != (self.batch,) or lens.min() < 0 or lens.max() > wl.PAGE_SIZE * self.max_blocks:
+            raise ValueError("seq_lens: a length within the table's width for every sequence")
+        stride = self._acc_stride(acc)
+        s = self._on(stream)
+        with torch.cuda.stream(s):
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("an eviction takes and gives back pages on the host: it cannot be captured")
         after = np.minimum(lens, keep).astype(np.int32)
         need = (after + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
-        ids = pkv.pkv_pool_alloc(self.pool, int(need.sum()))
-        dst = np.full((self.batch, self.max_blocks), -1, dtype=np.int32)
-        dst[np.arange(self.max_blocks)[None, :] < need[:, None]] = ids
-        dst_dev = torch.from_numpy(dst).to(self.device)
-        lens_dev = torch.from_numpy(lens).to(self.device)
         nbytes = pkv.pkv_evict_workspace_bytes(self.batch, keep)
-        pkv.pkv_evict(self.pool, self.bt[layer], self.max_blocks, lens_dev, self.batch, dst_dev, self.max_blocks, keep,
-                      recent, sinks, acc, acc.shape[-1], acc, acc.shape[-1], None, lens_dev,
-                      self._workspace("evict", nbytes), nbytes, self.err, stream)
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        workspace = self._workspace("evict", nbytes, stream)
+        ids = pkv.pkv_pool_alloc(self.pool, int(need.sum()))
+        try:
+            dst = np.full((self.batch, self.max_blocks), -1, dtype=np.int32)
+            dst[np.arange(self.max_blocks)[None, :] < need[:, None]] = ids
+            dst_dev = torch.from_numpy(dst).to(self.device)
+            lens_dev = torch.from_numpy(lens).to(self.device)
+            pkv.pkv_evict(self.pool, self.bt[layer], self.max_blocks, lens_dev, self.batch, dst_dev, self.max_blocks,
+                          keep, recent, sinks, acc, stride, acc, stride, None, lens_dev, workspace, nbytes, self.err, stream)
+        except Exception:
+            pkv.pkv_pool_free(self.pool, ids)
+            raise
         with torch.cuda.stream(s):
             self.bt[layer].copy_(dst_dev)
             for t in (dst_dev, lens_dev):
                 t.record_stream(s)
         old = self.bt_host[layer]
-        pkv.pkv_pool_free(self.pool, old[old >= 0])
+        pkv.pkv_pool_free(self.pool, np.unique(old[old >= 0]))
+        self.bt_host = self.bt_host.copy()  # (the caller may hold the old tables)
         self.bt_host[layer] = dst
         return after
 

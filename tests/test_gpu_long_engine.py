@@ -29,6 +29,94 @@ def rows_of(eng, kv, layer, b, tokens):
 
 
 @pytest.mark.parametrize("kv", KV)
+def test_refused_evictions_take_no_pages_and_shared_pages_are_freed_once(kv):
+    rng = np.random.default_rng(8)
+    lens, blocks = np.array([40, 40, 0], dtype=np.int32), 4
+    eng = DecodeEngine(40, 1, 3, max_blocks=blocks, max_pos=256, kv=kv)
+    own = eng.build_tables(np.array([40, 33, 1]))
+    bt = own.copy()
+    spare = int(bt[0, 1, 0])
+    bt[0, 1, 0] = bt[0, 0, 0]                    # rows 0 and 1 share their first page
+    pkv.pkv_pool_free(eng.pool, [spare])
+    eng.set_tables(bt)
+    pkv.pkv_prefill_append(eng.pool, *(bf16_dev(rng, (1, 40, HKV, D)) for _ in range(2)), lh.dev(bt[:, 0]), blocks, 1, 0,
+                           40, eng.rope, eng.max_pos, eng.err)
+    acc = torch.from_numpy(rng.random((3, HKV, blocks * PS)).astype(np.float32)).cuda()
+    free = pkv.pkv_pool_info(eng.pool)["num_free"]
+    for args, error in (((0, lens, acc, 20, 15, 6), pkv.PkvError),             # sinks + recent > keep
+                        ((0, lens, acc, 0, 0, 0), pkv.PkvError),
+                        ((0, [40, 65, 0], acc, 20, 4, 1), ValueError),         # a length beyond the table
+                        ((0, [40, -1, 0], acc, 20, 4, 1), ValueError),
+                        ((0, lens[:2], acc, 20, 4, 1), ValueError),
+                        ((0, lens, acc[:, :, ::2], 20, 4, 1), ValueError),
+                        ((0, lens, acc.double(), 20, 4, 1), ValueError)):
+        with pytest.raises(error):
+            eng.evict(*args)
+        assert pkv.pkv_pool_info(eng.pool)["num_free"] == free and np.array_equal(eng.bt_host, bt)
+    before = rows_of(eng, kv, 0, 0, range(40))
+    weights = acc.cpu().numpy()
+    assert eng.evict(0, lens, acc, 20, 4, 1).tolist() == [20, 20, 0]
+    after = rows_of(eng, kv, 0, 0, range(20))
+    for g in range(HKV):
+        ids = tl.plain_evict(weights[0, g], 40, 20, 4, 1)
+        assert np.array_equal(after[0][g], before[0][g, ids]) and np.array_equal(after[1][g], before[1][g, ids])
+    assert (eng.bt_host >= 0).sum() == 4 and np.unique(eng.bt_host[eng.bt_host >= 0]).size == 4
+    assert pkv.pkv_pool_info(eng.pool)["num_free"] == 40 - 4
+    assert eng.evict(0, [0, 0, 0], acc, 20, 4, 1).tolist() == [0, 0, 0]
+    assert pkv.pkv_pool_info(eng.pool)["num_free"] == 40
+    assert eng.check_errors() == (pkv.PKV_OK, 0)
+
+
+def test_first_calls_on_another_stream_and_in_a_capture():
+    """A workspace is zeroed on the stream that its call runs on, and never inside a capture."""
+    rng = np.random.default_rng(9)
+    lens, blocks, B = np.full(4, 200, dtype=np.int32), 16, 4
+    eng = DecodeEngine(80, 1, B, max_blocks=blocks, pages_per_chunk=2, max_pos=512)
+    eng.build_tables(lens)
+    for b in range(B):
+        pkv.pkv_prefill_append(eng.pool, *(bf16_dev(rng, (1, 200, HKV, D)) for _ in range(2)),
+                               lh.dev(eng.bt_host[:, b]), blocks, 1, 0, 200, eng.rope, eng.max_pos, eng.err)
+    q, lens_d = bf16_dev(rng, (B, HQ, D)), lh.dev(lens)
+    starts, none = lh.dev(np.array([0, B], dtype=np.int32)), lh.dev(np.zeros(1, dtype=np.int32))
+    acc = torch.zeros((B, HKV, blocks * PS), device="cuda")
+    want, out, scored = (torch.empty_like(q) for _ in range(3))
+    eng.attention(0, q, lens_d, want)
+    calls = [lambda st: eng.attention_shared(0, q, lens_d, starts, none, 0, out, stream=st),
+             lambda st: eng.attention_scored(0, q, lens_d, acc, acc, scored, stream=st)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        graph.capture_begin()
+        for call in calls:
+            with pytest.raises(RuntimeError, match="before it is captured"):
+                call(None)
+        with pytest.raises(RuntimeError, match="cannot be captured"):
+            eng.evict(0, lens, acc, 100, 10)
+        q.add_(0)
+        graph.capture_end()
+    torch.cuda.synchronize()
+    # garbage where the workspaces will be, and much work on the current stream
+    junk = torch.full((1 << 22,), 7, dtype=torch.int32, device="cuda")
+    del junk
+    slow = torch.zeros(1 << 26, device="cuda")
+    for _ in range(50):
+        slow.add_(1)
+    for call in calls:
+        call(s)
+    s.synchronize()
+    # the same partials merged in FP32: both round to BF16 values a step (2^-7) apart at most
+    for got in (out, scored):
+        assert ((got.double() - want.double()).abs() <= 2.0 ** -7 * want.double().abs() + 2.0 ** -30).all()
+    # 4 heads' weights add to 1 each, but for the roundings of a sum of 200 (2^-24 each) and of an
+    # exponent below 2^4 and its power of two (2^-19)
+    sums = acc.cpu().numpy().astype(np.float64).sum(-1)
+    assert (np.abs(sums - 4) <= 4 * (200 * 2.0 ** -24 + 2.0 ** -19)).all()
+    torch.cuda.synchronize()
+    assert eng.check_errors() == (pkv.PKV_OK, 0)
+
+
+@pytest.mark.parametrize("kv", KV)
 def test_scored_steps_evictions_and_more_steps(kv):
     rng = np.random.default_rng(5)
     layers, prompts = 2, np.array([70, 33, 20], dtype=np.int32)
