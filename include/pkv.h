@@ -598,7 +598,9 @@ size_t pkv_evict_workspace_bytes(int B, int keep);
  * page bt_dev[b][slots_dev[b] / 16], slot slots_dev[b] % 16.  The rotated query rows go to
  * q_out, which may be q; both may be NULL.  Device checks: pos outside [0, max_pos), a
  * slot outside [0, 16*max_blocks) or a page id outside the pool sets the flag and skips
- * that sequence. */
+ * that sequence.  For the launch contract of the decode calls (pkv_decode_attention) the
+ * token's position is its slot: one right behind this call relies on slots_dev[b] >=
+ * seq_lens[b] - 2, and is launched with PKV_STEP_NO_PDL where that does not hold. */
 int pkv_append_rope_at(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, const uint16_t *q,
                        uint16_t *q_out, const int32_t *bt_dev, int max_blocks, const int32_t *pos_dev,
                        const int32_t *slots_dev, int B, const float *rope_table, int max_pos, int32_t *dev_err_flag,

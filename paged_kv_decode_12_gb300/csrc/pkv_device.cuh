@@ -653,7 +653,6 @@ struct WholeSequence {
     __device__ __forceinline__ int logical(int i) const { return i; }
     __device__ __forceinline__ int before(int j) const { return j; }
     __device__ __forceinline__ FirstTokens tokens(int j) const { return {min(kPage, L - j * kPage)}; }
-    __device__ __forceinline__ int row(int b, int) const { return b; }
     __device__ __forceinline__ int first_slot() const { return 0; }
 };
 

@@ -189,8 +189,8 @@ select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_bloc
     __syncthreads();
     // the kept weights, four a thread at a time: all of them are read before any is written, and
     // none comes from further forward than it goes to, so this may be done in place
-    constexpr int kGroup4 = 4 * WARPS * 32;
-    for (int i0 = 0; i0 < n; i0 += kGroup4) {
+    constexpr int kRound = 4 * WARPS * 32;
+    for (int i0 = 0; i0 < n; i0 += kRound) {
         float x[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {

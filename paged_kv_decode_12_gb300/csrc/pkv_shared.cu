@@ -50,7 +50,6 @@ struct OwnPages {
         __device__ __forceinline__ int logical(int i) const { return i + prefix; }
         __device__ __forceinline__ int before(int j) const { return max(j - prefix, 0); }
         __device__ __forceinline__ FirstTokens tokens(int j) const { return {min(kPage, L - j * kPage)}; }
-        __device__ __forceinline__ int row(int b, int) const { return b; }
         __device__ __forceinline__ int first_slot() const { return slots; }
     };
 
@@ -161,7 +160,7 @@ struct Items {
             x.n = gp.n;
             x.prefix = gp.prefix;
             x.chunks = gp.ok ? gr.chunks(gp.prefix) : 0;
-            // (at most 8 x 2^11 row tiles x 2^17 chunks)
+            // (at most 8 x 2^10 pairs x 2^17 chunks)
             x.items = kHkv * (tiles / 2 * x.chunks + (tiles & 1) * ((x.chunks + 1) / 2));
         }
         return x;

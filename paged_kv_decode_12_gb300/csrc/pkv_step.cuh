@@ -28,7 +28,6 @@ using namespace dev;
 //   logical(i)   the sequence's page that entry i is, increasing in i
 //   before(j)    entries whose page is below j
 //   tokens(j)    the tokens of page j attended to
-//   row(b, j)    the sequence whose table row holds page j's entry
 //   first_slot() partials of the sequence that another kernel writes: they are merged
 //                before the units' own
 // and says
@@ -578,10 +577,8 @@ __device__ __forceinline__ void decode_unit(const CUtensorMap &tmap, const StepA
     const bool last_chunk = c == nchunks - 1;
     const int jn = min(nlist - j0, a.pages_per_chunk);
     const int nmine = warp < jn ? (jn - warp + kWarps - 1) / kWarps : 0;
-    if (!prefetched && lane < nmine) {
-        const int j = list.logical(j0 + warp + lane * kWarps);
-        my_page = a.bt[(size_t)list.row(b, j) * a.max_blocks + j];
-    }
+    if (!prefetched && lane < nmine)
+        my_page = a.bt[(size_t)b * a.max_blocks + list.logical(j0 + warp + lane * kWarps)];
     const bool bad = lane < nmine && (my_page < 0 || my_page >= a.num_pages);
     const bool any_bad = __syncthreads_or(bad);  // the new token's page is one of the last chunk's pages
 
@@ -787,10 +784,8 @@ __device__ __forceinline__ void decode_unit_fp8(const CUtensorMap &tmap, const S
     const bool last_chunk = c == nchunks - 1;
     const int jn = min(nlist - j0, a.pages_per_chunk);
     const int nmine = warp < jn ? (jn - warp + kWarps - 1) / kWarps : 0;
-    if (!prefetched && lane < nmine) {
-        const int j = list.logical(j0 + warp + lane * kWarps);
-        my_page = a.bt[(size_t)list.row(b, j) * a.max_blocks + j];
-    }
+    if (!prefetched && lane < nmine)
+        my_page = a.bt[(size_t)b * a.max_blocks + list.logical(j0 + warp + lane * kWarps)];
     const bool bad = lane < nmine && (my_page < 0 || my_page >= a.num_pages);
     const bool any_bad = __syncthreads_or(bad);
 

@@ -34,7 +34,6 @@ struct WindowPages {
         }
         // the tokens of a page below n (any n)
         __device__ __forceinline__ static uint32_t below(int n) { return (1u << min(max(n, 0), kPage)) - 1; }
-        __device__ __forceinline__ int row(int b, int) const { return b; }
         __device__ __forceinline__ int first_slot() const { return 0; }
     };
 
