@@ -1,4 +1,24 @@
 // pkv_shared.cu -- decode attention for groups of sequences that share a prefix.
+//
+//     out[b][h] = sum_t softmax_t(scale * q[b][h] . K_t) V_t,   t < seq_lens[b],
+//
+// where the tokens of the first prefix_pages[i] pages are the same for every sequence of group i.
+// softmax over a split axis: a part S of the tokens gives m = max, l = sum 2^(x - m) and
+// o = sum 2^(x - m) V over S (x the score times log2 e); parts join by 2^(m - M), M their maximum.
+//
+// The prefix is one part or several (chunks).  There the n sequences of a group and the 4 query
+// heads of a KV head are 4 n rows that meet the same keys: a matrix product of enough rows for the
+// tensor cores (tcgen05), S = Q K^T and O += P V with Q, S, P and O in tensor memory and K and V
+// in shared memory as TMA brought them.  What a sequence has behind the prefix goes through the
+// grid kernel of pkv_step.cuh, beside the prefix kernel, and its units (or merge_kernel) join all.
+//
+// What bounds it: a page is read once a row tile pair instead of once a sequence, so bytes count
+// little; 64 exponentials a row and half tile take 512 of the 1000 clocks it lasts, and the rest
+// is the way from one wait to the next.  Two row tiles a CTA fill each other's gaps (256 sequences
+// behind 32768 tokens: 90 us, 760 TFLOP/s).
+// Tried: 16 softmax warps with half a row each, in two forms (149 and 101 us where 8 warps took
+// 96), starting the second row tile half a step later (no change), 8 converter warps for FP8 with
+// registers moved to the softmax warps (30.3 us where 4 took 30.8).
 #include <cmath>
 
 #include "pkv_step.cuh"
@@ -74,7 +94,7 @@ struct OwnPages {
 
 constexpr int kStageSize = kTilePages * kStageBytes;           // 32 KiB: 8 x (K rows, V rows)
 constexpr int kRawSize = kTilePages * kFp8Unit;                // 17 KiB: FP8 units as they lie in the pages
-constexpr int kRaws = 3;                                       // of them in flight
+constexpr int kRaws = 2;                                       // of them in flight
 constexpr int kLoader = 8, kIssuer = 9, kConverter = 11;       // warps: 2 x 4 softmax, loader, two issuers, (FP8) four
 constexpr int kConverters = 4;                                 // converters
 constexpr int kOutRow = 32 * 4 + 16;                           // half an output row, padded to other banks
@@ -83,22 +103,21 @@ constexpr int kScales = 2 * kTilePages * kPage;                // row scales of 
 constexpr int kCols = 512;                                     // tensor memory, all of it
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;        // + 128 / 64 / 32 for the second tile
 
-// FP8 pages leave room for three stages beside the raw units.
-constexpr int stages_of(bool fp8) { return fp8 ? 3 : 4; }
+constexpr int kStages = 4;  // (FP8: three were 12 % slower, five or a third raw unit no faster)
 constexpr int prefix_threads(bool fp8) { return (kConverter + (fp8 ? kConverters : 0)) * 32; }
 
 struct PrefixBars {
-    uint64_t full[4], empty[4];              // a stage holds its pages / both tiles are done with it
+    uint64_t full[kStages], empty[kStages];              // a stage holds its pages / both tiles are done with it
     uint64_t raw_full[kRaws], raw_empty[kRaws];  // the same of the raw units
     uint64_t s_full[2][2], p_full[2][2];     // [row tile][half]: scores are in tensor memory / weights are
     uint64_t o_step[2];                      // one more product of weights and values is done
     uint64_t q_full[2], o_full[2];           // once an item: the queries are in / its last product is done
     uint32_t tmem;
     int stop;                                // a wait gave up
-    int bad[4], raw_bad[kRaws];              // the tile has a bad page id
+    int bad[kStages], raw_bad[kRaws];              // the tile has a bad page id
     uint64_t drained[2];
     // FP8: a stage's row scales, [K (times scale log2 e), V][half][64] in the order of S's columns
-    float scales[3][kScales];
+    float scales[kStages][kScales];
 };
 
 struct PrefixArgs {
@@ -229,7 +248,7 @@ struct Items {
 template <bool FP8>
 __device__ __forceinline__ void prefix_loader(const CUtensorMap *tmap, const PrefixArgs &a, uint8_t *ring, PrefixBars &bars)
 {
-    constexpr int kRing = FP8 ? kRaws : stages_of(false), kSize = FP8 ? kRawSize : kStageSize;
+    constexpr int kRing = FP8 ? kRaws : kStages, kSize = FP8 ? kRawSize : kStageSize;
     uint64_t *full = FP8 ? bars.raw_full : bars.full, *empty = FP8 ? bars.raw_empty : bars.empty;
     int *marks = FP8 ? bars.raw_bad : bars.bad;
     const int lane = threadIdx.x & 31;
@@ -302,7 +321,6 @@ __device__ __forceinline__ void bf16_of_e4m3x4(uint32_t w, uint32_t &lo, uint32_
 // that nothing is rounded here.
 __device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint8_t *raws, uint8_t *stages, PrefixBars &bars)
 {
-    constexpr int kRing = stages_of(true);
     const int t = threadIdx.x - kConverter * 32, lane = threadIdx.x & 31;
     const Items items(a.gr);
     Item x;
@@ -310,9 +328,9 @@ __device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint
     for (int it = blockIdx.x; items.find(it, x); it += gridDim.x) {
         const int n = x.loads();
         for (int i = 0; i < n; ++i, ++seq) {
-            const int rs = seq % kRaws, st = seq % kRing;
+            const int rs = seq % kRaws, st = seq % kStages;
             if (!tc::wait_warp(&bars.raw_full[rs], (seq / kRaws) & 1, &bars.stop) ||
-                (seq >= kRing && !tc::wait_warp(&bars.empty[st], (seq / kRing - 1) & 1, &bars.stop)))
+                (seq >= kStages && !tc::wait_warp(&bars.empty[st], (seq / kStages - 1) & 1, &bars.stop)))
                 return;
             const uint8_t *raw = raws + rs * kRawSize;
             uint8_t *dst = stages + st * kStageSize;
@@ -404,7 +422,6 @@ __device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p,
 
 // Each row tile has an issuer warp of its own, so that one's waits pass while the other's
 // products run: the tensor cores take only a few instructions ahead.
-template <int kStages>
 __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stages, PrefixBars &bars, uint32_t tmem, int s)
 {
     const uint32_t base = smem_addr(stages);
@@ -576,7 +593,6 @@ __device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, const Sca
 template <bool FP8>
 __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &bars, uint32_t tmem, int s, uint8_t *out)
 {
-    constexpr int kStages = stages_of(FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -723,7 +739,6 @@ template <bool FP8>
 __global__ void __launch_bounds__(prefix_threads(FP8), 1)
 prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
 {
-    constexpr int kStages = stages_of(FP8);
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded address: the compiler keeps shared-memory instructions)
     uint8_t *stages = smem_raw + (-smem_addr(smem_raw) & 1023u);
@@ -766,7 +781,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
     else if (FP8 && warp >= kConverter)
         prefix_converter(a, raws, stages, bars);
     else if (warp >= kIssuer)
-        prefix_issuer<kStages>(a, stages, bars, tmem, warp - kIssuer);
+        prefix_issuer(a, stages, bars, tmem, warp - kIssuer);
     else
         prefix_softmax<FP8>(a, bars, tmem, warp >> 2, outs + warp * (32 * kOutRow));
     __syncthreads();
@@ -780,17 +795,18 @@ constexpr int kSms = 152;
 
 // Pages per prefix chunk where the caller leaves it to the library: the chunk count whose waves
 // of work items (two row tiles each, one CTA per SM) take the least time, in key tiles (BF16 pages
-// 1.05 us, FP8 pages, which are converted, 2.1 us): an item costs 3.3 (1.6) besides its own, and
-// every chunk 0.42 (0.12) of merging and as much as 0.5 (0.25) more with the number of sequences,
+// 1.05 us, FP8 pages, which are converted, 1.85 us): an item costs 3.3 (1) besides its own, and
+// every chunk 0.42 (0.12) of merging and as much as 0.5 (0.1) more with the number of sequences,
 // to 256.  Of several groups the others are taken to be half as long as the longest.  Measured
-// with chunks of 8 / 16 / 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 338 / 222 / 154
-// / 116 / 100 / 89; 64 sequences, 128 pages 24 / 20 / 16 / 18 / 27; 16 sequences, 512 pages 24 / 17
-// / 13 / 16 / 25 / 60, FP8 25 / 19 / 20 / 27 / 44 / 102; 4 sequences, 32 pages 7.3 / 8.4 / 9.5.
+// with chunks of 8 / 16 / 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 336 / 224 / 155
+// / 117 / 101 / 90; 64 sequences, 128 pages 22 / 19 / 16 / 18 / 27; 16 sequences, 512 pages 24 / 17
+// / 14 / 16 / 25 / 61, FP8 26 / 19 / 20 / 23 / 38 / 100; 200 sequences in 3 groups, 500 FP8 pages
+// 74 / 54 / 44 / 39 / 47; 4 sequences, 32 pages 7.2 / 8.4 / 9.5.
 int default_prefix_chunk(int B, int groups, int max_prefix, bool fp8)
 {
     const int tiles = (max_prefix + kTilePages - 1) / kTilePages;
     const double row_tiles = (B + kTileSeqs - 1) / kTileSeqs + (groups - 1) / 2.0;
-    const double item = fp8 ? 1.6 : 3.3, chunk = fp8 ? 0.12 + 0.25 * B / 256 : 0.42 + 0.5 * B / 256;
+    const double item = fp8 ? 1.0 : 3.3, chunk = fp8 ? 0.12 + 0.1 * B / 256 : 0.42 + 0.5 * B / 256;
     int best = tiles;
     double best_cost = 1e30;
     for (int chunks = 1; chunks <= tiles && chunks <= 64; ++chunks) {
@@ -840,7 +856,7 @@ int launch_prefix(const pkv_pool *pool, const PrefixArgs &a, int64_t max_items, 
     if (!tmap)
         return PKV_ERR_CUDA;
     constexpr int smem =
-        1024 + stages_of(FP8) * kStageSize + kOutSize + (FP8 ? kRaws * kRawSize : 0) + (int)sizeof(PrefixBars);
+        1024 + kStages * kStageSize + kOutSize + (FP8 ? kRaws * kRawSize : 0) + (int)sizeof(PrefixBars);
     static PerDeviceOnce attr;
     if (const int st = ensure_smem_attr(attr, prefix_kernel<FP8>, smem); st != PKV_OK)
         return st;
