@@ -10,7 +10,7 @@
 // compacted the same way.  A sequence with L <= keep is copied whole.
 //
 // Two launches.  select_kernel: one CTA per (sequence, KV head) finds the least kept weight
-// by its bits, from the top, over order-preserving 32-bit keys, then writes the kept indices
+// by histograms of order-preserving 32-bit keys, then writes the kept indices
 // in order with one ranked pass.  copy_*_kernel: a warp per (sequence, KV head, run of
 // destination pages) gathers the rows by 16-byte moves.
 #include <algorithm>
@@ -40,17 +40,20 @@ __device__ __forceinline__ bool evict_length_ok(int L, int src_blocks, int dst_b
     return L >= 0 && L <= src_blocks * kPage && min(L, keep) <= dst_blocks * kPage;
 }
 
+constexpr int kBins = 1024;
+
 // One CTA of WARPS warps per (sequence, KV head); warp v has the row's tokens 32 v per .. and on,
 // `per` times 32 of them.  PER > 0: their keys (at most PER a thread) stay in registers; PER = 0,
 // for rows longer than that: they are read again in every step.
 //
-// The least kept key is found bit by bit, from the top: a bit is set if at least `keep` keys are
-// not below.  Counting takes no atomics (a histogram's bins would be few and crowded: weights
-// share their exponents) and one barrier a step; once no more keys than threads begin with the
-// bits found, they are gathered, one a thread, for the steps left.  The kept tokens' ranks then
-// take one more barrier: every warp counts its own first.  What bounds it is the number of
-// instructions, so few warps with many keys each (512 rows of 6000 weights: 62 us with 32 warps
-// of 8 keys that all counted to the end).
+// The least kept key is found by histograms: the keys up for choice in a range (at first from their
+// least to their greatest) fall into up to 1024 bins of equal width, the bin that holds the wanted
+// rank becomes the next range, and a range of one key, or one that is kept whole, ends the search:
+// four steps at most, two as a rule.  Once no more keys than threads are left, they are gathered,
+// one a thread, for the steps left.  The kept tokens' ranks then take one more barrier: every warp
+// counts its own first.  What bounds it is the number of instructions and barriers, so few warps
+// with many keys each (512 rows of 6000 weights: 62 us with 32 warps of 8 keys that counted bit by
+// bit, 29 us with 8 warps of 32, 23 us by histograms).
 template <int WARPS, int PER>
 __global__ void __launch_bounds__(WARPS * 32, WARPS == 8 ? 4 : 1)
 select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_blocks, int keep, int recent, int sinks,
@@ -58,8 +61,10 @@ select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_bloc
               int32_t *__restrict__ err)
 {
     constexpr int kThreadsHere = WARPS * 32;
-    __shared__ int sums[2][32], tie_sums[32], gathered;
-    __shared__ uint32_t few[kThreadsHere];
+    constexpr int kPerThread = kBins / kThreadsHere;  // bins a thread
+    __shared__ int sums[32], tie_sums[32], gathered, bins[kBins];
+    __shared__ uint32_t few[kThreadsHere], least[32], greatest[32];
+    __shared__ int3 found;
     const int g = blockIdx.x, b = blockIdx.y;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     grid_dependency_wait();
@@ -112,54 +117,83 @@ select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_bloc
     // kept: keys above `bar`, and the first `ties` tokens of that key
     uint32_t bar = kNone;
     int ties = 0;
-    if (L > keep) {
-        int above = 0, reach = L;  // keys above those that begin with bar's bits; keys not below bar
-        int bit = 31, buf = 0;
-        const auto total_of = [&](int c) {
-            c = __reduce_add_sync(kFull, c);
-            if (lane == 0)
-                sums[buf][warp] = c;
-            __syncthreads();
-            const int total = __reduce_add_sync(kFull, lane < WARPS ? sums[buf][lane] : 0);
-            buf ^= 1;
-            return total;
-        };
-        const auto settle = [&](uint32_t with, int total) {
-            if (total >= keep) {
-                bar = with;
-                reach = total;
-            } else {
-                above = total;
+    int want = keep - sinks - recent;  // of the keys up for choice that are left, how many are kept
+    if (L > keep && want == 0) {
+        bar = kStays - 1;
+    } else if (L > keep) {
+        uint32_t lo = kStays, hi = kNone;
+        each([&](int, uint32_t k) {
+            if (k != kNone && k != kStays) {
+                lo = min(lo, k);
+                hi = max(hi, k);
             }
-        };
-        for (; bit >= 0 && reach > keep && reach - above > kThreadsHere; --bit) {
-            const uint32_t with = bar | 1u << bit;
-            int c = 0;
-            each([&](int, uint32_t k) { c += k >= with; });
-            settle(with, total_of(c));
+        });
+        lo = __reduce_min_sync(kFull, lo);
+        hi = __reduce_max_sync(kFull, hi);
+        if (lane == 0) {
+            least[warp] = lo;
+            greatest[warp] = hi;
         }
-        if (bit >= 0 && reach > keep) {
+        __syncthreads();
+        lo = __reduce_min_sync(kFull, lane < WARPS ? least[lane] : kStays);
+        hi = __reduce_max_sync(kFull, lane < WARPS ? greatest[lane] : kNone);
+        int left = L - sinks - recent;  // keys in lo .. hi; more than `want`, and `want` is positive
+        const auto narrow = [&](const auto &each_key) {
+            const int shift = max(22 - __clz(hi - lo), 0);  // hi - lo in ten bits
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i)
+                bins[tid * kPerThread + i] = 0;
+            __syncthreads();
+            each_key([&](int, uint32_t k) {
+                if (k - lo <= hi - lo)
+                    atomicAdd(&bins[(k - lo) >> shift], 1);
+            });
+            __syncthreads();
+            int own[kPerThread], from = 0;  // this thread's bins; keys in them and in all above them
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) {
+                own[i] = bins[tid * kPerThread + i];
+                from += own[i];
+            }
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_down_sync(kFull, from, off);
+                if (lane + off < 32)
+                    from += y;
+            }
+            if (lane == 0)
+                sums[warp] = from;
+            __syncthreads();
+            from += __reduce_add_sync(kFull, lane > warp && lane < WARPS ? sums[lane] : 0);
+#pragma unroll
+            for (int i = 0; i < kPerThread; ++i) {
+                if (from >= want && from - own[i] < want)
+                    found = make_int3(tid * kPerThread + i, from - own[i], own[i]);
+                from -= own[i];
+            }
+            __syncthreads();
+            lo += (uint32_t)found.x << shift;
+            hi = min(hi, lo + ((1u << shift) - 1));
+            want -= found.y;
+            left = found.z;
+        };
+        while (lo != hi && left != want && left > kThreadsHere)
+            narrow(each);
+        if (lo != hi && left != want) {
             if (tid == 0)
                 gathered = 0;
             __syncthreads();
-            const int free_bits = bit + 1;
             each([&](int, uint32_t k) {
-                if (k != kNone && (free_bits == 32 || (k >> free_bits) == (bar >> free_bits)))
+                if (k - lo <= hi - lo)
                     few[atomicAdd(&gathered, 1)] = k;
             });
             __syncthreads();
             const uint32_t mine = tid < gathered ? few[tid] : kNone;
-            const int beyond = above;
-            for (; bit >= 0 && reach > keep; --bit) {
-                const uint32_t with = bar | 1u << bit;
-                settle(with, beyond + total_of(mine >= with));
-            }
+            while (lo != hi && left != want)
+                narrow([&](const auto &f) { f(0, mine); });
         }
-        ties = keep - above;
-        if (reach == keep) {  // every key from bar on is kept
-            bar -= 1;
-            ties = 0;
-        }
+        bar = left == want ? lo - 1 : lo;  // (a range that is kept whole, or one key)
+        ties = left == want ? 0 : want;
         __syncthreads();
     }
     int sure = 0, tied = 0;  // of this thread, then of the warps before
@@ -170,11 +204,11 @@ select_kernel(const int32_t *__restrict__ seq_lens, int src_blocks, int dst_bloc
     sure = __reduce_add_sync(kFull, sure);
     tied = __reduce_add_sync(kFull, tied);
     if (lane == 0) {
-        sums[0][warp] = sure;
+        sums[warp] = sure;
         tie_sums[warp] = tied;
     }
     __syncthreads();
-    sure = __reduce_add_sync(kFull, lane < warp ? sums[0][lane] : 0);
+    sure = __reduce_add_sync(kFull, lane < warp ? sums[lane] : 0);
     tied = __reduce_add_sync(kFull, lane < warp ? tie_sums[lane] : 0);
     const uint32_t lower = (1u << lane) - 1;
     each([&](int i, uint32_t k) {
