@@ -132,25 +132,27 @@ def _ptr(x):
     return x.data_ptr()
 
 
-_torch = None
+_raw_stream = _raw_device = None
 
 
 def _stream(stream):
     if stream is None:
-        global _torch
-        if _torch is None:
-            import torch
-
-            _torch = torch
         # the raw handle of torch.cuda.current_stream(), without making its Stream object where
         # torch can (a few microseconds of every call)
-        raw = getattr(_torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is None or not _torch.cuda.is_initialized():
-            return _torch.cuda.current_stream().cuda_stream
-        return raw(_torch._C._cuda_getDevice())
+        return _raw_stream(_raw_device()) if _raw_stream is not None else _first_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _first_stream():
+    global _raw_stream, _raw_device
+    import torch
+
+    stream = torch.cuda.current_stream().cuda_stream  # (initialises CUDA)
+    _raw_device = getattr(torch._C, "_cuda_getDevice", None)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) if _raw_device is not None else None
+    return stream
 
 
 def _check(status: int, what: str) -> int:
@@ -585,14 +587,18 @@ EXPORTED_PROBE = ("pkv_probe_read_ldg", "pkv_probe_read_bulk")
 _lib_long = lib
 
 
+_bound = None
+
+
 def lib():  # noqa: F811 -- extends the loader with the probe signatures
-    L = _lib_long()
-    if not getattr(L, "_pkv_probe_bound", False):
+    global _bound
+    if _bound is None:
+        L = _lib_long()
         for name in EXPORTED_PROBE:
             getattr(L, name).argtypes = [_vp, ctypes.c_size_t, _vp, _i32, _vp]
             getattr(L, name).restype = ctypes.c_int
-        L._pkv_probe_bound = True
-    return L
+        _bound = L
+    return _bound
 
 
 def pkv_probe_read_ldg(buf, nbytes: int, sink, ctas_per_sm: int = 2, stream=None) -> None:
