@@ -9,9 +9,11 @@
 // managed by offsets; the caller allocates that slab, the library manages ids.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
+#include <thread>
 
 #include "pkv_internal.h"
 
@@ -237,17 +239,38 @@ int pkv_rope_table_init(double theta, int max_pos, int half_dim, float *dev_cos_
         return PKV_ERR_INVALID_ARG;
     }
     const double dim = 2.0 * half_dim;
-    for (int p = 0; p < max_pos; ++p) {
-        for (int i = 0; i < half_dim; ++i) {
-            const double angle = (double)p * std::pow(theta, -2.0 * i / dim);
-            const double c = std::cos(angle), s = std::sin(angle);
-            float *e = &table[((size_t)p * half_dim + i) * 4];
-            e[0] = (float)c;                      // nearest FP32
-            e[1] = (float)s;
-            e[2] = (float)(c - (double)e[0]);     // the rest (exact in FP64), rounded to FP32
-            e[3] = (float)(s - (double)e[1]);
+    double freq[PKV_HEAD_DIM / 2];
+    for (int i = 0; i < half_dim; ++i)
+        freq[i] = std::pow(theta, -2.0 * i / dim);
+    const auto fill = [&](int p0, int p1) {
+        for (int p = p0; p < p1; ++p) {
+            for (int i = 0; i < half_dim; ++i) {
+                const double angle = (double)p * freq[i];
+                const double c = std::cos(angle), s = std::sin(angle);
+                float *e = &table[((size_t)p * half_dim + i) * 4];
+                e[0] = (float)c;                      // nearest FP32
+                e[1] = (float)s;
+                e[2] = (float)(c - (double)e[0]);     // the rest (exact in FP64), rounded to FP32
+                e[3] = (float)(s - (double)e[1]);
+            }
         }
+    };
+    // long tables on several cores: 65536 positions took 73 ms on one
+    const int threads = (int)std::max(1u, std::min({(unsigned)max_pos / 2048, std::thread::hardware_concurrency(), 16u}));
+    const int64_t each = threads > 1 ? ((int64_t)max_pos + threads - 1) / threads : max_pos;
+    std::vector<std::thread> others;
+    int64_t begun = each;  // positions that this thread or another one fills
+    try {
+        others.reserve(threads);
+        for (; begun < max_pos; begun += each)
+            others.emplace_back(fill, (int)begun, (int)std::min<int64_t>(begun + each, max_pos));
+    } catch (...) {  // no more threads: the rest is filled here
     }
+    fill(0, (int)each);
+    if (begun < max_pos)
+        fill((int)begun, max_pos);
+    for (std::thread &t : others)
+        t.join();
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     cudaError_t e = cudaMemcpyAsync(dev_cos_sin, table.data(), table.size() * sizeof(float),
                                     cudaMemcpyHostToDevice, s);

@@ -580,3 +580,16 @@ def test_append_at(kv, with_q):
     assert pkv.pkv_check_device_error(err) == (pkv.PKV_ERR_DEVICE_BOUNDS, pkv.PKV_DEVERR_LENGTH)
     assert torch.equal(start, c.slab) and torch.equal(q1, q2)
     c.close()
+
+
+@pytest.mark.parametrize("max_pos", [4095, 20011])
+def test_long_rope_tables(max_pos):
+    """Filled by several threads: every row is there.  An angle p f of a frequency f <= 1, both
+    rounded to 64 bits (the power to a unit in the last place), is p 2^-51 off at most between the
+    two sides; the factors are held to 2^-48."""
+    got = pkv.rope_table(max_pos, "cuda", lh.THETA).cpu().numpy().reshape(max_pos, D // 2, 4).astype(np.float64)
+    p, i = np.arange(max_pos)[:, None], np.arange(D // 2)[None, :]
+    angle = p * float(lh.THETA) ** (-2.0 * i / D)
+    tol = max_pos * 2.0 ** -51 + 2.0 ** -47
+    assert (np.abs(got[..., 0] + got[..., 2] - np.cos(angle)) <= tol).all()
+    assert (np.abs(got[..., 1] + got[..., 3] - np.sin(angle)) <= tol).all()
