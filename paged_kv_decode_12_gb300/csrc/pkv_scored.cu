@@ -197,15 +197,15 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     a.out = out;
     a.err = dev_err_flag;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    // Largest units first where there are several waves of them and the library chooses: 64
-    // sequences up to 16384 tokens (FP8) 85 us instead of 93; with up to 2048 tokens, two waves,
-    // the order costs more than it gives (18.8 us instead of 17.2).
-    if (pages_per_chunk == 0 && B <= kMaxSortedBatch && (int64_t)B * kHkv * ((max_blocks + ppc - 1) / ppc) > 4 * 152 * 6)
+    // Largest units first where there are more than two waves of them and the library chooses: 64
+    // sequences up to 16384 tokens (FP8) 83 us instead of 99, up to 2048 29 instead of 31, but 32 up
+    // to 4096 27.7 instead of 27.3, 8 up to 8192 30 instead of 27.
+    if (pages_per_chunk == 0 && B <= kMaxSortedBatch && (int64_t)B * kHkv * ((max_blocks + ppc - 1) / ppc) > 2 * 152 * 6)
         options |= PKV_STEP_SORTED;
-    // in the same launch: rows of 4096 tokens at most, or of 16384 where many units finish at
-    // different times (1 sequence of 1024 tokens 5.6 us instead of 7.0, 64 up to 16384 89 instead of
-    // 93; but 8 up to 8192 20 instead of 18)
-    if (sel.tokens <= (B * kHkv >= 3 * 152 ? 16384 : 4096))
+    // in the same launch: rows of 2048 tokens at most, or of 16384 where many units finish at
+    // different times (1 sequence of 1024 tokens 5.5 us instead of 6.3, 64 up to 2048 14.8 instead of
+    // 16.9; but 8 up to 4096 20 instead of 18, 8 up to 8192 34 instead of 27)
+    if (sel.tokens <= (B * kHkv >= 3 * 152 ? 16384 : 2048))
         return launch_fused<false>(pool, a, sel, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
     const ScoredPages<false> apart = {sel.scores, sel.lse, sel.tokens, acc, acc_out, acc_stride};
     if (const int st = launch_fused<false>(pool, a, apart, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
