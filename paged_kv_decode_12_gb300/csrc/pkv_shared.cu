@@ -16,8 +16,8 @@
 // little; 64 exponentials a row and half tile take 512 of the 1000 clocks it lasts, and the rest
 // is the way from one wait to the next.  Two row tiles a CTA fill each other's gaps (256 sequences
 // behind 32768 tokens: 90 us, 760 TFLOP/s).
-// Tried: 16 softmax warps with half a row each, in two forms (149 and 101 us where 8 warps took
-// 96), starting the second row tile half a step later (no change), 8 converter warps for FP8 with
+// Tried: 16 softmax warps, with half a row each or as four sets of their own (149 us where 8 took
+// 101), starting the second row tile half a step later (no change), 8 converter warps for FP8 with
 // registers moved to the softmax warps (30.3 us where 4 took 30.8).
 #include <cmath>
 
@@ -548,38 +548,44 @@ __device__ __forceinline__ float max_score(uint32_t ts, int k, const Scale &sc, 
 // every score 2^8 above it, as narrower types need, made most half tiles of 32 rows rescale O.)
 constexpr float kMostWeight = 18446744073709551616.f;
 
+// An item's first half tile: the row's maximum.  (Not inlined: the loop would pay for its
+// registers; 256 sequences behind 32768 tokens 94 us instead of 91.)
+template <class Scale>
+__device__ __noinline__ float first_reference(uint32_t ts, Scale sc, int pages)
+{
+    return fmaxf(max_score<true>(ts, 0, sc, pages), max_score<true>(ts, 1, sc, pages));
+}
+
 // Half a key tile's scores of one query row become weights, in place: P is the first half of
 // S's columns.  MASK: only the first `pages` pages of the tile count.  Returns false if a wait
 // gave up.
 template <bool MASK, class Scale>
 __device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, const Scale &sc, int pages, int before,
-                                             uint64_t *o_step, bool first, volatile int *stop, float &m, float &l)
+                                             uint64_t *o_step, volatile int *stop, float &m, float &l)
 {
     uint32_t p0[16], p1[16];
     float s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
-    const bool move = first || !(s < kMostWeight);
+    const bool move = !(s < kMostWeight);
     if (__any_sync(kFull, move)) {
         const float top = fmaxf(max_score<MASK>(ts, 0, sc, pages), max_score<MASK>(ts, 1, sc, pages));
-        const float mn = move ? (first ? top : fmaxf(top, m)) : m;
-        const float f = first ? 0.f : ex2_approx(m - mn);  // 1 where the reference stays
+        const float mn = move ? fmaxf(top, m) : m;
+        const float f = ex2_approx(m - mn);  // 1 where the reference stays
         m = mn;
         l *= f;
         s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
         // Once the product before this one is done, nothing else touches O.  (These scores came
         // after the product before that, so the wait is one phase behind at most.)
-        if (!first) {
-            if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
-                return false;
-            tc::fence_after();
+        if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
+            return false;
+        tc::fence_after();
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t o[16];
-                tc::ld16(to + k * 16, o);
+        for (int k = 0; k < 4; ++k) {
+            uint32_t o[16];
+            tc::ld16(to + k * 16, o);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tc::st16(to + k * 16, o);
-            }
+            for (int i = 0; i < 16; ++i)
+                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tc::st16(to + k * 16, o);
         }
     }
     l += s;
@@ -662,14 +668,15 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
                 }
                 tc::fence_after();
                 const int before = 2 * (done + j) + hf;  // products of this row tile so far
-                const bool first = j == 0 && hf == 0;
                 const int seq = loaded + x.order(s, j), st = seq % kStages;
                 const auto half = [&](const auto &sc) {
+                    if (j == 0 && hf == 0)
+                        m = first_reference(ts, sc, pages);
                     return pages >= kTilePages
-                               ? softmax_half<false>(ts + hf * kHalf, to, sc, kTilePages, before, &bars.o_step[s], first,
-                                                     &bars.stop, m, l)
-                               : softmax_half<true>(ts + hf * kHalf, to, sc, pages, before, &bars.o_step[s], first,
-                                                    &bars.stop, m, l);
+                               ? softmax_half<false>(ts + hf * kHalf, to, sc, kTilePages, before, &bars.o_step[s], &bars.stop,
+                                                     m, l)
+                               : softmax_half<true>(ts + hf * kHalf, to, sc, pages, before, &bars.o_step[s], &bars.stop, m,
+                                                    l);
                 };
                 bool go;
                 if constexpr (FP8) {
