@@ -470,6 +470,11 @@ def acc_of(rng, shape, kind):
         x[rng.random(shape) < 0.1] = -np.inf
         x[rng.random(shape) < 0.1] = 1e-42       # subnormal
         return x
+    if kind == "near":                           # neighbours of 1 between two far values
+        x = (1 + rng.integers(0, 5000, shape) * 2.0 ** -23).astype(np.float32)
+        x[rng.random(shape) < 0.001] = 3e38
+        x[rng.random(shape) < 0.001] = -3e38
+        return x
     return np.exp(2 * rng.standard_normal(shape)).astype(np.float32)
 
 
@@ -481,6 +486,11 @@ EVICTS = [
     ([300, 5], 299, 5, 5, "real"),
     # rows longer than the 8192 and 32768 weights that are held in registers
     ([9000, 8193, 20], 3000, 100, 4, "real"), ([33000, 32769], 5000, 500, 3, "ties"), ([16384], 4096, 0, 0, "odd"),
+    ([40000, 33001], 6000, 100, 2, "real"),
+    # crowded histograms: several steps over all weights
+    ([3000, 700, 257], 600, 20, 3, "near"), ([20000], 7000, 0, 1, "near"), ([36000], 1000, 10, 0, "near"),
+    # nothing up for choice; all but one
+    ([5000, 70], 64, 60, 4, "real"), ([5000], 4999, 7, 2, "near"),
 ]
 
 
