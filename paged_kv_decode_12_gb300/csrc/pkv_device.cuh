@@ -179,6 +179,11 @@ struct TokenSet {
     __device__ __forceinline__ bool all() const { return bits == (1u << kPage) - 1; }
 };
 
+struct EveryToken {
+    __device__ __forceinline__ bool operator()(int) const { return true; }
+    __device__ __forceinline__ bool all() const { return true; }
+};
+
 // What becomes of a page's scores besides the softmax: nothing.
 struct NoScores {
     __device__ __forceinline__ void operator()(int, int, float, float) const {}
@@ -526,6 +531,20 @@ __device__ __forceinline__ void update_page(SimtWarp &w, const uint8_t *stage, F
     w.page(stage, keep);
 }
 
+// Page j of a list through a policy.  With kWhole the pages that are attended to as a whole, nearly
+// all, have code of their own without a mask.
+template <class Warp, class List, class Emit>
+__device__ __forceinline__ void visit_page(Warp &w, const uint8_t *stage, const List &list, int j, const Emit &emit)
+{
+    if constexpr (List::kWhole) {
+        if (list.whole(j)) {
+            update_page(w, stage, EveryToken{}, emit);
+            return;
+        }
+    }
+    update_page(w, stage, list.tokens(j), emit);
+}
+
 // ------------------------------------------------------------------ page streaming
 
 // Shared-memory carve-up of a decode CTA: STAGES 4 KiB stages per warp (1024-byte
@@ -626,7 +645,7 @@ __device__ __forceinline__ bool consume_list(const CUtensorMap *tmap, uint8_t *m
         const int j = list.logical(j0 + warp + k * kWarps);
         uint8_t *stage = my_stages + s * kStageBytes;
         patch(stage, j);
-        update_page(w, stage, list.tokens(j), emit_of(j));
+        visit_page(w, stage, list, j, emit_of(j));
         __syncwarp();
         if (k + STAGES < nmine) {
             const int pk = __shfl_sync(kFull, my_page, k + STAGES);
@@ -647,6 +666,7 @@ __device__ __forceinline__ bool consume_list(const CUtensorMap *tmap, uint8_t *m
 
 // The list of a sequence of length L whose every page is visited.
 struct WholeSequence {
+    static constexpr bool kWhole = false;
     int L;
     __device__ __forceinline__ bool ok() const { return true; }
     __device__ __forceinline__ int count() const { return (L + kPage - 1) / kPage; }

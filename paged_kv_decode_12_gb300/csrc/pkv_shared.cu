@@ -64,6 +64,7 @@ struct OwnPages {
     Groups gr;
 
     struct List {
+        static constexpr bool kWhole = false;
         int L, prefix, slots;  // prefix < 0: the sequence is in no valid group
         __device__ __forceinline__ bool ok() const { return prefix >= 0 && (int64_t)prefix * kPage <= L; }
         __device__ __forceinline__ int count() const { return (L + kPage - 1) / kPage - prefix; }

@@ -28,6 +28,9 @@ using namespace dev;
 //   logical(i)   the sequence's page that entry i is, increasing in i
 //   before(j)    entries whose page is below j
 //   tokens(j)    the tokens of page j attended to
+//   kWhole       pages attended to as a whole go through code without a mask; whole(j) says which
+//                (256 windows of 4112 FP8 tokens 181 us instead of 187; no faster for whole
+//                sequences, whose masks are one comparison)
 //   first_slot() partials of the sequence that another kernel writes: they are merged
 //                before the units' own
 // and says
@@ -861,7 +864,7 @@ __device__ __forceinline__ void decode_unit_fp8(const CUtensorMap &tmap, const S
                 put_new_token_fp8(stage, slot, sm.new_codes, sm.new_scales, lane);
                 __syncwarp();
             }
-            w.page(stage, list.tokens(j), emit_of(j));
+            visit_page(w, stage, list, j, emit_of(j));
             __syncwarp();
             if (k + STAGES < nmine) {
                 const int pk = __shfl_sync(kFull, my_page, k + STAGES);

@@ -21,12 +21,18 @@ struct WindowPages {
     int window, sinks;
 
     struct List {
+        static constexpr bool kWhole = true;
         int L, cut, head;  // tokens below head and from cut on are attended to (head <= cut)
         int nhead, gap;    // pages of the first tokens; pages left out behind them
         __device__ __forceinline__ bool ok() const { return true; }
         __device__ __forceinline__ int count() const { return (L + kPage - 1) / kPage - gap; }
         __device__ __forceinline__ int logical(int i) const { return i < nhead ? i : i + gap; }
         __device__ __forceinline__ int before(int j) const { return j <= nhead ? j : max(nhead, j - gap); }
+        __device__ __forceinline__ bool whole(int j) const
+        {
+            const int t0 = j * kPage;
+            return t0 + kPage <= head || (t0 >= cut && t0 + kPage <= L);
+        }
         __device__ __forceinline__ TokenSet tokens(int j) const
         {
             const int t0 = j * kPage;
