@@ -501,10 +501,11 @@ struct RowScales {
 
 // 32 scores of one query row (columns 32 k ..) as weights 2^(S c - m): their sum, and the weights
 // in pairs rounded to BF16 (half a step, 2^-9) for the second product: what the matrix instruction
-// takes beside BF16 values.  The sum is of the weights before that rounding; summing them behind
-// it would take most of the error out where few weights make the sum (0.0017 instead of 0.0023 over
-// 256 sequences behind 32768 tokens), but takes 108 us instead of 92.  MASK: columns of pages from `pages` on weigh
-// nothing.  Four chains of sums, so that no chain's latency is the time of the whole.
+// takes beside BF16 values.  The sum is of the weights before that rounding; summing them behind it
+// would take out most of the error where few weights make the sum (0.0017 instead of 0.0023 over
+// 256 sequences behind 32768 tokens), but took 108 us instead of 92.  MASK: columns of pages from
+// `pages` on weigh nothing.  Four chains of sums, so that no chain's latency is the time of the
+// whole.
 template <bool MASK, class Scale>
 __device__ __forceinline__ float make_weights(uint32_t ts, int k, const Scale &sc, int pages, float m, uint32_t (&pk)[16])
 {
