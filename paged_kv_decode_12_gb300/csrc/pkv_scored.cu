@@ -201,7 +201,8 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     // chooses: 64 sequences up to 16384 tokens (FP8) 83 us instead of 99, 32 up to 16384 69 instead
     // of 75, 160 up to 2048 34 instead of 42; but 64 up to 4096 43 instead of 41, and with units of
     // 64 pages or less 256 up to 1024 39 instead of 36, 8 up to 8192 30 instead of 27.
-    if (pages_per_chunk == 0 && B <= kMaxSortedBatch && ppc > 64 && (int64_t)B * kHkv * ((max_blocks + ppc - 1) / ppc) > 152 * 6)
+    if (pages_per_chunk == 0 && B <= kMaxSortedBatch && ppc > 64 &&
+        (int64_t)B * kHkv * ((max_blocks + ppc - 1) / ppc) > 152 * 6)
         options |= PKV_STEP_SORTED;
     // in the same launch: rows of 2048 tokens at most, or of 16384 where many units finish at
     // different times (1 sequence of 1024 tokens 5.5 us instead of 6.3, 64 up to 2048 14.8 instead of

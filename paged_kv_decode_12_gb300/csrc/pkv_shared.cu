@@ -810,9 +810,10 @@ constexpr int kSms = 152;
 // 1.05 us, FP8 pages, which are converted, 1.85 us): an item costs 3.3 (1) besides its own, and
 // every chunk 0.42 (0.12) of merging and 0.5 (0.1) more for every 256 sequences.  Of several
 // groups the others are taken to be half as long as the longest.  Measured with chunks of 8 / 16 /
-// 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 336 / 224 / 155 / 117 / 101 / 90; 64 sequences, 128 pages 22 / 19 / 16 / 18 / 27; 16 sequences, 512 pages 24 / 17
-// / 14 / 16 / 25 / 61, FP8 26 / 19 / 20 / 23 / 38 / 100; 200 sequences in 3 groups, 500 FP8 pages
-// 74 / 54 / 44 / 39 / 47; 4 sequences, 32 pages 7.2 / 8.4 / 9.5.
+// 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 322 / 208 / 148 / 114 / 99 / 91; 64
+// sequences, 128 pages 21 / 19 / 16 / 19 / 27; 16 sequences, 512 pages 24 / 17 / 13 / 16 / 24 / 61, FP8
+// 26 / 18 / 19 / 23 / 37 / 100; 200 sequences in 3 groups, 500 FP8 pages 74 / 54 / 44 / 39 / 47; 4
+// sequences, 32 pages 7.1 / 8.1 / 9.1.
 int default_prefix_chunk(int B, int groups, int max_prefix, bool fp8)
 {
     const int tiles = (max_prefix + kTilePages - 1) / kTilePages;
