@@ -102,7 +102,8 @@ constexpr int kOutRow = 32 * 4 + 16;                           // half an output
 constexpr int kOutSize = 2 * kRowTile * kOutRow;               // 36 KiB: of every row
 constexpr int kScales = 2 * kTilePages * kPage;                // row scales of a tile: K's, then V's
 constexpr int kCols = 512;                                     // tensor memory, all of it
-constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;        // + 128 / 64 / 32 for the second tile
+constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColL = 448;  // + 128 / 64 / 32 / 16 for the second tile
+constexpr int kOnesSize = 16 * 128;                            // BF16 pages: 16 rows of ones, for the sums
 
 constexpr int kStages = 4;  // (FP8: three were 12 % slower, five or a third raw unit no faster)
 constexpr int prefix_threads(bool fp8) { return (kConverter + (fp8 ? kConverters : 0)) * 32; }
@@ -397,9 +398,9 @@ __device__ __forceinline__ void issue_scores(uint32_t k, uint32_t s, uint32_t q,
     __syncwarp();
 }
 
-template <bool FIRST>
-__device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p, uint64_t *free_stage, int uses,
-                                             uint64_t *done, uint64_t *last)
+template <bool FIRST, bool SUM>
+__device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p, uint32_t ones, uint32_t l,
+                                             uint64_t *free_stage, int uses, uint64_t *done, uint64_t *last)
 {
     // O[128 x 64] += P V: 16 columns of P are 8 slots of two pages
     constexpr uint32_t kIdesc = tc::instr_desc(64, true, true), kHi = tc::smem_desc_hi(kStageBytes);
@@ -409,6 +410,14 @@ __device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p,
 #pragma unroll
         for (int i = 1; i < kHalf / 16; ++i)
             tc::mma_ts<true>(o, p + i * 8, lo + i * (2 * kStageBytes / 16), kHi, kIdesc);
+        if constexpr (SUM) {  // L[128 x 16] += P 1
+            constexpr uint32_t kOnes = tc::instr_desc(16, true, false), kOnesHi = tc::smem_desc_hi(1024);
+            const uint32_t one = tc::smem_desc_lo(ones, 1024);
+            tc::mma_ts<!FIRST>(l, p, one, kOnesHi, kOnes);
+#pragma unroll
+            for (int i = 1; i < kHalf / 16; ++i)
+                tc::mma_ts<true>(l, p + i * 8, one, kOnesHi, kOnes);
+        }
         tc::commit(done);
         if (last)
             tc::commit(last);
@@ -423,9 +432,11 @@ __device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p,
 
 // Each row tile has an issuer warp of its own, so that one's waits pass while the other's
 // products run: the tensor cores take only a few instructions ahead.
-__device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stages, PrefixBars &bars, uint32_t tmem, int s)
+template <bool FP8>
+__device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stages, const uint8_t *ones, PrefixBars &bars,
+                                              uint32_t tmem, int s)
 {
-    const uint32_t base = smem_addr(stages);
+    const uint32_t base = smem_addr(stages), one = smem_addr(ones), tl = tmem + kColL + s * 16;
     const uint32_t ts = tmem + kColS + s * 128, to = tmem + kColO + s * 64, tq = tmem + kColQ + s * 32;
     Item x;
     int loaded = 0;  // key tiles of earlier items
@@ -451,9 +462,9 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
         uint64_t *last = h == 1 && j + 1 == nt ? &bars.o_full[s] : nullptr;
         const int uses = x.shared ? 1 : 2;  // a stage is free after two arrivals
         if (j == 0 && h == 0)
-            issue_output<true>(v, to, p, empty, uses, &bars.o_step[s], last);
+            issue_output<true, !FP8>(v, to, p, one, tl, empty, uses, &bars.o_step[s], last);
         else
-            issue_output<false>(v, to, p, empty, uses, &bars.o_step[s], last);
+            issue_output<false, !FP8>(v, to, p, one, tl, empty, uses, &bars.o_step[s], last);
         return true;
     };
     const Items items(a.gr);
@@ -488,12 +499,14 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
 // What turns 64 scores into exponents and weights into the second product's operand: one
 // factor, or (FP8) a factor and a scale for every column.
 struct OneFactor {
+    static constexpr bool kSum = false;  // the sum is made by the matrix instruction
     float c;
     __device__ __forceinline__ float2 factor(int) const { return make_float2(c, c); }
     __device__ __forceinline__ float2 weight(int, float2 e) const { return e; }
 };
 
 struct RowScales {
+    static constexpr bool kSum = true;
     const float2 *k, *v;  // 32 pairs of columns
     __device__ __forceinline__ float2 factor(int i) const { return k[i]; }
     __device__ __forceinline__ float2 weight(int i, float2 e) const { return tc::mul2(e, v[i]); }
@@ -501,11 +514,14 @@ struct RowScales {
 
 // 32 scores of one query row (columns 32 k ..) as weights 2^(S c - m): their sum, and the weights
 // in pairs rounded to BF16 (half a step, 2^-9) for the second product: what the matrix instruction
-// takes beside BF16 values.  The sum is of the weights before that rounding; summing them behind it
-// would take out most of the error where few weights make the sum (0.0017 instead of 0.0023 over
-// 256 sequences behind 32768 tokens), but took 108 us instead of 92.  MASK: columns of pages from
-// `pages` on weigh nothing.  Four chains of sums, so that no chain's latency is the time of the
-// whole.
+// takes beside BF16 values.  MASK: columns of pages from `pages` on weigh nothing.  Four chains of
+// sums, so that no chain's latency is the time of the whole.
+//
+// BF16 pages: the softmax's sum is of the weights as rounded, made by the matrix instruction too (L
+// += P 1, 16 equal columns), so that the quotient has none of their rounding where few weights make
+// it.  256 sequences behind 32768 tokens: error 0.0017 in 96 us, where the sum of the unrounded
+// weights, which this function returns, gives 0.0023 in 92, and unpacking the rounded ones took 108.
+// FP8 pages: what is rounded is the weight times V's row scale, so the sum stays the unrounded one.
 template <bool MASK, class Scale>
 __device__ __forceinline__ float make_weights(uint32_t ts, int k, const Scale &sc, int pages, float m, uint32_t (&pk)[16])
 {
@@ -565,7 +581,7 @@ __device__ __noinline__ float first_reference(uint32_t ts, Scale sc, int pages)
 // S's columns.  MASK: only the first `pages` pages of the tile count.  Returns false if a wait
 // gave up.
 template <bool MASK, class Scale>
-__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, const Scale &sc, int pages, int before,
+__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, uint32_t tl, const Scale &sc, int pages, int before,
                                              uint64_t *o_step, volatile int *stop, float &m, float &l)
 {
     uint32_t p0[16], p1[16];
@@ -592,6 +608,14 @@ __device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, const Sca
                 o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
             tc::st16(to + k * 16, o);
         }
+        if constexpr (!Scale::kSum) {
+            uint32_t x[16];
+            tc::ld16(tl, x);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            tc::st16(tl, x);
+        }
     }
     l += s;
     tc::st16(ts, p0);  // columns 2i, 2i + 1 of S are column i of P
@@ -608,7 +632,7 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
     const int r = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + kColS + s * 128, to = tmem + lanes + kColO + s * 64,
-                   tq = tmem + lanes + kColQ + s * 32;
+                   tq = tmem + lanes + kColQ + s * 32, tl = tmem + lanes + kColL + s * 16;
     const Items items(a.gr);
     int it = blockIdx.x;
     int loaded = 0, done = 0, used = 0;
@@ -678,9 +702,9 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
                     if (j == 0 && hf == 0)
                         m = first_reference(ts, sc, pages);
                     return pages >= kTilePages
-                               ? softmax_half<false>(ts + hf * kHalf, to, sc, kTilePages, before, &bars.o_step[s], &bars.stop,
+                               ? softmax_half<false>(ts + hf * kHalf, to, tl, sc, kTilePages, before, &bars.o_step[s], &bars.stop,
                                                      m, l)
-                               : softmax_half<true>(ts + hf * kHalf, to, sc, pages, before, &bars.o_step[s], &bars.stop, m,
+                               : softmax_half<true>(ts + hf * kHalf, to, tl, sc, pages, before, &bars.o_step[s], &bars.stop, m,
                                                     l);
                 };
                 bool go;
@@ -713,6 +737,11 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
         tc::fence_after();
         // The chunk's partial; with a bad page id it is empty.  A thread's row goes through shared
         // memory, so that the warp writes whole lines: 128 bytes of four rows at once.
+        if constexpr (!FP8) {
+            uint32_t sums[16];
+            tc::ld16(tl, sums);
+            l = __uint_as_float(sums[0]);
+        }
         const int ns = x.ns[s] - (warp & 3) * 8;  // of the warp's 8 sequences, those there are
         const size_t first = ((size_t)(x.s0[s] + (warp & 3) * 8) * kHq + x.g * kGroup) * a.max_chunks + x.chunk[s];
         const size_t per_seq = (size_t)kHq * a.max_chunks;
@@ -755,8 +784,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
     // (an offset, not a rounded address: the compiler keeps shared-memory instructions)
     uint8_t *stages = smem_raw + (-smem_addr(smem_raw) & 1023u);
     uint8_t *outs = stages + kStages * kStageSize;
-    uint8_t *raws = outs + kOutSize;
-    PrefixBars &bars = *reinterpret_cast<PrefixBars *>(raws + (FP8 ? kRaws * kRawSize : 0));
+    uint8_t *raws = outs + kOutSize;  // (BF16 pages: the ones)
+    PrefixBars &bars = *reinterpret_cast<PrefixBars *>(raws + (FP8 ? kRaws * kRawSize : kOnesSize));
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
@@ -782,6 +811,11 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
     }
     if (warp == kIssuer)
         tc::alloc<kCols>(&bars.tmem);
+    if (!FP8) {
+        for (int i = threadIdx.x; i < kOnesSize / 4; i += prefix_threads(FP8))
+            reinterpret_cast<uint32_t *>(raws)[i] = 0x3f803f80u;
+        fence_proxy_async_smem();
+    }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -793,7 +827,7 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
     else if (FP8 && warp >= kConverter)
         prefix_converter(a, raws, stages, bars);
     else if (warp >= kIssuer)
-        prefix_issuer(a, stages, bars, tmem, warp - kIssuer);
+        prefix_issuer<FP8>(a, stages, raws, bars, tmem, warp - kIssuer);
     else
         prefix_softmax<FP8>(a, bars, tmem, warp >> 2, outs + warp * (32 * kOutRow));
     __syncthreads();
@@ -868,7 +902,7 @@ int launch_prefix(const pkv_pool *pool, const PrefixArgs &a, int64_t max_items, 
     if (!tmap)
         return PKV_ERR_CUDA;
     constexpr int smem =
-        1024 + kStages * kStageSize + kOutSize + (FP8 ? kRaws * kRawSize : 0) + (int)sizeof(PrefixBars);
+        1024 + kStages * kStageSize + kOutSize + (FP8 ? kRaws * kRawSize : kOnesSize) + (int)sizeof(PrefixBars);
     static PerDeviceOnce attr;
     if (const int st = ensure_smem_attr(attr, prefix_kernel<FP8>, smem); st != PKV_OK)
         return st;

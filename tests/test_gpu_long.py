@@ -247,6 +247,31 @@ def test_shared(kv, case):
 
 
 @pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("scale", [64, 256, 1024])
+@pytest.mark.parametrize("groups", [[(130, [5, 9, 1])], [(40, [3] * 40), (25, [30]), (8, [1, 1])]])
+def test_shared_scores_far_apart(kv, scale, groups):
+    """Long queries: later scores lie hundreds of powers of two above the first ones (at scale 64 some
+    rows' do, at 1024 nearly every row's, several times), so the references of rows move, in some rows
+    of a tile and not in others."""
+    c, bt, view, lens, starts, prefix, rng = shared_case(kv, groups, 220 + scale)
+    q, qf = lh.query(rng, len(lens))
+    q, qf = q * scale, qf * scale                 # a power of two: exact
+    outs = [run_shared(c, bt, lens, starts, prefix, q, *a)[0] for a in ((0, 0), (2, 8), (1, 10000))]
+    moved = 0
+    for b, L in enumerate(lens):
+        K, V = c.rows(view[b], range(int(L)))
+        want, off, _, _ = lh.attend(qf[b], K, V, kv, 2.0 ** -8)
+        for o in outs:
+            close(o[b], want, off, (b, L))
+        n = int(prefix[np.searchsorted(starts, b, side="right") - 1]) * PS
+        s = np.einsum("hd,hnd->hn", qf[b], np.repeat(K, 4, 0))[:, :n] * (lh.SCALE * np.log2(np.e))
+        first = s[:, [t for t in range(min(n, 128)) if t % PS < 8]].max(1)
+        moved += int((s.max(1) > first + 70).sum())
+    assert moved or scale == 64
+    c.close()
+
+
+@pytest.mark.parametrize("kv", KV)
 def test_shared_rows_do_not_depend_on_their_group(kv):
     groups = [(20, [5, 33, 2, 90]), (3, [7]), (0, [40, 1])]
     c, bt, view, lens, starts, prefix, rng = shared_case(kv, groups, 5, extra_blocks=3)
