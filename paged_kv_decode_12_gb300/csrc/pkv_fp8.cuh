@@ -152,7 +152,12 @@ __device__ __forceinline__ void tma_load_unit(void *dst, const CUtensorMap *map,
 //    by this warp, so P'' = p * scale_v / sref <= 1 fits FP16 with its rounding
 //    relative to the unit's own magnitude, and the MMA accumulates straight into
 //    O^T; when a page raises sref, O^T is rescaled with the softmax correction.
-struct Fp8MmaWarp {
+//  * FINE: the second term is held 2^5 up (at most 2^8: half a step of the first is 2^3) and summed
+//    apart, so that query entries down to 2^-15 of their row's largest are exact, where they
+//    otherwise are down to 2^-10.  For weights that are an output of their own, in FP32.
+template <bool FINE>
+struct Fp8MmaWarpOf {
+    static constexpr float kUp = FINE ? 32.f : 1.f;
     uint32_t qt[2][4];  // E4M3 terms of Q' for head gid, dims 16tig..16tig+15 (4 bytes per word)
     float hf[2];        // 2^(e-134) * scale * log2(e) for heads 2tig, 2tig+1 (0 for padding heads)
     float o[4][4];      // O^T accumulators, in units of sref
@@ -196,7 +201,7 @@ struct Fp8MmaWarp {
             for (int h = 0; h < 2; ++h) {
                 const float x0 = qv[4 * j + 2 * h] * norm, x1 = qv[4 * j + 2 * h + 1] * norm;
                 const uint32_t c = e4m3x2_of(x0, x1);
-                const uint32_t r = e4m3x2_of(x0 - e4m3_value(c & 0xffu), x1 - e4m3_value(c >> 8));
+                const uint32_t r = e4m3x2_of((x0 - e4m3_value(c & 0xffu)) * kUp, (x1 - e4m3_value(c >> 8)) * kUp);
                 t1 |= c << (16 * h);
                 t2 |= r << (16 * h);
             }
@@ -229,10 +234,21 @@ struct Fp8MmaWarp {
         {
             const uint4 ka = *reinterpret_cast<const uint4 *>(codes + gid * kD + 16 * tig);
             const uint4 kb = *reinterpret_cast<const uint4 *>(codes + (gid + 8) * kD + 16 * tig);
+            if constexpr (FINE) {
+                float f[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_e4m3(s, ka.x, kb.x, ka.y, kb.y, qt[0][0], qt[0][1]);
+                mma_e4m3(f, ka.x, kb.x, ka.y, kb.y, qt[1][0], qt[1][1]);
+                mma_e4m3(s, ka.z, kb.z, ka.w, kb.w, qt[0][2], qt[0][3]);
+                mma_e4m3(f, ka.z, kb.z, ka.w, kb.w, qt[1][2], qt[1][3]);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                mma_e4m3(s, ka.x, kb.x, ka.y, kb.y, qt[t][0], qt[t][1]);
-                mma_e4m3(s, ka.z, kb.z, ka.w, kb.w, qt[t][2], qt[t][3]);
+                for (int i = 0; i < 4; ++i)
+                    s[i] = fmaf(f[i], 1.f / kUp, s[i]);
+            } else {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    mma_e4m3(s, ka.x, kb.x, ka.y, kb.y, qt[t][0], qt[t][1]);
+                    mma_e4m3(s, ka.z, kb.z, ka.w, kb.w, qt[t][2], qt[t][3]);
+                }
             }
         }
         const float sk0 = scales[gid], sk1 = scales[gid + 8];
@@ -367,6 +383,8 @@ struct Fp8MmaWarp {
         }
     }
 };
+
+using Fp8MmaWarp = Fp8MmaWarpOf<false>;
 
 template <int STAGES>
 struct Fp8Smem {

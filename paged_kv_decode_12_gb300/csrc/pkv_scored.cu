@@ -55,7 +55,8 @@ __device__ __forceinline__ void add_weights(const float4 *scores, float4 n, cons
 
 template <bool INLINE>
 struct ScoredPages {
-    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
+    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false,
+                          kFine = true;
     float *scores;  // [B][8][tokens][4]
     float *lse;     // [B][32] log2 of the sum of 2^score
     int tokens;     // per (sequence, KV head): 16 * max_blocks

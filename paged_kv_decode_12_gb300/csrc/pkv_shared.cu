@@ -60,7 +60,8 @@ struct Groups {
 // the units wait for the prefix's partials and merge; else merge_kernel does.
 template <bool MERGE>
 struct OwnPages {
-    static constexpr bool kIdentity = false, kSortable = false, kLateWait = MERGE, kPublish = !MERGE, kLoops = true;
+    static constexpr bool kIdentity = false, kSortable = false, kLateWait = MERGE, kPublish = !MERGE, kLoops = true,
+                          kFine = false;
     Groups gr;
 
     struct List {

@@ -43,12 +43,14 @@ using namespace dev;
 //   kLoops       a CTA goes on to chunk c + gridDim.z: the grid need not have a CTA for every
 //                chunk of the table's width, which with wide tables and short sequences would
 //                be mostly CTAs with nothing to do
+//   kFine        scores of FP8 pages for FP32 outputs
 // `emit(b, g)` makes what takes the units' scores, `skipped(b, g, j0, jn)` is told of a
 // unit that a bad page id keeps from being computed, `finished(b, g, L, M, l, scratch)` is
 // called by all threads of the unit that finishes a (sequence, KV head), each with its
 // head's softmax statistics; `scratch` is shared memory that the unit has done with.
 struct AllPages {
-    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
+    static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false,
+                          kFine = false;
     __device__ __forceinline__ WholeSequence list(int, int L) const { return {L}; }
     __device__ __forceinline__ EmitNothing emit(int, int) const { return {}; }
     __device__ __forceinline__ void skipped(int, int, int, int) const {}
@@ -848,7 +850,7 @@ __device__ __forceinline__ void decode_unit_fp8(const CUtensorMap &tmap, const S
         sel.skipped(b, g, j0, jn);
     }
 
-    fp8::Fp8MmaWarp w;
+    fp8::Fp8MmaWarpOf<Sel::kFine> w;
     w.init(sm.q_rot, a.scale_log2, lane);
     if (!any_bad) {
         const uint32_t first_limit = b == a.expire_seq ? 0u : kWaitLimit;

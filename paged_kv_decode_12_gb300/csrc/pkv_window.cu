@@ -17,7 +17,8 @@ namespace pkv {
 namespace {
 
 struct WindowPages {
-    static constexpr bool kIdentity = false, kSortable = true, kLateWait = false, kPublish = false, kLoops = false;
+    static constexpr bool kIdentity = false, kSortable = true, kLateWait = false, kPublish = false, kLoops = false,
+                          kFine = false;
     int window, sinks;
 
     struct List {

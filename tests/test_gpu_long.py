@@ -424,14 +424,53 @@ def test_scored_with_a_workspace_off_the_line(blocks, offset):
 
 @pytest.mark.parametrize("kv", KV)
 def test_scored_output_is_decode_attention(kv):
+    """Bit for bit on BF16 pages; on FP8 pages the scores are held more exactly, and both are within
+    their distance of the same values."""
     c, bt, lens, rng = whole_case(kv, [300, 77, 16, 1], 8)
-    q, _ = lh.query(rng, 4)
+    q, qf = lh.query(rng, 4)
     acc = torch.zeros((4, HKV, bt.shape[1] * PS), device="cuda")
     out, _ = run_scored(c, bt, lens, q, acc, acc, 4)
     ws = ws_of(pkv.pkv_decode_workspace_bytes(4, bt.shape[1], 4))
     ref = torch.empty_like(out)
     pkv.pkv_decode_attention(c.pool, q, lh.dev(bt), bt.shape[1], lh.dev(lens), 4, lh.SCALE, 4, ws, ws.numel(), ref)
-    assert torch.equal(out, ref)
+    if kv == "bf16":
+        assert torch.equal(out, ref)
+    for b, L in enumerate(lens):
+        off = lh.attend(qf[b], *c.rows(bt[b], range(int(L))), kv)[1]
+        close(out[b], lh.bf16_values(ref[b]), 2 * off, b)
+    c.close()
+
+
+def test_scored_fp8_weights_see_small_query_entries():
+    """Query entries 2^-11 to 2^-14 of their row's largest, which meets keys of nothing: the scores are
+    the small entries' alone, and as exact as FP32 sums of their products."""
+    rng = np.random.default_rng(77)
+    c, bt, lens, _ = whole_case("fp8", [200, 33], 53)
+    P = c.f8
+    for b, L in enumerate(lens):
+        t = np.arange(int(L))
+        codes = P.index[bt[b][t // PS], 0, :, t % PS]                 # [L][8][64] of K
+        k = rng.integers(0x30, 0x58, codes.shape).astype(np.uint8) | (rng.integers(0, 2, codes.shape) << 7).astype(np.uint8)
+        k[..., 0] = 0
+        c.host[codes] = k
+        P.scales[bt[b][t // PS], 0, :, t % PS] = 2.0 ** 9             # keys of 2^8 to 2^13
+    c.slab.copy_(torch.from_numpy(c.host).cuda())
+    x = rng.uniform(1, 2, (2, HQ, D)) * 2.0 ** -rng.integers(12, 15, (2, HQ, D)) * rng.choice([-1, 1], (2, HQ, D))
+    x[..., 0] = 1.0
+    bits = lh.bf16_bits(x)
+    q = torch.from_numpy(bits.view(np.int16).copy()).view(torch.bfloat16)
+    qf, q = q.double().numpy(), q.cuda()
+    acc = torch.zeros((2, HKV, bt.shape[1] * PS), device="cuda")
+    run_scored(c, bt, lens, q, acc, acc)
+    got = acc.cpu().numpy().astype(np.float64)
+    for b, L in enumerate(lens):
+        K, _ = c.rows(bt[b], range(int(L)))
+        p, s = lh.weights(qf[b], K)
+        ds = lh.SCALE * 2.0 ** -18 * np.einsum("hd,hnd->hn", np.abs(qf[b]), np.abs(np.repeat(K, 4, 0))) + 2.0 ** -20 * (1 + np.abs(s))
+        assert np.ptp(s, axis=1).min() > 1 and ds.max() < 2.0 ** -9  # (an entry's last two bits move scores by more)
+        dp = p * 2 * ds.max(1, keepdims=True) + 2.0 ** -126
+        w, dw = p.reshape(HKV, 4, -1).sum(1), dp.reshape(HKV, 4, -1).sum(1)
+        assert (np.abs(got[b, :, :L] - w) <= dw + 2.0 ** -22 * w).all(), b
     c.close()
 
 
