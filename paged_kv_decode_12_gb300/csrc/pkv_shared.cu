@@ -15,7 +15,7 @@
 // What bounds it: a page is read once a row tile pair instead of once a sequence, so bytes count
 // little; 64 exponentials a row and half tile take 512 of the 1000 clocks it lasts, and the rest
 // is the way from one wait to the next.  Two row tiles a CTA fill each other's gaps (256 sequences
-// behind 32768 tokens: 90 us, 760 TFLOP/s).
+// behind 32768 tokens: 94 us, 730 TFLOP/s).
 // Tried: 16 softmax warps, with half a row each or as four sets of their own (149 us where 8 took
 // 101), starting the second row tile half a step later (no change), 8 converter warps for FP8 with
 // registers moved to the softmax warps (30.3 us where 4 took 30.8).
@@ -520,7 +520,7 @@ struct RowScales {
 //
 // BF16 pages: the softmax's sum is of the weights as rounded, made by the matrix instruction too (L
 // += P 1, 16 equal columns), so that the quotient has none of their rounding where few weights make
-// it.  256 sequences behind 32768 tokens: error 0.0017 in 96 us, where the sum of the unrounded
+// it.  256 sequences behind 32768 tokens: error 0.0017 in 94 us, where the sum of the unrounded
 // weights, which this function returns, gives 0.0023 in 92, and unpacking the rounded ones took 108.
 // FP8 pages: what is rounded is the weight times V's row scale, so the sum stays the unrounded one.
 template <bool MASK, class Scale>
