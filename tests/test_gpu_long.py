@@ -271,6 +271,22 @@ def test_shared_scores_far_apart(kv, scale, groups):
     c.close()
 
 
+@pytest.mark.parametrize("scale", [0.0, 1e-38, 2.0 ** -90])
+def test_shared_fp8_values_of_nothing(scale):
+    """Prefix tokens whose V row scale is zero or nearly so: they weigh, and add nothing."""
+    c, bt, view, lens, starts, prefix, rng = shared_case("fp8", [(17, [5, 33, 1])], 231)
+    for t in rng.choice(17 * PS, 120, replace=False):
+        c.f8.scales[bt[0, t // PS], 1, :, t % PS] = scale
+    c.slab.copy_(torch.from_numpy(c.host).cuda())
+    q, qf = lh.query(rng, len(lens))
+    out, _ = run_shared(c, bt, lens, starts, prefix, q, 0, 0)
+    for b, L in enumerate(lens):
+        K, V = c.rows(view[b], range(int(L)))
+        want, off, _, _ = lh.attend(qf[b], K, V, "fp8", 2.0 ** -8)
+        close(out[b], want, off, (b, L))
+    c.close()
+
+
 @pytest.mark.parametrize("kv", KV)
 def test_shared_rows_do_not_depend_on_their_group(kv):
     groups = [(20, [5, 33, 2, 90]), (3, [7]), (0, [40, 1])]
