@@ -17,8 +17,8 @@
 // is the way from one wait to the next.  Two row tiles a CTA fill each other's gaps (256 sequences
 // behind 32768 tokens: 94 us, 730 TFLOP/s).
 // Tried: 16 softmax warps, with half a row each or as four sets of their own (149 us where 8 took
-// 101), starting the second row tile half a step later (no change), 8 converter warps for FP8 with
-// registers moved to the softmax warps (30.3 us where 4 took 30.8).
+// 101), starting the second row tile half a step later (no change), 8 converter warps for FP8 (30.3 us
+// where 4 took 30.8).
 #include <cmath>
 
 #include "pkv_step.cuh"
@@ -837,7 +837,8 @@ prefix_kernel(const __grid_constant__ CUtensorMap tmap, PrefixArgs a)
     const uint32_t tmem = bars.tmem;
     grid_dependency_wait();
     allow_dependent_launch();  // the sequences' own pages need nothing of this kernel until they merge
-    // FP8: 512 threads of 128 registers; the softmax warps take 168 and leave the others 88.
+    // FP8: 512 threads of 128 registers; the softmax warps take 168, so that none spill, and leave the
+    // others 88.  (Registers move by fours of warps: warp 11 only fills up its four.)
     if (warp < kLoader) {
         if constexpr (FP8)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
