@@ -89,7 +89,7 @@ class DecodeEngine:
         self.attn_options = pkv.PKV_DECODE_SPLIT_MERGE | variant if split_merge else self.step_options
         self.bt = None
         self.bt_host = None
-        self._extra_ws = {}   # workspaces of the shared, scored and evict calls, by call and size
+        self._extra_ws = {}   # workspaces of the shared, scored and evict calls, by call: [outgrown ones, current]
         self.chains = chains
         self.chain_bounds = chain_bounds(batch, chains)
         # each chain has its own stream and its own workspace (counters start at zero)
@@ -417,18 +417,19 @@ class DecodeEngine:
 
     def _workspace(self, call: str, nbytes: int, stream):
         """The call's workspace of at least ``nbytes`` (zeroed on its stream when made, then kept: the
-        calls leave their merge counters at zero).  Calls of one kind on two streams must not overlap."""
-        ws = self._extra_ws.get(call)
-        if ws is None or ws.numel() < nbytes:
-            s = self._on(stream)
-            with torch.cuda.stream(s):
+        calls leave their merge counters at zero).  Calls of one kind on two streams must not overlap.
+        One that is outgrown stays with the engine, because a captured graph may hold its address; a
+        new one is half as large again as the one before, so that all of them take a few times the
+        largest's bytes."""
+        kept = self._extra_ws.setdefault(call, [])
+        if not kept or kept[-1].numel() < nbytes:
+            with torch.cuda.stream(self._on(stream)):
                 # (one made inside a capture would be zeroed by the graph's replays only)
                 if torch.cuda.is_current_stream_capturing():
                     raise RuntimeError(f"make the {call} call once with these sizes before it is captured")
-                if ws is not None:
-                    ws.record_stream(s)
-                ws = self._extra_ws[call] = torch.zeros(max(nbytes, 16), dtype=torch.uint8, device=self.device)
-        return ws
+                least = kept[-1].numel() * 3 // 2 if kept else 16
+                kept.append(torch.zeros(max(nbytes, least), dtype=torch.uint8, device=self.device))
+        return kept[-1]
 
     def attention_shared(self, layer: int, q, seq_lens_dev, group_starts_dev, prefix_pages_dev, max_prefix_pages: int,
                          out, stream=None, prefix_pages_per_chunk: int = 0) -> None:

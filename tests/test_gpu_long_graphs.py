@@ -1,0 +1,49 @@
+"""Captured graphs of an engine that goes on being used: what a graph holds the address of stays."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_decode_12_gb300 import pkv
+from paged_kv_decode_12_gb300.engine import DecodeEngine
+from tests import long_helpers as lh
+from tests import test_gpu_long as tl
+
+pytestmark = pytest.mark.gpu
+
+native = tl.native
+
+
+@pytest.mark.parametrize("kv", tl.KV)
+def test_a_captured_call_outlives_a_larger_one(kv):
+    """attention_shared with a short prefix is captured, then called with a longer one (a larger
+    workspace); whatever memory comes free is filled; the graph still gives what it gave."""
+    c, bt, view, lens, starts, prefix, rng = tl.shared_case(kv, [(9, [20, 5, 33]), (2, [7, 40])], 31, extra_blocks=300)
+    B = lens.size
+    eng = DecodeEngine(c.pages, 1, B, max_blocks=bt.shape[1], pages_per_chunk=4, kv=kv)
+    eng.slab.copy_(c.slab)
+    eng.set_tables(bt[None])
+    q, qf = lh.query(rng, B)
+    args = (0, q, lh.dev(lens), lh.dev(starts), lh.dev(prefix))
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    eng.attention_shared(*args, 9, want, prefix_pages_per_chunk=8)
+    held = eng._extra_ws["shared"][-1].numel()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(2):
+            eng.attention_shared(*args, 9, out, prefix_pages_per_chunk=8)
+    larger = torch.empty_like(q)
+    eng.attention_shared(*args, 300, larger, prefix_pages_per_chunk=8)
+    assert eng._extra_ws["shared"][-1].numel() > held
+    fresh = [torch.full((held,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want)
+    assert torch.equal(larger, want)             # (fixed chunks: the bound on the prefixes changes no bit)
+    assert all(bool((t == 0x5A).all()) for t in fresh)
+    assert eng.check_errors() == (pkv.PKV_OK, 0)
+    for b in range(B):
+        K, V = c.rows(view[b], range(int(lens[b])))
+        tl.close(out[b], *lh.attend(qf[b], K, V, kv, 2.0 ** -8)[:2])
+    eng.close()
+    c.close()

@@ -1,0 +1,43 @@
+"""CPU checks of the engine's own bookkeeping for long contexts: an engine without a device, CUDA's
+streams stood in for."""
+import contextlib
+import gc
+import weakref
+
+import pytest
+import torch
+
+from paged_kv_decode_12_gb300.engine import DecodeEngine
+
+
+@pytest.fixture
+def bare(monkeypatch):
+    """An engine with none of its buffers, on the CPU."""
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    eng = DecodeEngine.__new__(DecodeEngine)
+    eng.device, eng.pool, eng._extra_ws = torch.device("cpu"), None, {}
+    return eng
+
+
+def test_outgrown_workspaces_stay_for_the_graphs_that_hold_them(bare):
+    """A captured graph keeps a workspace's address only: the memory must not go to anybody else."""
+    made = []
+    for nbytes in (100, 5000, 300, 70000):
+        ws = bare._workspace("shared", nbytes, None)
+        assert ws.numel() >= nbytes and not ws.any()
+        made.append((ws.data_ptr(), weakref.ref(ws)))
+        del ws
+    gc.collect()
+    assert [r() is not None and r().data_ptr() == p for p, r in made] == [True] * 4
+    # the largest serves what is smaller, and the kinds of call do not share
+    assert bare._workspace("shared", 6000, None).data_ptr() == made[-1][0]
+    assert bare._workspace("scored", 6000, None).data_ptr() not in [p for p, _ in made]
+
+
+def test_workspaces_that_grow_a_little_at_a_time_do_not_pile_up(bare):
+    for nbytes in range(1000, 100000, 500):
+        bare._workspace("shared", nbytes, None)
+    assert sum(t.numel() for kept in bare._extra_ws.values() for t in kept) <= 5 * 100000
