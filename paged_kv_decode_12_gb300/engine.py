@@ -126,9 +126,15 @@ class DecodeEngine:
         return bt
 
     def set_tables(self, bt_host: np.ndarray) -> None:
+        """The block tables of all layers.  New ones take the old ones' place on the device, where
+        captured graphs read them, once the work in flight is done."""
         assert bt_host.shape == (self.layers, self.batch, self.max_blocks)
         self.bt_host = np.ascontiguousarray(bt_host, dtype=np.int32)
-        self.bt = torch.from_numpy(self.bt_host).to(self.device)
+        if self.bt is None:
+            self.bt = torch.empty(self.bt_host.shape, dtype=torch.int32, device=self.device)
+        else:
+            torch.cuda.synchronize(self.device)
+        self.bt.copy_(torch.from_numpy(self.bt_host))
 
     def close(self) -> None:
         if self.pool is not None:

@@ -47,3 +47,31 @@ def test_a_captured_call_outlives_a_larger_one(kv):
         tl.close(out[b], *lh.attend(qf[b], K, V, kv, 2.0 ** -8)[:2])
     eng.close()
     c.close()
+
+
+@pytest.mark.parametrize("kv", tl.KV)
+def test_a_captured_call_reads_the_tables_that_are_set(kv):
+    """The same cache held twice, on other pages and in other rows' order: the graph follows the tables."""
+    c, bt, lens, rng = tl.whole_case(kv, [100, 100, 100], 61)
+    B, blocks = bt.shape
+    eng = DecodeEngine(c.pages, 1, B, max_blocks=blocks, pages_per_chunk=3, kv=kv)
+    eng.slab.copy_(c.slab)
+    eng.set_tables(bt[None])
+    q, qf = lh.query(rng, B)
+    lens_d, out = lh.dev(lens), torch.empty_like(q)
+    eng.attention(0, q, lens_d, out)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        eng.attention(0, q, lens_d, out)
+    for order in ([0, 1, 2], [2, 0, 1], [1, 1, 0]):
+        eng.set_tables(bt[order][None])
+        fresh = [torch.full((B * blocks,), -1, dtype=torch.int32, device="cuda") for _ in range(8)]
+        out.zero_()
+        g.replay()
+        assert eng.check_errors() == (pkv.PKV_OK, 0)
+        for b in range(B):
+            K, V = c.rows(bt[order[b]], range(100))
+            tl.close(out[b], *lh.attend(qf[b], K, V, kv)[:2])
+        assert all(bool((t == -1).all()) for t in fresh)
+    eng.close()
+    c.close()

@@ -4,6 +4,7 @@ import contextlib
 import gc
 import weakref
 
+import numpy as np
 import pytest
 import torch
 
@@ -16,6 +17,7 @@ def bare(monkeypatch):
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: None)
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda *a: None)
     monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
     eng = DecodeEngine.__new__(DecodeEngine)
     eng.device, eng.pool, eng._extra_ws = torch.device("cpu"), None, {}
@@ -41,3 +43,20 @@ def test_workspaces_that_grow_a_little_at_a_time_do_not_pile_up(bare):
     for nbytes in range(1000, 100000, 500):
         bare._workspace("shared", nbytes, None)
     assert sum(t.numel() for kept in bare._extra_ws.values() for t in kept) <= 5 * 100000
+
+
+def test_new_tables_go_where_the_old_ones_were(bare):
+    """Captured graphs hold the device tables' address."""
+    bare.layers, bare.batch, bare.max_blocks, bare.bt, bare.bt_host = 2, 3, 4, None, None
+    first = np.arange(24, dtype=np.int32).reshape(2, 3, 4)
+    bare.set_tables(first)
+    at = bare.bt.data_ptr()
+    second = first[::-1] + 100
+    bare.set_tables(second)
+    assert bare.bt.data_ptr() == at and np.array_equal(bare.bt.numpy(), second)
+    assert np.array_equal(bare.bt_host, second) and bare.bt_host.flags.c_contiguous
+    # the caller's array is neither the device's nor changed with it
+    own = second.copy()
+    bare.set_tables(own)
+    own[:] = -5
+    assert np.array_equal(bare.bt.numpy(), second)
