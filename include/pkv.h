@@ -140,10 +140,14 @@ int pkv_pool_destroy(pkv_pool *pool);
 int pkv_pool_alloc(pkv_pool *pool, int n, int32_t *ids_out);
 
 /* Return n pages (same section: pages come back when a request finishes or
- * stops early).  All ids are checked first: an id outside the pool is
+ * stops early).  All ids are checked first: an id outside the pool, or of a page that a
+ * scheduler holds for a request (pkv_sched_finish returns those), is
  * PKV_ERR_INVALID_ARG, an id not currently allocated (or repeated in the call)
  * is PKV_ERR_DOUBLE_FREE; on error nothing is freed. */
 int pkv_pool_free(pkv_pool *pool, int n, const int32_t *ids);
+
+/* What pkv_pool_free would return for these ids; nothing is freed. */
+int pkv_pool_check(pkv_pool *pool, int n, const int32_t *ids);
 
 /* Report the slab's K base, V base (= K base + 16 KiB; FP8 pools: head 0's V
  * codes, K base + 1 KiB, with the heads' units 2176 bytes apart), page stride in
@@ -282,7 +286,10 @@ int pkv_decode_attention_variant(const pkv_pool *pool, const uint16_t *q, const 
  * only after the current one has finished ("构建": --static / --continuous).
  * Host only (no CUDA call).  The scheduler assumes it owns the pool's pages that
  * are free when it is created (their number is the credit total); every page it
- * hands out belongs to exactly one (request, layer).  Not thread-safe. */
+ * hands out belongs to exactly one (request, layer) until the request ends, so it is
+ * not for giving back behind a window or after pkv_evict (pkv_pool_free refuses it), and
+ * its requests share no prefix: a batch that does so allocates its pages itself.  Not
+ * thread-safe. */
 typedef struct pkv_sched pkv_sched;
 
 #define PKV_SCHED_CONTINUOUS 0
@@ -572,8 +579,9 @@ size_t pkv_decode_scored_workspace_bytes(int B, int max_blocks, int pages_per_ch
  * copied bit by bit, in order, to slots 0 .. n-1, n = min(L, keep), of the pages of
  * bt_dst_dev [B][dst_blocks]; keys keep the rotation of their position.  Slots from n on
  * stay as they were, and so do the source pages: when the call's work is done the caller
- * gives them back.  The destination pages must be distinct from each other and from the
- * call's source pages (otherwise their contents are undefined).
+ * gives them back (a scheduler's requests keep theirs: see pkv_sched).  The destination
+ * pages must be distinct from each other and from the call's source pages (otherwise
+ * their contents are undefined).
  *   acc        FP32 [B][8][acc_stride], acc_stride >= 16 * src_blocks
  *   acc_out    FP32 [B][8][acc_out_stride], acc_out_stride >= 16 * dst_blocks: the kept
  *              tokens' weights, zeros behind them; may be acc itself with the same stride

@@ -80,7 +80,7 @@ int create_pool(void *dev_slab, size_t slab_bytes, int kv_format, size_t page_by
     p->page_bytes = page_bytes;
     try {
         p->free_list.resize(pages);
-        p->allocated.assign(pages, 0);
+        p->allocated.assign(pages, kPageFree);
     } catch (...) {
         delete p;
         return PKV_ERR_INVALID_ARG;
@@ -99,6 +99,62 @@ int create_pool(void *dev_slab, size_t slab_bytes, int kv_format, size_t page_by
 }
 
 }  // namespace
+
+namespace pkv {
+
+int pool_alloc(pkv_pool *pool, int n, int32_t *ids_out, PageOwner owner)
+{
+    if (!pool || n < 0 || (n > 0 && !ids_out))
+        return PKV_ERR_INVALID_ARG;
+    if ((size_t)n > pool->free_list.size())
+        return PKV_ERR_OUT_OF_PAGES;
+    for (int i = 0; i < n; ++i) {
+        int32_t id = pool->free_list.back();
+        pool->free_list.pop_back();
+        pool->allocated[id] = owner;
+        ids_out[i] = id;
+    }
+    return PKV_OK;
+}
+
+// Every id must be its holder's and appear once.
+int pool_check(pkv_pool *pool, int n, const int32_t *ids, PageOwner owner)
+{
+    constexpr uint8_t kSeen = 0x80;
+    if (!pool || n < 0 || (n > 0 && !ids))
+        return PKV_ERR_INVALID_ARG;
+    for (int i = 0; i < n; ++i)
+        if (ids[i] < 0 || ids[i] >= pool->num_pages)
+            return PKV_ERR_INVALID_ARG;
+    int status = PKV_OK;
+    int i = 0;
+    for (; i < n; ++i) {
+        uint8_t &holder = pool->allocated[ids[i]];
+        if (holder != owner) {
+            const bool held = !(holder & kSeen) && holder != kPageFree;
+            status = held ? PKV_ERR_INVALID_ARG : PKV_ERR_DOUBLE_FREE;
+            break;
+        }
+        holder |= kSeen;
+    }
+    for (int k = 0; k < i; ++k)
+        pool->allocated[ids[k]] = owner;  // undo the marks
+    return status;
+}
+
+int pool_free(pkv_pool *pool, int n, const int32_t *ids, PageOwner owner)
+{
+    // every id is checked before any is freed
+    if (const int status = pool_check(pool, n, ids, owner); status != PKV_OK)
+        return status;
+    for (int k = 0; k < n; ++k) {
+        pool->allocated[ids[k]] = kPageFree;
+        pool->free_list.push_back(ids[k]);
+    }
+    return PKV_OK;
+}
+
+}  // namespace pkv
 
 extern "C" {
 
@@ -131,48 +187,11 @@ int pkv_pool_destroy(pkv_pool *pool)
     return PKV_OK;
 }
 
-int pkv_pool_alloc(pkv_pool *pool, int n, int32_t *ids_out)
-{
-    if (!pool || n < 0 || (n > 0 && !ids_out))
-        return PKV_ERR_INVALID_ARG;
-    if ((size_t)n > pool->free_list.size())
-        return PKV_ERR_OUT_OF_PAGES;
-    for (int i = 0; i < n; ++i) {
-        int32_t id = pool->free_list.back();
-        pool->free_list.pop_back();
-        pool->allocated[id] = 1;
-        ids_out[i] = id;
-    }
-    return PKV_OK;
-}
+int pkv_pool_alloc(pkv_pool *pool, int n, int32_t *ids_out) { return pkv::pool_alloc(pool, n, ids_out, kPageCaller); }
 
-int pkv_pool_free(pkv_pool *pool, int n, const int32_t *ids)
-{
-    if (!pool || n < 0 || (n > 0 && !ids))
-        return PKV_ERR_INVALID_ARG;
-    for (int i = 0; i < n; ++i)
-        if (ids[i] < 0 || ids[i] >= pool->num_pages)
-            return PKV_ERR_INVALID_ARG;
-    // check every id before freeing any: each must be allocated and appear once
-    int status = PKV_OK;
-    int i = 0;
-    for (; i < n; ++i) {
-        if (pool->allocated[ids[i]] != 1) {
-            status = PKV_ERR_DOUBLE_FREE;
-            break;
-        }
-        pool->allocated[ids[i]] = 2;  // mark "seen in this call"
-    }
-    for (int k = 0; k < i; ++k)
-        pool->allocated[ids[k]] = 1;  // undo the marks
-    if (status != PKV_OK)
-        return status;
-    for (int k = 0; k < n; ++k) {
-        pool->allocated[ids[k]] = 0;
-        pool->free_list.push_back(ids[k]);
-    }
-    return PKV_OK;
-}
+int pkv_pool_free(pkv_pool *pool, int n, const int32_t *ids) { return pkv::pool_free(pool, n, ids, kPageCaller); }
+
+int pkv_pool_check(pkv_pool *pool, int n, const int32_t *ids) { return pkv::pool_check(pool, n, ids, kPageCaller); }
 
 int pkv_pool_info(const pkv_pool *pool, void **k_base, void **v_base, int64_t *page_stride_bytes,
                   int *num_pages, int *num_free)

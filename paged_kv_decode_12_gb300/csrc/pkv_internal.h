@@ -11,12 +11,16 @@
 
 #include "../../include/pkv.h"
 
+// Who holds a page.  What a scheduler holds only a scheduler gives back: it belongs to a request
+// until that ends.
+enum PageOwner : uint8_t { kPageFree = 0, kPageCaller = 1, kPageScheduler = 2 };
+
 struct pkv_pool {
     char *slab = nullptr;          // caller-owned device slab
     size_t slab_bytes = 0;
     int32_t num_pages = 0;
     std::vector<int32_t> free_list;  // stack of free page ids; pop from the back
-    std::vector<uint8_t> allocated;  // 1 while a page is handed out
+    std::vector<uint8_t> allocated;  // PageOwner of every page
     int kv_format = PKV_KV_BF16;     // PKV_KV_BF16 or PKV_KV_FP8
     size_t page_bytes = PKV_PAGE_BYTES;
     // TMA descriptor of the slab.  BF16 pools: [num_pages][2][8][16][64] BF16,
@@ -34,6 +38,11 @@ struct pkv_pool {
 };
 
 namespace pkv {
+
+// pkv_pool_alloc and pkv_pool_free for a holder of pages; pool_check says what pool_free would.
+int pool_alloc(pkv_pool *pool, int n, int32_t *ids_out, PageOwner owner);
+int pool_free(pkv_pool *pool, int n, const int32_t *ids, PageOwner owner);
+int pool_check(pkv_pool *pool, int n, const int32_t *ids, PageOwner owner);
 
 constexpr int kPage = PKV_PAGE_SIZE;      // tokens per page
 constexpr int kHq = PKV_NUM_Q_HEADS;      // query heads

@@ -66,11 +66,11 @@ int grow(pkv_sched *s, pkv_sched::Req &r, int tokens)
     const int add = need - r.npages;
     for (int l = 0; l < s->layers; ++l) {
         int32_t *row = &r.pages[(size_t)l * s->max_blocks];
-        const int st = pkv_pool_alloc(s->pool, add, row + r.npages);
+        const int st = pkv::pool_alloc(s->pool, add, row + r.npages, kPageScheduler);
         if (st != PKV_OK) {
             for (int k = 0; k < l; ++k) {  // undo the layers already grown
                 int32_t *done = &r.pages[(size_t)k * s->max_blocks] + r.npages;
-                (void)pkv_pool_free(s->pool, add, done);
+                (void)pkv::pool_free(s->pool, add, done, kPageScheduler);
                 std::fill(done, done + add, -1);
             }
             return st;
@@ -88,7 +88,7 @@ void release(pkv_sched *s, pkv_sched::Req &r)
     for (int l = 0; l < s->layers; ++l) {
         const int32_t *row = &r.pages[(size_t)l * s->max_blocks];
         if (r.npages > 0)
-            (void)pkv_pool_free(s->pool, r.npages, row);
+            (void)pkv::pool_free(s->pool, r.npages, row, kPageScheduler);
     }
     s->allocated -= (int64_t)r.npages * s->layers;
     s->free_credits += r.budget_pages;

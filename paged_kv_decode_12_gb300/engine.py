@@ -465,7 +465,8 @@ class DecodeEngine:
         later work on it comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the
         table of all layers in step: each layer is cut by its own call with the same arguments.
         A row names all of its sequence's pages; rows may share some (a prefix), and no longer do
-        after it.  Cannot be captured."""
+        after it.  Every page must be the caller's to give back (allocated, and not a scheduler's:
+        a PkvError otherwise, with nothing done).  Cannot be captured."""
         lens = np.asarray(seq_lens, dtype=np.int32)
         if lens.shape != (self.batch,) or lens.min() < 0 or lens.max() > wl.PAGE_SIZE * self.max_blocks:
             raise ValueError("seq_lens: a length within the table's width for every sequence")
@@ -474,6 +475,9 @@ class DecodeEngine:
         with torch.cuda.stream(s):
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("an eviction takes and gives back pages on the host: it cannot be captured")
+        old = self.bt_host[layer]
+        old = np.unique(old[old >= 0])
+        pkv.pkv_pool_check(self.pool, old)
         after = np.minimum(lens, keep).astype(np.int32)
         need = (after + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
         nbytes = pkv.pkv_evict_workspace_bytes(self.batch, keep)
@@ -493,8 +497,7 @@ class DecodeEngine:
             self.bt[layer].copy_(dst_dev)
             for t in (dst_dev, lens_dev):
                 t.record_stream(s)
-        old = self.bt_host[layer]
-        pkv.pkv_pool_free(self.pool, np.unique(old[old >= 0]))
+        pkv.pkv_pool_free(self.pool, old)
         self.bt_host = self.bt_host.copy()  # (the caller may hold the old tables)
         self.bt_host[layer] = dst
         return after

@@ -54,7 +54,7 @@ def PKV_STEP_RING(n: int) -> int:
 
 # every symbol include/pkv.h declares
 EXPORTED = (
-    "pkv_pool_create", "pkv_pool_destroy", "pkv_pool_alloc", "pkv_pool_free", "pkv_pool_info",
+    "pkv_pool_create", "pkv_pool_destroy", "pkv_pool_alloc", "pkv_pool_free", "pkv_pool_check", "pkv_pool_info",
     "pkv_block_tables_build", "pkv_rope_table_bytes", "pkv_rope_table_init", "pkv_append_rope",
     "pkv_decode_workspace_bytes",
     "pkv_decode_attention", "pkv_decode_attention_variant", "pkv_decode_attention_noalloc",
@@ -88,6 +88,7 @@ def lib():
     L.pkv_pool_destroy.argtypes = [_vp]
     L.pkv_pool_alloc.argtypes = [_vp, _i32, _i32p]
     L.pkv_pool_free.argtypes = [_vp, _i32, _i32p]
+    L.pkv_pool_check.argtypes = [_vp, _i32, _i32p]
     L.pkv_pool_info.argtypes = [_vp, ctypes.POINTER(_vp), ctypes.POINTER(_vp), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(_i32), ctypes.POINTER(_i32)]
     L.pkv_block_tables_build.argtypes = [_vp, _i32, _i32, _i32p, _i32, _i32p]
@@ -203,6 +204,12 @@ def pkv_pool_alloc(pool, n: int) -> np.ndarray:
 def pkv_pool_free(pool, ids) -> None:
     ids = _np_i32(ids)
     _check(lib().pkv_pool_free(pool, ids.size, ids.ctypes.data_as(_i32p)), "pkv_pool_free")
+
+
+def pkv_pool_check(pool, ids) -> None:
+    """Raises what pkv_pool_free would for these ids; nothing is freed."""
+    ids = _np_i32(ids)
+    _check(lib().pkv_pool_check(pool, ids.size, ids.ctypes.data_as(_i32p)), "pkv_pool_check")
 
 
 def pkv_pool_info(pool) -> dict:
