@@ -245,9 +245,9 @@ size_t pkv_decode_workspace_bytes(int B, int max_blocks, int pages_per_chunk);
  * So the kernel immediately before this call on the stream may write q (e.g. a
  * projection) and positions seq_len - 1 and seq_len - 2 (the append of this step,
  * pkv_append_rope at pos = seq_len - 1, or of the previous step), but must not
- * write seq_lens, bt_dev or any earlier position of these sequences' pages.  A
- * pkv_prefill_append on the same pool makes the next decode launch on the pool go
- * without programmatic dependent launch.
+ * write seq_lens, bt_dev or any earlier position of these sequences' pages.  After a
+ * pkv_prefill_append or pkv_evict the next decode launch on the pool, and the next one on
+ * that call's stream, go without programmatic dependent launch.
  * Device checks: seq_len outside [1, 16*max_blocks] or a page id outside the
  * pool sets the flag; the affected (sequence, head) outputs are zeros. */
 int pkv_decode_attention(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
@@ -349,8 +349,8 @@ int pkv_sched_get_stats(const pkv_sched *sched, pkv_sched_stats *out);
  * position).  k, v: [layers][T][8][64] BF16; bt_rows: device [layers][max_blocks]
  * (this sequence's table in every layer).  Device checks: a position beyond the
  * table or max_pos, or a page id outside the pool, sets the flag and skips it.
- * The next pkv_decode_step / pkv_decode_attention launch on this pool goes without
- * programmatic dependent launch, because it may read these pages. */
+ * The next pkv_decode_* launch on this pool, and the next one on this stream, go without
+ * programmatic dependent launch, because they may read these pages. */
 int pkv_prefill_append(const pkv_pool *pool, const uint16_t *k, const uint16_t *v, const int32_t *bt_rows,
                        int max_blocks, int layers, int start_pos, int T, const float *rope_table, int max_pos,
                        int32_t *dev_err_flag, void *cuda_stream);
@@ -407,8 +407,8 @@ size_t pkv_decode_step_workspace_bytes(int B, int max_blocks, int pages_per_chun
  * seq_len - 2, and it lets the next launch begin only after its own wait.  So the
  * previous step of the same layer may be the immediately preceding kernel (a
  * one-layer model: it wrote position seq_len - 2), but that kernel must not write
- * seq_lens, bt_dev or earlier positions.  The first decode launch on a pool after
- * a pkv_prefill_append on it goes without programmatic dependent launch.
+ * seq_lens, bt_dev or earlier positions.  The first decode launches after a
+ * pkv_prefill_append or pkv_evict go without programmatic dependent launch (see there).
  * Device checks as pkv_decode_attention, plus seq_len > max_pos.
  * FP8 pools: the same single launch (a ring stage is one 2176-byte unit): the new
  * token's rotated key row and value row are quantized as pkv_append_rope quantizes
@@ -589,8 +589,8 @@ size_t pkv_decode_scored_workspace_bytes(int B, int max_blocks, int pages_per_ch
  *              then `workspace` holds them (pkv_evict_workspace_bytes, 4-byte aligned)
  *   seq_lens_out int32 [B]: n; may be seq_lens_dev itself
  * The next token of such a sequence is appended with pkv_append_rope_at: its position is
- * no longer its slot.  The next pkv_decode_* launch on this pool goes without
- * programmatic dependent launch, because it may read these pages.
+ * no longer its slot.  The next pkv_decode_* launch on this pool, and the next one on this
+ * stream, go without programmatic dependent launch, because they may read these pages.
  * Device checks: L outside [0, 16*src_blocks] or n > 16*dst_blocks sets
  * PKV_DEVERR_LENGTH, and the sequence is treated as empty; a page id outside the pool
  * sets PKV_DEVERR_PAGE_RANGE, and the rows concerned are not copied. */

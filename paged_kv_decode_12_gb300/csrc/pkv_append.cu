@@ -184,7 +184,7 @@ extern "C" int pkv_prefill_append(const pkv_pool *pool, const uint16_t *k, const
         15u)
         return PKV_ERR_INVALID_ARG;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    pool->serialize_next_launch = true;  // the next decode launch may read these pages
+    pages_written(pool, s);  // a decode launch behind it may read these pages
     if (pool->kv_format == PKV_KV_FP8)
         return fp8_prefill_append(pool, k, v, bt_rows, max_blocks, layers, start_pos, T, rope_table, max_pos,
                                   dev_err_flag, s);

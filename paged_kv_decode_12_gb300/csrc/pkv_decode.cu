@@ -272,7 +272,7 @@ extern "C" int pkv_decode_attention_variant(const pkv_pool *pool, const uint16_t
     const CUtensorMap *tmap = pool_tensor_map(pool);
     if (!tmap)
         return PKV_ERR_CUDA;
-    (void)take_pdl_permission(pool, false);  // this form launches without programmatic dependent launch
+    (void)take_pdl_permission(pool, s, false);  // this form launches without programmatic dependent launch
     const WorkspaceLayout ws = workspace_layout(B, max_chunks);
     char *wsp = static_cast<char *>(workspace);
     SplitArgs a;

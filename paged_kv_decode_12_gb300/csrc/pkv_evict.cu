@@ -456,9 +456,9 @@ extern "C" int pkv_evict(const pkv_pool *pool, const int32_t *bt_src_dev, int sr
         kept = static_cast<int32_t *>(workspace);
     }
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-    // rows written here are read by later launches: the next decode launch on the pool may
-    // not copy pages before its dependency wait
-    pool->serialize_next_launch = true;
+    // rows written here are read by later launches: a decode launch behind them may not copy pages
+    // before its dependency wait
+    pages_written(pool, s);
     const int longest = src_blocks * kPage, threads = longest <= 8 * 32 * 32 ? 8 * 32 : 32 * 32;
     const auto select = longest <= 8 * 32 * 32    ? select_kernel<8, 32>
                         : longest <= 32 * 32 * 32 ? select_kernel<32, 32>

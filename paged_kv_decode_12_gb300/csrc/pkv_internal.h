@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
 #include <mutex>
 #include <utility>
@@ -31,10 +32,18 @@ struct pkv_pool {
     // needs the CUDA driver.
     CUtensorMap tmap;  // 64-byte aligned by its own declaration
     bool tmap_ready = false;
-    // Set by a prefill on this pool: the prefill wrote cached positions that the next
-    // decode launch would otherwise start copying before its dependency wait, so that
-    // launch goes without programmatic dependent launch (and clears the flag).
-    mutable bool serialize_next_launch = false;
+    // Where pages were last written by a call other than a decode step's append (pkv_prefill_append,
+    // pkv_evict): the next decode launch on the pool, and the next one on that stream, go
+    // without programmatic dependent launch, because they would otherwise start copying pages
+    // before their dependency wait.  (The next one on the pool may be on another stream, and leaves
+    // the one behind the writes to wait.)
+    struct Fence {
+        std::mutex mu;
+        bool next = false;
+        bool always = false;  // no memory to remember a stream
+        std::vector<cudaStream_t> streams;
+    };
+    mutable Fence fence;
 };
 
 namespace pkv {
@@ -166,13 +175,34 @@ int launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem,
     return status_from_cuda(cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...));
 }
 
-// Whether a decode launch on `pool` may use programmatic dependent launch: not the
-// first one after a prefill on the pool (see pkv_pool::serialize_next_launch).
-inline bool take_pdl_permission(const pkv_pool *pool, bool pdl_requested)
+// A call on `s` writes pages of `pool` (see pkv_pool::Fence).
+inline void pages_written(const pkv_pool *pool, cudaStream_t s)
 {
-    const bool fence = pool->serialize_next_launch;
-    pool->serialize_next_launch = false;
-    return pdl_requested && !fence;
+    pkv_pool::Fence &f = pool->fence;
+    std::lock_guard<std::mutex> lock(f.mu);
+    f.next = true;
+    if (std::find(f.streams.begin(), f.streams.end(), s) != f.streams.end())
+        return;
+    try {
+        f.streams.push_back(s);
+    } catch (...) {
+        f.always = true;
+    }
+}
+
+// Whether a decode launch on `pool` and `s` may use programmatic dependent launch.
+inline bool take_pdl_permission(const pkv_pool *pool, cudaStream_t s, bool pdl_requested)
+{
+    pkv_pool::Fence &f = pool->fence;
+    std::lock_guard<std::mutex> lock(f.mu);
+    bool waits = f.next || f.always;
+    f.next = false;
+    const auto at = std::find(f.streams.begin(), f.streams.end(), s);
+    if (at != f.streams.end()) {
+        waits = true;
+        f.streams.erase(at);
+    }
+    return pdl_requested && !waits;
 }
 
 }  // namespace pkv

@@ -1016,7 +1016,7 @@ extern "C" int pkv_decode_shared(const pkv_pool *pool, const uint16_t *q, const 
     // both launches check the options; the first is the one that must not run if they are refused
     if (const int st = check_options<OwnPages<true>>(pool, B, max_blocks, plan.own_ppc, options); st != PKV_OK)
         return st;
-    const bool pdl = take_pdl_permission(pool, !(options & PKV_STEP_NO_PDL));
+    const bool pdl = take_pdl_permission(pool, s, !(options & PKV_STEP_NO_PDL));
     if (plan.max_items > 0) {
         const WorkspaceLayout ws = workspace_layout(B, plan.max_chunks);
         PrefixArgs p;

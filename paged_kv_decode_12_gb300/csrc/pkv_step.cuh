@@ -1085,7 +1085,7 @@ int launch_fused(const pkv_pool *pool, StepArgs &a, const Sel &sel, int B, int m
     a.sorted = (options & PKV_STEP_SORTED) ? 1 : 0;
     a.expire_seq = (options & PKV_STEP_TEST_EXPIRE_WAIT) ? 0 : -1;
     const bool wanted = !(options & PKV_STEP_NO_PDL);
-    const bool pdl = follows ? wanted : take_pdl_permission(pool, wanted);
+    const bool pdl = follows ? wanted : take_pdl_permission(pool, s, wanted);
     // (selections of pages: 2 stages were the fastest or within 1 % of it at every size)
     const int depth = ring ? ring : std::is_same_v<Sel, AllPages> ? default_ring(pages_per_chunk) : 2;
     if (pool->kv_format == PKV_KV_FP8)

@@ -75,3 +75,54 @@ def test_a_captured_call_reads_the_tables_that_are_set(kv):
         assert all(bool((t == -1).all()) for t in fresh)
     eng.close()
     c.close()
+
+
+@pytest.mark.parametrize("kv", tl.KV)
+def test_attention_behind_an_eviction_with_a_call_elsewhere_between(kv):
+    """An eviction on one stream, a call over another cache on a second one, then attention over the cut
+    cache right behind the eviction: it reads the rows that the eviction has put there."""
+    c, bt, lens, rng = tl.whole_case(kv, [1500, 1490, 1480, 1470], 62, blocks=100)
+    B, blocks, keep = bt.shape[0], bt.shape[1], 1024
+    acc = tl.acc_of(rng, (B, lh.HKV, blocks * lh.PS), "real")
+    dst = np.full((B, blocks), -1, dtype=np.int32)
+    dst[:, :keep // lh.PS] = np.arange(B * keep // lh.PS).reshape(B, -1)
+    big = lh.Cache(kv, c.pages + B * keep // lh.PS)
+    big.host[:c.host.size] = c.host
+    dst[dst >= 0] += c.pages
+    big.upload()
+    other, obt, olens, _ = tl.whole_case(kv, [90, 33], 63)
+    q, _ = lh.query(rng, B)
+    n = pkv.pkv_decode_workspace_bytes(B, blocks, 16)
+    ws, ws2, err = tl.ws_of(n), tl.ws_of(n), tl.flag()
+    bt_d, dst_d, lens_d, acc_d = lh.dev(bt), lh.dev(dst), lh.dev(lens), lh.dev(acc)
+    after, cut = torch.zeros_like(lens_d), torch.full_like(lens_d, keep)
+    acc_out = torch.zeros((B, lh.HKV, blocks * lh.PS), device="cuda")
+    kept = torch.zeros((B, lh.HKV, keep), dtype=torch.int32, device="cuda")
+    want, out, side = (torch.empty_like(q) for _ in range(3))
+    obt_d, olens_d = lh.dev(obt), lh.dev(olens)
+    start = big.slab.clone()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def evict(st):
+        pkv.pkv_evict(big.pool, bt_d, blocks, lens_d, B, dst_d, blocks, keep, 100, 4, acc_d, acc.shape[-1], acc_out,
+                      acc.shape[-1], kept, after, None, 0, err, st)
+
+    def attend(o, st):
+        pkv.pkv_decode_attention(big.pool, q, dst_d, blocks, cut, B, lh.SCALE, 16, ws, n, o, err, st)
+
+    evict(None)
+    torch.cuda.synchronize()
+    attend(want, None)
+    assert not torch.isnan(want).any()
+    for _ in range(20):
+        big.slab.copy_(start)                    # the pages to be cut to hold NaN again
+        out.fill_(7.0)
+        torch.cuda.synchronize()
+        evict(a)
+        pkv.pkv_decode_attention(big.pool, q[:2], obt_d, obt.shape[1], olens_d, 2, lh.SCALE, 16, ws2, n, side[:2], err, b)
+        attend(out, a)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert pkv.pkv_check_device_error(err) == (pkv.PKV_OK, 0)
+    for x in (big, c, other):
+        x.close()
