@@ -258,8 +258,26 @@ struct Fp8MmaWarpOf {
         // across the warp and O^T, l are rescaled -- so most pages need no reduction and
         // the weights stay below 2^kDeferLog2 (m, l, o remain a valid log-sum-exp triple).
         const float skh00 = sk0 * hf[0], skh01 = sk0 * hf[1], skh10 = sk1 * hf[0], skh11 = sk1 * hf[1];
-        float z[4] = {fmaf(s[0], skh00, -m[0]), fmaf(s[1], skh01, -m[1]), fmaf(s[2], skh10, -m[0]),
-                      fmaf(s[3], skh11, -m[1])};
+        float x[4], z[4];
+        if constexpr (FINE) {  // the weights that are summed are those of the scores as emitted, rounded
+            x[0] = __fmul_rn(s[0], skh00);
+            x[1] = __fmul_rn(s[1], skh01);
+            x[2] = __fmul_rn(s[2], skh10);
+            x[3] = __fmul_rn(s[3], skh11);
+            z[0] = x[0] - m[0];
+            z[1] = x[1] - m[1];
+            z[2] = x[2] - m[0];
+            z[3] = x[3] - m[1];
+        } else {
+            x[0] = s[0] * skh00;
+            x[1] = s[1] * skh01;
+            x[2] = s[2] * skh10;
+            x[3] = s[3] * skh11;
+            z[0] = fmaf(s[0], skh00, -m[0]);
+            z[1] = fmaf(s[1], skh01, -m[1]);
+            z[2] = fmaf(s[2], skh10, -m[0]);
+            z[3] = fmaf(s[3], skh11, -m[1]);
+        }
         if (!keep(gid)) {
             z[0] = z[1] = -INFINITY;
             sv0 = 0.f;
@@ -270,13 +288,12 @@ struct Fp8MmaWarpOf {
         }
         if (tig < 2) {
             if (keep(gid))
-                emit(gid, 2 * tig, s[0] * skh00, s[1] * skh01);
+                emit(gid, 2 * tig, x[0], x[1]);
             if (keep(gid + 8))
-                emit(gid + 8, 2 * tig, s[2] * skh10, s[3] * skh11);
+                emit(gid + 8, 2 * tig, x[2], x[3]);
         }
         float al0 = 1.f, al1 = 1.f;
         if (__any_sync(kFull, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) > kDeferLog2)) {
-            float x[4] = {s[0] * skh00, s[1] * skh01, s[2] * skh10, s[3] * skh11};
             if (!keep(gid))
                 x[0] = x[1] = -INFINITY;
             if (!keep(gid + 8))

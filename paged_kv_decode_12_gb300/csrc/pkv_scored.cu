@@ -6,8 +6,9 @@
 //
 // A weight is known only when the whole sequence's maximum and sum are.  The grid kernel of
 // pkv_step.cuh goes over every page and also stores the scores (log2 domain, FP32, the four heads
-// of a token side by side); the unit that finishes a (sequence, KV head) knows log2 of each head's
-// sum and turns the scores into weights.  For short rows it does so itself, while other units
+// of a token side by side); the unit that finishes a (sequence, KV head) knows each head's maximum M
+// and log2 of its sum l and turns the scores into weights, 2^((x - M) - log2 l).  (Not 2^(x - (M +
+// log2 l)): that sum's rounding at M would be every weight's, 1e-4 of it at an M of 2000.)  For short rows it does so itself, while other units
 // stream their pages; a long row would keep one CTA busy behind all others, so there a second
 // launch does it, one (KV head, token) per thread.
 // Either way 128 bytes per token are re-read where a second pass over the keys would read 1024
@@ -17,12 +18,12 @@
 namespace pkv {
 namespace {
 
-// acc_out[t] = acc[t] + the four heads' weights of token t, from its scores and log2 of the heads'
-// sums, for t = t0, t0 + STEP, ... < L (t0: a multiple of 32, plus the lane): N of them, all read
+// acc_out[t] = acc[t] + the four heads' weights of token t, from its scores, the heads' maxima and log2
+// of their sums, for t = t0, t0 + STEP, ... < L (t0: a multiple of 32, plus the lane): N of them, all read
 // before any is written (acc and acc_out may be one array, so the compiler may not reorder them
 // itself).
 template <int N, int STEP>
-__device__ __forceinline__ void add_weights(const float4 *scores, float4 n, const float *acc, float *acc_out, int t0, int L)
+__device__ __forceinline__ void add_weights(const float4 *scores, float4 m, float4 n, const float *acc, float *acc_out, int t0, int L)
 {
     float4 s[N];
     float a[N];
@@ -38,8 +39,8 @@ __device__ __forceinline__ void add_weights(const float4 *scores, float4 n, cons
     for (int i = 0; i < N; ++i) {
         const int t = t0 + i * STEP;
         if (t < L)
-            acc_out[t] = a[i] + ((ex2_approx(s[i].x - n.x) + ex2_approx(s[i].y - n.y)) +
-                                 (ex2_approx(s[i].z - n.z) + ex2_approx(s[i].w - n.w)));
+            acc_out[t] = a[i] + ((ex2_approx((s[i].x - m.x) - n.x) + ex2_approx((s[i].y - m.y) - n.y)) +
+                                 (ex2_approx((s[i].z - m.z) - n.z) + ex2_approx((s[i].w - m.w) - n.w)));
     }
     // The scores are not needed again: whole lines that this warp has read (its tokens are 32 in a
     // row) are dropped from L2 instead of being written to memory some time later (64 sequences up
@@ -58,7 +59,9 @@ struct ScoredPages {
     static constexpr bool kIdentity = true, kSortable = true, kLateWait = false, kPublish = false, kLoops = false,
                           kFine = true;
     float *scores;  // [B][8][tokens][4]
-    float *lse;     // [B][32] log2 of the sum of 2^score
+    float *logs;    // [B][32] log2 of the sum of 2^(score - maximum)
+    float2 *tops;   // [B][32][max_chunks] the attention's partials; the first one's place takes the maximum
+    int max_chunks;
     int tokens;     // per (sequence, KV head): 16 * max_blocks
     const float *acc;
     float *acc_out;
@@ -92,21 +95,29 @@ struct ScoredPages {
     __device__ __forceinline__ void finished(int b, int g, int L, float M, float l, float *scratch) const
     {
         const int hl = threadIdx.x >> 5;
-        const float n = l > 0.f ? M + log2f(l) : INFINITY;  // nothing computed: every weight is 0
+        const bool some = l > 0.f;  // nothing computed: every weight is 0
+        const float m = some ? M : 0.f, n = some ? log2f(l) : INFINITY;
         if (!INLINE) {
-            if ((threadIdx.x & 31) == 0)
-                lse[b * kHq + g * kGroup + hl] = n;
+            __syncwarp();  // the warp has merged its head's partials
+            if ((threadIdx.x & 31) == 0) {
+                const int h = b * kHq + g * kGroup + hl;
+                logs[h] = n;
+                tops[(size_t)h * max_chunks].x = m;
+            }
             return;
         }
         __syncthreads();
-        if ((threadIdx.x & 31) == 0)
-            scratch[hl] = n;
+        if ((threadIdx.x & 31) == 0) {
+            scratch[hl] = m;
+            scratch[kGroup + hl] = n;
+        }
         __syncthreads();
-        const float4 all = *reinterpret_cast<const float4 *>(scratch);
+        const float4 ms = *reinterpret_cast<const float4 *>(scratch);
+        const float4 ns = *reinterpret_cast<const float4 *>(scratch + kGroup);
         const float4 *x = reinterpret_cast<const float4 *>(row(b, g));
         const size_t at = ((size_t)b * kHkv + g) * acc_stride;
         for (int t0 = 0; t0 < L; t0 += 8 * kThreads)
-            add_weights<8, kThreads>(x, all, acc + at, acc_out + at, t0 + threadIdx.x, L);
+            add_weights<8, kThreads>(x, ms, ns, acc + at, acc_out + at, t0 + threadIdx.x, L);
     }
 };
 
@@ -114,8 +125,9 @@ constexpr int kAccThreads = 256;
 constexpr int kAccTokens = 4 * kAccThreads;  // tokens per CTA, so that long tables make few empty CTAs
 
 __global__ void __launch_bounds__(kAccThreads)
-accumulate_kernel(const float4 *__restrict__ scores, const float *__restrict__ lse, const int32_t *__restrict__ seq_lens,
-                  int max_blocks, const float *acc, float *acc_out, int64_t acc_stride)
+accumulate_kernel(const float4 *__restrict__ scores, const float *__restrict__ logs, const float2 *__restrict__ tops,
+                  int max_chunks, const int32_t *__restrict__ seq_lens, int max_blocks, const float *acc, float *acc_out,
+                  int64_t acc_stride)
 {
     const int g = blockIdx.y, b = blockIdx.z, t0 = blockIdx.x * kAccTokens;
     const int L = seq_lens[b];
@@ -123,16 +135,19 @@ accumulate_kernel(const float4 *__restrict__ scores, const float *__restrict__ l
     allow_dependent_launch();
     if (L < 1 || L > max_blocks * kPage || t0 >= L)
         return;
-    const float4 n = *reinterpret_cast<const float4 *>(lse + b * kHq + g * kGroup);
+    const int h = b * kHq + g * kGroup;
+    const float4 n = *reinterpret_cast<const float4 *>(logs + h);
+    const float2 *top = tops + (size_t)h * max_chunks;
+    const float4 m = make_float4(top[0].x, top[max_chunks].x, top[2 * (size_t)max_chunks].x, top[3 * (size_t)max_chunks].x);
     const size_t row = (size_t)b * kHkv + g;
     const float4 *x = scores + row * ((size_t)max_blocks * kPage);
-    add_weights<kAccTokens / kAccThreads, kAccThreads>(x, n, acc + row * acc_stride, acc_out + row * acc_stride,
+    add_weights<kAccTokens / kAccThreads, kAccThreads>(x, m, n, acc + row * acc_stride, acc_out + row * acc_stride,
                                                        t0 + threadIdx.x, L);
 }
 
 struct ScoredWorkspace {
-    size_t attention, scores, lse;
-    size_t total() const { return attention + scores + lse; }
+    size_t attention, scores, logs;
+    size_t total() const { return attention + scores + logs; }
 };
 
 ScoredWorkspace scored_workspace(int B, int max_blocks, int max_chunks)
@@ -140,7 +155,7 @@ ScoredWorkspace scored_workspace(int B, int max_blocks, int max_chunks)
     ScoredWorkspace w;
     w.attention = align256(workspace_layout(B, max_chunks).total());
     w.scores = align256((size_t)B * kHq * max_blocks * kPage * sizeof(float));
-    w.lse = align256((size_t)B * kHq * sizeof(float));
+    w.logs = align256((size_t)B * kHq * sizeof(float));
     return w;
 }
 
@@ -184,7 +199,9 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     char *base = static_cast<char *>(workspace);
     ScoredPages<true> sel;
     sel.scores = reinterpret_cast<float *>(base + w.attention);
-    sel.lse = reinterpret_cast<float *>(base + w.attention + w.scores);
+    sel.logs = reinterpret_cast<float *>(base + w.attention + w.scores);
+    sel.max_chunks = (max_blocks + ppc - 1) / ppc;
+    sel.tops = reinterpret_cast<float2 *>(base + workspace_layout(B, sel.max_chunks).ml_offset());
     sel.tokens = max_blocks * kPage;
     sel.acc = acc;
     sel.acc_out = acc_out;
@@ -210,12 +227,13 @@ extern "C" int pkv_decode_scored(const pkv_pool *pool, const uint16_t *q, const 
     // 16.9; but 8 up to 4096 20 instead of 18, 8 up to 8192 34 instead of 27)
     if (sel.tokens <= (B * kHkv >= 3 * 152 ? 16384 : 2048))
         return launch_fused<false>(pool, a, sel, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
-    const ScoredPages<false> apart = {sel.scores, sel.lse, sel.tokens, acc, acc_out, acc_stride};
+    const ScoredPages<false> apart = {sel.scores, sel.logs, sel.tops, sel.max_chunks, sel.tokens,
+                                      acc,        acc_out,  acc_stride};
     if (const int st = launch_fused<false>(pool, a, apart, B, max_blocks, max_blocks, 0, ppc, workspace, s, options);
         st != PKV_OK)
         return st;
     const dim3 grid((sel.tokens + kAccTokens - 1) / kAccTokens, kHkv, B);
     return launch_kernel(accumulate_kernel, grid, dim3(kAccThreads), 0, s, !(options & PKV_STEP_NO_PDL),
-                         reinterpret_cast<const float4 *>(sel.scores), static_cast<const float *>(sel.lse), seq_lens_dev,
-                         max_blocks, acc, acc_out, acc_stride);
+                         reinterpret_cast<const float4 *>(sel.scores), static_cast<const float *>(sel.logs),
+                         static_cast<const float2 *>(sel.tops), sel.max_chunks, seq_lens_dev, max_blocks, acc, acc_out, acc_stride);
 }
