@@ -32,7 +32,8 @@ Long contexts: an engine with ``window=W`` (and ``sinks=S``) attends to the last
 S tokens in every step; ``attention_shared`` attends for groups of sequences behind a shared
 prefix, ``attention_scored`` also gathers every cached token's weight, and ``evict`` cuts the
 caches to a budget by those weights (``append`` with ``slots`` then puts a token behind a cut
-cache: its position is no longer its slot).
+cache: its position is no longer its slot).  ``pages_per_chunk=0`` leaves the size of the work
+units to the library in all of these (the step's, where it has a window).
 """
 from __future__ import annotations
 
@@ -78,9 +79,8 @@ class DecodeEngine:
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
         # the attention workspace (the fused step's too) starts with per-(sequence, KV head)
         # merge counters that must be zero before the first call (every call leaves them zero)
-        self.ws_bytes = pkv.pkv_decode_workspace_bytes(batch, max_blocks, pages_per_chunk)
+        self.ws_bytes = self.step_ws_bytes = self._attention_bytes()
         self.workspace = torch.zeros(max(self.ws_bytes, 16), dtype=torch.uint8, device=self.device)
-        self.step_ws_bytes = pkv.pkv_decode_step_workspace_bytes(batch, max_blocks, pages_per_chunk)
         self.step_ws = self.workspace
         self.fused = fused
         # launch options of the fused step and of the separate path's attention call
@@ -96,6 +96,15 @@ class DecodeEngine:
         self.chain_streams = [torch.cuda.Stream(device=self.device) for _ in range(chains)] if chains > 1 else []
         self.chain_ws = [torch.zeros(self.step_ws_bytes, dtype=torch.uint8, device=self.device)
                          for _ in range(chains)] if chains > 1 else []
+
+    def _attention_bytes(self) -> int:
+        """Workspace of the step's attention calls (fused and separate alike) for any rows of the batch."""
+        if not self.window:
+            return pkv.pkv_decode_workspace_bytes(self.batch, self.max_blocks, self.pages_per_chunk)
+        # the library's own units (pages_per_chunk 0) are finer for fewer rows, as chains have them
+        sizes = range(1, self.batch + 1) if self.pages_per_chunk == 0 else (self.batch,)
+        return max(pkv.pkv_decode_window_workspace_bytes(b, self.max_blocks, self.window, self.sinks, self.pages_per_chunk)
+                   for b in sizes)
 
     # ------------------------------------------------------------------ setup
     def pool_view(self) -> torch.Tensor:
@@ -438,24 +447,29 @@ class DecodeEngine:
         return kept[-1]
 
     def attention_shared(self, layer: int, q, seq_lens_dev, group_starts_dev, prefix_pages_dev, max_prefix_pages: int,
-                         out, stream=None, prefix_pages_per_chunk: int = 0) -> None:
+                         out, stream=None, prefix_pages_per_chunk: int = 0, pages_per_chunk: int | None = None) -> None:
         """pkv_decode_shared of one layer over the engine's batch: group i is rows group_starts[i] ..
-        group_starts[i + 1] - 1, behind the first prefix_pages[i] pages of its first row."""
+        group_starts[i + 1] - 1, behind the first prefix_pages[i] pages of its first row.  Work units of
+        ``pages_per_chunk`` pages (None: the engine's; 0: the library's choice)."""
+        ppc = self.pages_per_chunk if pages_per_chunk is None else pages_per_chunk
         groups = prefix_pages_dev.numel()
-        args = (self.batch, self.max_blocks, groups, max_prefix_pages, self.pages_per_chunk, prefix_pages_per_chunk)
+        args = (self.batch, self.max_blocks, groups, max_prefix_pages, ppc, prefix_pages_per_chunk)
         nbytes = pkv.pkv_decode_shared_workspace_bytes(*args)
         pkv.pkv_decode_shared(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, group_starts_dev,
-                              prefix_pages_dev, groups, max_prefix_pages, self.scale, self.pages_per_chunk,
+                              prefix_pages_dev, groups, max_prefix_pages, self.scale, ppc,
                               prefix_pages_per_chunk, self._workspace("shared", nbytes, stream), nbytes, out, self.err,
                               stream, self.step_options & ~pkv.PKV_STEP_SORTED)
 
-    def attention_scored(self, layer: int, q, seq_lens_dev, acc, acc_out, out, stream=None) -> None:
+    def attention_scored(self, layer: int, q, seq_lens_dev, acc, acc_out, out, stream=None,
+                         pages_per_chunk: int | None = None) -> None:
         """pkv_decode_scored of one layer: acc_out = acc + the weights (float32 [batch][8][n] with
-        n >= 16 * max_blocks, contiguous; they may be one tensor)."""
+        n >= 16 * max_blocks, contiguous; they may be one tensor).  ``pages_per_chunk`` as for
+        ``attention_shared``."""
+        ppc = self.pages_per_chunk if pages_per_chunk is None else pages_per_chunk
         stride = self._acc_stride(acc, acc_out)
-        nbytes = pkv.pkv_decode_scored_workspace_bytes(self.batch, self.max_blocks, self.pages_per_chunk)
+        nbytes = pkv.pkv_decode_scored_workspace_bytes(self.batch, self.max_blocks, ppc)
         pkv.pkv_decode_scored(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, self.scale, acc,
-                              acc_out, stride, self.pages_per_chunk, self._workspace("scored", nbytes, stream),
+                              acc_out, stride, ppc, self._workspace("scored", nbytes, stream),
                               nbytes, out, self.err, stream, self.step_options)
 
     def evict(self, layer: int, seq_lens, acc, keep: int, recent: int, sinks: int = 0, stream=None) -> np.ndarray:

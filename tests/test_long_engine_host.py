@@ -8,6 +8,7 @@ import numpy as np
 import pytest
 import torch
 
+from paged_kv_decode_12_gb300 import pkv
 from paged_kv_decode_12_gb300.engine import DecodeEngine
 
 
@@ -60,3 +61,20 @@ def test_new_tables_go_where_the_old_ones_were(bare):
     bare.set_tables(own)
     own[:] = -5
     assert np.array_equal(bare.bt.numpy(), second)
+
+
+def test_workspace_of_a_windowed_engine(bare):
+    """What the window's calls need for any rows of the batch: not a whole table's, and not nothing where the
+    library chooses the units (smaller batches are cut finer)."""
+    need = pkv.pkv_decode_window_workspace_bytes
+    bare.batch, bare.max_blocks, bare.window, bare.sinks = 256, 2048, 4096, 16
+    for ppc in (1, 16, 128):
+        bare.pages_per_chunk = ppc
+        assert bare._attention_bytes() == need(256, 2048, 4096, 16, ppc) < pkv.pkv_decode_workspace_bytes(256, 2048, ppc)
+    bare.pages_per_chunk = 0
+    assert bare._attention_bytes() >= max(need(b, 2048, 4096, 16, 0) for b in (1, 2, 3, 5, 8, 64, 100, 256)) > 0
+    bare.batch, bare.max_blocks, bare.window, bare.sinks = 64, 63, 1000, 5
+    assert bare._attention_bytes() >= max(need(b, 63, 1000, 5, 0) for b in range(1, 65)) > need(64, 63, 1000, 5, 0)
+    bare.window = bare.sinks = 0
+    bare.pages_per_chunk = 20
+    assert bare._attention_bytes() == pkv.pkv_decode_workspace_bytes(64, 63, 20)
