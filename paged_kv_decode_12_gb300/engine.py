@@ -453,6 +453,9 @@ class DecodeEngine:
         ``pages_per_chunk`` pages (None: the engine's; 0: the library's choice)."""
         ppc = self.pages_per_chunk if pages_per_chunk is None else pages_per_chunk
         groups = prefix_pages_dev.numel()
+        for t, n in ((group_starts_dev, groups + 1), (prefix_pages_dev, max(groups, 1))):
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device.type != self.device.type:
+                raise ValueError("groups: int32, contiguous, on the engine's device; n + 1 starts for n prefixes")
         args = (self.batch, self.max_blocks, groups, max_prefix_pages, ppc, prefix_pages_per_chunk)
         nbytes = pkv.pkv_decode_shared_workspace_bytes(*args)
         pkv.pkv_decode_shared(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, self.batch, group_starts_dev,

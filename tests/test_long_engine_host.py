@@ -78,3 +78,27 @@ def test_workspace_of_a_windowed_engine(bare):
     bare.window = bare.sinks = 0
     bare.pages_per_chunk = 20
     assert bare._attention_bytes() == pkv.pkv_decode_workspace_bytes(64, 63, 20)
+
+
+def test_shared_refuses_groups_that_it_would_read_past(bare, monkeypatch):
+    """The bounds of n groups are n + 1 numbers; both arrays are read as int32 in a row."""
+    bare.batch, bare.max_blocks, bare.pages_per_chunk, bare.bt = 4, 8, 4, torch.zeros((1, 4, 8), dtype=torch.int32)
+    bare.scale, bare.err, bare.step_options = 0.125, None, 0
+    called = []
+    monkeypatch.setattr(pkv, "pkv_decode_shared", lambda *a: called.append(a))
+
+    def i32(*x):
+        return torch.tensor(x, dtype=torch.int32)
+
+    def call(starts, prefix):
+        bare.attention_shared(0, None, None, starts, prefix, 2, None)
+
+    for starts, prefix in ((i32(0, 4), i32(1, 1)), (i32(0, 2, 3, 4), i32(1, 1)), (i32(0), i32(1)), (i32(0, 4), i32()),
+                           (torch.tensor([0, 2, 4]), i32(1, 1)), (i32(0, 2, 4), torch.tensor([1, 1])),
+                           (i32(0, 9, 2, 9, 4)[::2], i32(1, 1)), (i32(0, 2, 4), i32(1, 9, 1)[::2]),
+                           (i32(0, 2, 4).to("meta"), i32(1, 1)), (i32(0, 2, 4), i32(1, 1).to("meta"))):
+        with pytest.raises(ValueError):
+            call(starts, prefix)
+    assert not called
+    call(i32(0, 2, 4), i32(1, 1))
+    assert len(called) == 1
