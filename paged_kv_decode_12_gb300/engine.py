@@ -426,8 +426,9 @@ class DecodeEngine:
     def _acc_stride(self, *accs) -> int:
         for acc in accs:
             if (acc.dtype != torch.float32 or acc.shape != accs[0].shape or not acc.is_contiguous() or
-                    acc.dim() != 3 or acc.shape[:2] != (self.batch, wl.NUM_KV_HEADS)):
-                raise ValueError("weights: float32 [batch][8][n], contiguous")
+                    acc.device.type != self.device.type or acc.dim() != 3 or
+                    acc.shape[:2] != (self.batch, wl.NUM_KV_HEADS)):
+                raise ValueError("weights: float32 [batch][8][n], contiguous, on the engine's device")
         return acc.shape[-1]
 
     def _workspace(self, call: str, nbytes: int, stream):

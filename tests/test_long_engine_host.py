@@ -102,3 +102,12 @@ def test_shared_refuses_groups_that_it_would_read_past(bare, monkeypatch):
     assert not called
     call(i32(0, 2, 4), i32(1, 1))
     assert len(called) == 1
+
+
+def test_weights_on_another_device_are_refused(bare):
+    bare.batch = 2
+    good = torch.zeros(2, 8, 32)
+    assert bare._acc_stride(good, good) == 32
+    for bad in (good.to("meta"), good.double(), good[:, :, ::2], good[:1], good[0]):
+        with pytest.raises(ValueError):
+            bare._acc_stride(good, bad)
