@@ -476,15 +476,19 @@ class DecodeEngine:
                               acc_out, stride, ppc, self._workspace("scored", nbytes, stream),
                               nbytes, out, self.err, stream, self.step_options)
 
-    def evict(self, layer: int, seq_lens, acc, keep: int, recent: int, sinks: int = 0, stream=None) -> np.ndarray:
+    def evict(self, layer: int, seq_lens, acc, keep: int, recent: int, sinks: int = 0, stream=None,
+              room: int = 0) -> np.ndarray:
         """Cut one layer's caches (lengths ``seq_lens``, host int32) to ``keep`` tokens per KV head by
-        ``acc`` (pkv_evict), in place in ``acc``: new pages are taken from the pool, the table's rows
-        are pointed at them, and the old pages given back (work on the stream so far still reads them;
-        later work on it comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the
-        table of all layers in step: each layer is cut by its own call with the same arguments.
+        ``acc`` (pkv_evict), in place in ``acc``: new pages are taken from the pool, enough for each cut
+        cache and ``room`` tokens more (as far as the table is wide), the table's rows are pointed at
+        them, and the old pages given back (work on the stream so far still reads them; later work on it
+        comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the table of all layers in
+        step: each layer is cut by its own call with the same arguments.
         A row names all of its sequence's pages; rows may share some (a prefix), and no longer do
         after it.  Every page must be the caller's to give back (allocated, and not a scheduler's:
         a PkvError otherwise, with nothing done).  Cannot be captured."""
+        if room < 0:
+            raise ValueError("room: a number of tokens")
         lens = np.asarray(seq_lens, dtype=np.int32)
         if lens.shape != (self.batch,) or lens.min() < 0 or lens.max() > wl.PAGE_SIZE * self.max_blocks:
             raise ValueError("seq_lens: a length within the table's width for every sequence")
@@ -497,7 +501,8 @@ class DecodeEngine:
         old = np.unique(old[old >= 0])
         pkv.pkv_pool_check(self.pool, old)
         after = np.minimum(lens, keep).astype(np.int32)
-        need = (after + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
+        last = np.minimum(after.astype(np.int64) + room, wl.PAGE_SIZE * self.max_blocks)
+        need = (last + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
         nbytes = pkv.pkv_evict_workspace_bytes(self.batch, keep)
         workspace = self._workspace("evict", nbytes, stream)
         ids = pkv.pkv_pool_alloc(self.pool, int(need.sum()))
