@@ -498,7 +498,8 @@ int pkv_decode_window(const pkv_pool *pool, const uint16_t *q, const int32_t *bt
                       void *cuda_stream, int options);
 
 /* pkv_decode_step with pkv_decode_window's attention: append and attention in one
- * launch, bit-identical to pkv_append_rope followed by pkv_decode_window. */
+ * launch, bit-identical to pkv_append_rope followed by pkv_decode_window.  The workspace
+ * is always needed. */
 int pkv_decode_step_window(const pkv_pool *pool, const uint16_t *k_new, const uint16_t *v_new, uint16_t *q,
                            const int32_t *bt_dev, int max_blocks, const int32_t *seq_lens_dev, int B,
                            const float *rope_table, int max_pos, float scale, int window, int sinks,
@@ -511,8 +512,11 @@ size_t pkv_decode_window_workspace_bytes(int B, int max_blocks, int window, int 
 /* ------------------------------------------------------------- a shared prefix */
 
 /* Paged decode attention for groups of sequences that share a prefix, for one layer:
- * pkv_decode_attention's result, with every shared page read once for its whole group
- * instead of once per sequence.  The pages have no counterpart.
+ * pkv_decode_attention's definition, with every shared page read once for its whole group
+ * instead of once per sequence.  The pages have no counterpart.  The prefix's softmax
+ * weights are rounded to BF16 for the product with the values (2^-8 each), on FP8 pages
+ * too, where pkv_decode_attention rounds them to FP16; the softmax's sum is of the rounded
+ * weights.  Values up to 2^45 in size give finite results.
  *   group_starts_dev int32 [groups + 1]: group i is the sequences group_starts[i] ..
  *              group_starts[i + 1] - 1 (group_starts[0] = 0, group_starts[groups] = B,
  *              increasing);

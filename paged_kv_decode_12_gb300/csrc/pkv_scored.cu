@@ -8,7 +8,7 @@
 // pkv_step.cuh goes over every page and also stores the scores (log2 domain, FP32, the four heads
 // of a token side by side); the unit that finishes a (sequence, KV head) knows each head's maximum M
 // and log2 of its sum l and turns the scores into weights, 2^((x - M) - log2 l).  (Not 2^(x - (M +
-// log2 l)): that sum's rounding at M would be every weight's, 1e-4 of it at an M of 2000.)  For short rows it does so itself, while other units
+// log2 l)): that sum's rounding at M would be every weight's, up to 4e-5 of it at an M of 2000.)  For short rows it does so itself, while other units
 // stream their pages; a long row would keep one CTA busy behind all others, so there a second
 // launch does it, one (KV head, token) per thread.
 // Either way 128 bytes per token are re-read where a second pass over the keys would read 1024

@@ -527,7 +527,7 @@ struct RowScales {
 };
 
 // 32 scores of one query row (columns 32 k ..) as weights 2^(S c - m): their sum, and the weights
-// in pairs rounded to BF16 (half a step, 2^-9) for the second product: what the matrix instruction
+// in pairs rounded to BF16 (half a step, 2^-8) for the second product: what the matrix instruction
 // takes beside BF16 values.  MASK: columns of pages from `pages` on weigh nothing.  Four chains of
 // sums, so that no chain's latency is the time of the whole.
 //
@@ -582,10 +582,12 @@ __device__ __forceinline__ float max_score(uint32_t ts, int k, const Scale &sc, 
 // half tile's weights sum to 2^64 or more: FP32 and BF16 hold 2^127, so m, l and O remain a
 // valid log-sum-exp triple that far above m, and no maximum is taken on the way.  (Moving m for
 // every score 2^8 above it, as narrower types need, made most half tiles of 32 rows rescale O.)
+// O is finite for values up to 2^45: 2^64 times that, over at most 2^18 half tiles.
 constexpr float kMostWeight = 18446744073709551616.f;
 
 // An item's first half tile: the row's maximum.  (Not inlined: the loop would pay for its
-// registers; 256 sequences behind 32768 tokens 94 us instead of 91.)
+// registers; 256 sequences behind 32768 tokens 94.5 us instead of 95.1, though 4 behind 512 tokens
+// 7.5 instead of 7.2.)
 template <class Scale>
 __device__ __noinline__ float first_reference(uint32_t ts, Scale sc, int pages)
 {
@@ -867,10 +869,10 @@ constexpr int kSms = 152;
 // 1.05 us, FP8 pages, which are converted, 1.85 us): an item costs 3.3 (1) besides its own, and
 // every chunk 0.42 (0.12) of merging and 0.5 (0.1) more for every 256 sequences.  Of several
 // groups the others are taken to be half as long as the longest.  Measured with chunks of 8 / 16 /
-// 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 322 / 208 / 148 / 114 / 99 / 91; 64
-// sequences, 128 pages 21 / 19 / 16 / 19 / 27; 16 sequences, 512 pages 24 / 17 / 13 / 16 / 24 / 61, FP8
-// 26 / 18 / 19 / 23 / 37 / 100; 200 sequences in 3 groups, 500 FP8 pages 74 / 54 / 44 / 39 / 47; 4
-// sequences, 32 pages 7.1 / 8.1 / 9.1.
+// 32 / 64 / 128 / 512 pages (us): 256 sequences, 2048 pages 323 / 216 / 151 / 115 / 101 / 93; 64
+// sequences, 128 pages 21 / 19 / 16 / 19 / 28; 16 sequences, 512 pages 24 / 16 / 14 / 17 / 25 / 64, FP8
+// 27 / 20 / 20 / 27 / 43 / 102; 200 sequences in 3 groups, 500 FP8 pages 69 / 53 / 45 / 41 / 52; 4
+// sequences, 32 pages 7.6 / 8.7 / 9.8.
 int default_prefix_chunk(int B, int groups, int max_prefix, bool fp8)
 {
     const int tiles = (max_prefix + kTilePages - 1) / kTilePages;
