@@ -173,7 +173,7 @@ class ClockSampler:
 
 
 # the sources the fused step kernels are built from (kernels, policies, tensor maps)
-KERNEL_SOURCES = ("pkv_device.cuh", "pkv_fp8.cuh", "pkv_step.cu", "pkv_host.cpp", "pkv_internal.h")
+KERNEL_SOURCES = ("pkv_device.cuh", "pkv_fp8.cuh", "pkv_step.cu", "pkv_step.cuh", "pkv_host.cpp", "pkv_internal.h")
 
 
 def kernel_source_digest() -> str:
