@@ -484,7 +484,8 @@ class DecodeEngine:
         them, and the old pages given back (work on the stream so far still reads them; later work on it
         comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the table of all layers in
         step: each layer is cut by its own call with the same arguments.
-        A row names all of its sequence's pages; rows may share some (a prefix), and no longer do
+        A row names all of its sequence's pages (a ValueError otherwise: it need not for
+        ``attention_shared`` or behind a window); rows may share some (a prefix), and no longer do
         after it.  Every page must be the caller's to give back (allocated, and not a scheduler's:
         a PkvError otherwise, with nothing done).  Cannot be captured."""
         if room < 0:
@@ -498,6 +499,9 @@ class DecodeEngine:
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("an eviction takes and gives back pages on the host: it cannot be captured")
         old = self.bt_host[layer]
+        pages = (lens + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
+        if ((old < 0) & (np.arange(self.max_blocks)[None, :] < pages[:, None])).any():
+            raise ValueError("a row of the table lacks pages of its sequence")
         old = np.unique(old[old >= 0])
         pkv.pkv_pool_check(self.pool, old)
         after = np.minimum(lens, keep).astype(np.int32)

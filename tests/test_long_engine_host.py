@@ -111,3 +111,23 @@ def test_weights_on_another_device_are_refused(bare):
     for bad in (good.to("meta"), good.double(), good[:, :, ::2], good[:1], good[0]):
         with pytest.raises(ValueError):
             bare._acc_stride(good, bad)
+
+
+def test_evictions_refuse_rows_that_lack_pages(bare):
+    """Rows behind a shared prefix may have no entries for it, and rows of a window none for what has slid out: an
+    eviction would find no rows there, and give back the pages that hold the rest."""
+    bare.pool = pkv.pkv_pool_create(0x7F0000000000, 20 * pkv.PKV_PAGE_BYTES)
+    bare.layers, bare.batch, bare.max_blocks, bare.bt, bare.err = 1, 2, 4, None, None
+    own = pkv.pkv_pool_alloc(bare.pool, 6)
+    whole = np.full((1, 2, 4), -1, dtype=np.int32)
+    whole[0, 0, :3], whole[0, 1, :3] = own[:3], own[3:]
+    acc = torch.zeros(2, 8, 64)
+    for hole, lens in (((0, 1, 0), [48, 48]), ((0, 0, 2), [33, 1]), ((0, 1, 1), [16, 17])):
+        bt = whole.copy()
+        bt[hole] = -1
+        bare.set_tables(bt)
+        with pytest.raises(ValueError, match="pages"):
+            bare.evict(0, np.array(lens, np.int32), acc, 20, 4, 1)
+        assert pkv.pkv_pool_info(bare.pool)["num_free"] == 14 and np.array_equal(bare.bt_host, bt)
+    pkv.pkv_pool_destroy(bare.pool)
+    bare.pool = None
