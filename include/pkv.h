@@ -81,6 +81,7 @@ extern "C" {
 #define PKV_DEVERR_PAGE_RANGE 0x1  /* a block-table entry outside [0, num_pages) */
 #define PKV_DEVERR_LENGTH 0x2      /* seq_len < 1, seq_len > max_blocks*16, or pos out of range */
 #define PKV_DEVERR_TIMEOUT 0x4     /* a bounded wait on a copy barrier gave up */
+#define PKV_DEVERR_PAGES 0x8       /* a list of pages to take from is used up (pkv_chunk_tables) */
 
 /* decode kernel variants (pkv_decode_attention_variant) */
 #define PKV_DECODE_DEFAULT 0 /* the fastest measured variant */
@@ -617,6 +618,96 @@ int pkv_append_rope_at(const pkv_pool *pool, const uint16_t *k_new, const uint16
                        uint16_t *q_out, const int32_t *bt_dev, int max_blocks, const int32_t *pos_dev,
                        const int32_t *slots_dev, int B, const float *rope_table, int max_pos, int32_t *dev_err_flag,
                        void *cuda_stream);
+
+/* ------------------------------------------------------------ chunks of new tokens */
+
+/* A step whose sequences bring several tokens each -- prompts, pieces of prompts -- beside those
+ * that bring one or none: T tokens side by side, sequence b's being starts[b] .. starts[b + 1] - 1.
+ * pkv_chunk_tables makes the step's tables and slots, then every layer runs pkv_chunk_append and
+ * pkv_chunk_attention.  The pages have no counterpart ("Prefill 與 Decode" of the Tiny-vLLM overview
+ * keeps the two apart).  T is the arrays' size: a captured graph is replayed with fewer tokens,
+ * those behind starts[B] being padding.  Up to 4096 sequences a call. */
+
+/* Block tables extended, positions and slots of the new tokens, made on the GPU, for all layers.
+ * Sequence b holds seq_lens[b] tokens (its table rows name their pages) and brings new[b] >= 0.
+ *   bt_dev     int32 [layers][B][max_blocks]: the new pages' entries are written, layer by layer and
+ *              sequence by sequence, from the list; the others stay as they are
+ *   pages_dev  int32 [pages]: page ids to take (e.g. from pkv_pool_alloc); the first *pages_used_dev
+ *              are taken already.  They must be distinct and nobody else's
+ *   pages_used_out  int32: those taken after the call; may be pages_used_dev itself
+ *   starts_out int32 [B + 1]: prefix sums of new
+ *   seq_lens_out int32 [B]: seq_lens + new; may be seq_lens_dev itself
+ *   pos_out    int32 [max_tokens]: the new tokens' positions; 0 behind the last
+ *   slots_out  int64 [layers][max_tokens]: 16 * page + place in it; -1 behind the last
+ *   workspace  >= pkv_chunk_tables_workspace_bytes(B) bytes, 16-byte aligned, zero before the FIRST
+ *              call; every call leaves it zero.  Calls sharing it must not overlap on the GPU.
+ * Device checks: a row with a negative count or one that does not fit the table brings nothing (its
+ * length stays) and sets PKV_DEVERR_LENGTH; more than max_tokens tokens set PKV_DEVERR_LENGTH, and a list
+ * that is too short PKV_DEVERR_PAGES: then no row brings anything and no page is taken.  A page
+ * id outside the pool sets PKV_DEVERR_PAGE_RANGE; the slots in it are -1 (and its entry, of a new page).
+ * The next pkv_decode_* launch on this pool, and the next one on this stream, go without
+ * programmatic dependent launch, because they may read these lengths and tables. */
+int pkv_chunk_tables(const pkv_pool *pool, const int32_t *seq_lens_dev, const int32_t *new_dev, int B, int32_t *bt_dev,
+                     int max_blocks, int layers, const int32_t *pages_dev, int pages, const int32_t *pages_used_dev,
+                     int32_t *pages_used_out, int max_tokens, int32_t *starts_out, int32_t *seq_lens_out,
+                     int32_t *pos_out, int64_t *slots_out, void *workspace, size_t workspace_bytes,
+                     int32_t *dev_err_flag, void *cuda_stream);
+
+size_t pkv_chunk_tables_workspace_bytes(int B);
+
+/* Norms of the query and key heads, rotation, and append of T tokens, for one layer.  A head's row x:
+ *     y = R(x * w) / sqrt(mean(x^2) + eps)    (without weights: R(x))
+ * in FP32 (the number next to the exact one), rounded to BF16 (FP8 pools: key rows are then quantized as pkv_append_rope does).  R turns
+ * the pairs (i, i + 32) by pos * theta^(-2i/64), from the table.  Without norms the
+ * results are pkv_append_rope's bit for bit.
+ *   k, v       [T][8][64], token t at k + t * k_stride (BF16 elements, at least 512, a multiple of 4)
+ *   q, q_out   [T][32][64]: rows of q at q_stride (at least 2048, a multiple of 4), q_out contiguous;
+ *              q_out may be q where q_stride is 2048.  Both may be NULL
+ *   q_norm, k_norm  BF16 [64]: weights of the norms; NULL (both, where there is a q): no norms.  eps > 0 with
+ *              norms.  (Weights up to 2^60 in size; rows of any finite values.)
+ *   slots_dev  int64 [T]: the rows go to page slot / 16, place slot % 16; -1: the token is padding and
+ *              nothing of it is written.  Slots of a call must be distinct (one that is not ends up
+ *              with rows of either token)
+ *   pos_dev    int32 positions: one a token [T] (axis_pairs NULL), or three axes (e.g. time, height, width)
+ *              [3][pos_stride], pos_stride >= T: the first axis_pairs[0] pairs turn by the first,
+ *              the next axis_pairs[1] by the second, the last axis_pairs[2] by the third; axis_pairs
+ *              is a host array that sums to 32
+ * k, v, q, q_out and the weights 8-byte, the rope table 16-byte aligned.
+ * Device checks: a slot outside the pool sets PKV_DEVERR_PAGE_RANGE, a position outside [0, max_pos)
+ * PKV_DEVERR_LENGTH; nothing of that token is written.
+ * The next pkv_decode_* launch on this pool, and the next one on this stream, go without
+ * programmatic dependent launch, because they may read these pages. */
+int pkv_chunk_append(const pkv_pool *pool, const uint16_t *k, int64_t k_stride, const uint16_t *v, int64_t v_stride,
+                     const uint16_t *q, int64_t q_stride, uint16_t *q_out, const uint16_t *q_norm,
+                     const uint16_t *k_norm, float eps, const int64_t *slots_dev, const int32_t *pos_dev,
+                     int64_t pos_stride, const int32_t *axis_pairs, int T, const float *rope_table, int max_pos,
+                     int32_t *dev_err_flag, void *cuda_stream);
+
+/* Causal attention of the new tokens over their sequences' pages, for one layer.  Sequence b's n =
+ * starts[b + 1] - starts[b] tokens are its last n (they are in its pages already): token starts[b] + i
+ * has position p = seq_lens[b] - n + i, and
+ *     out[t][h] = sum_j softmax_j(scale * q[t][h] . K_j) V_j   over j <= p
+ * and, with a window > 0, of those with j > p - window or j < sinks (a token by itself: what
+ * pkv_decode_window gives).  Only pages that hold such tokens are read and looked up.
+ *   q, out     BF16 [T][32][64] (16-byte aligned); rows behind starts[B] are neither read nor written
+ *   seq_lens_dev int32 [B], after the append; starts_dev int32 [B + 1], starts[0] = 0, starts[B] <= T.
+ *              A sequence without new tokens is not looked at
+ *   workspace  >= pkv_chunk_attention_workspace_bytes(B, T) bytes, 16-byte aligned, zero before the FIRST
+ *              call (its counters are zero after every call).  Calls sharing it must not overlap on the GPU.
+ *   options    0, or PKV_STEP_NO_PDL | PKV_STEP_TEST_EXPIRE_WAIT
+ * Results are the same from run to run; in another batch they may differ by rounding.
+ * What is not attended to has no effect, whatever is there (NaN included).
+ * Launch: programmatic dependent launch, everything read behind the dependency wait.
+ * Device checks: starts that decrease or leave [0, T], a sequence shorter than its new tokens or longer
+ * than its table set PKV_DEVERR_LENGTH; a page id outside the pool PKV_DEVERR_PAGE_RANGE.  Outputs of
+ * the tokens concerned are zeros (of a bad page: those of the tokens that are worked on together
+ * with one that attends to it; tokens that starts places nowhere have none). */
+int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
+                        const int32_t *seq_lens_dev, const int32_t *starts_dev, int B, int T, float scale, int window,
+                        int sinks, void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *dev_err_flag,
+                        void *cuda_stream, int options);
+
+size_t pkv_chunk_attention_workspace_bytes(int B, int T);
 
 /* ------------------------------------------------------------------ misc */
 

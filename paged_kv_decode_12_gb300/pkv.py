@@ -37,6 +37,7 @@ PKV_ERR_WORKSPACE_TOO_SMALL = -8
 PKV_DEVERR_PAGE_RANGE = 0x1
 PKV_DEVERR_LENGTH = 0x2
 PKV_DEVERR_TIMEOUT = 0x4
+PKV_DEVERR_PAGES = 0x8
 
 PKV_DECODE_DEFAULT = 0
 PKV_DECODE_SIMT = 1
@@ -586,12 +587,81 @@ def pkv_append_rope_at(pool, k_new, v_new, q, q_out, bt_dev, max_blocks: int, po
                                     _stream(stream)), "pkv_append_rope_at")
 
 
+# ---------------------------------------------------------------------------- chunks of new tokens
+
+EXPORTED = EXPORTED + (
+    "pkv_chunk_tables", "pkv_chunk_tables_workspace_bytes", "pkv_chunk_append", "pkv_chunk_attention",
+    "pkv_chunk_attention_workspace_bytes",
+)
+
+_lib_long = lib
+
+
+def lib():  # noqa: F811 -- extends the loader with the signatures of chunks
+    L = _lib_long()
+    if not getattr(L, "_pkv_chunk_bound", False):
+        f, z, i64 = ctypes.c_float, ctypes.c_size_t, ctypes.c_int64
+        L.pkv_chunk_tables.argtypes = [_vp, _vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp,
+                                       _vp, _vp, z, _vp, _vp]
+        L.pkv_chunk_tables_workspace_bytes.argtypes = [_i32]
+        L.pkv_chunk_append.argtypes = [_vp, _vp, i64, _vp, i64, _vp, i64, _vp, _vp, _vp, f, _vp, _vp, i64, _i32p, _i32,
+                                       _vp, _i32, _vp, _vp]
+        L.pkv_chunk_attention.argtypes = [_vp, _vp, _vp, _i32, _vp, _vp, _i32, _i32, f, _i32, _i32, _vp, z, _vp, _vp,
+                                          _vp, _i32]
+        L.pkv_chunk_attention_workspace_bytes.argtypes = [_i32] * 2
+        for name in EXPORTED[-5:]:
+            getattr(L, name).restype = z if name.endswith("_workspace_bytes") else ctypes.c_int
+        L._pkv_chunk_bound = True
+    return L
+
+
+def pkv_chunk_tables_workspace_bytes(B: int) -> int:
+    return int(lib().pkv_chunk_tables_workspace_bytes(B))
+
+
+def pkv_chunk_tables(pool, seq_lens_dev, new_dev, B: int, bt_dev, max_blocks: int, layers: int, pages_dev, pages: int,
+                     pages_used_dev, pages_used_out, max_tokens: int, starts_out, seq_lens_out, pos_out, slots_out,
+                     workspace, workspace_bytes: int, dev_err_flag=None, stream=None) -> None:
+    _check(lib().pkv_chunk_tables(pool, _ptr(seq_lens_dev), _ptr(new_dev), B, _ptr(bt_dev), max_blocks, layers,
+                                  _ptr(pages_dev), int(pages), _ptr(pages_used_dev), _ptr(pages_used_out),
+                                  int(max_tokens), _ptr(starts_out), _ptr(seq_lens_out), _ptr(pos_out),
+                                  _ptr(slots_out), _ptr(workspace), int(workspace_bytes), _ptr(dev_err_flag),
+                                  _stream(stream)), "pkv_chunk_tables")
+
+
+def pkv_chunk_append(pool, k, k_stride: int, v, v_stride: int, q, q_stride: int, q_out, q_norm, k_norm, eps: float,
+                     slots_dev, pos_dev, pos_stride: int, axis_pairs, T: int, rope_table, max_pos: int,
+                     dev_err_flag=None, stream=None) -> None:
+    """``axis_pairs``: None, or the rotation pairs of each of three position axes (host integers)."""
+    if axis_pairs is not None:
+        if len(axis_pairs) != 3:
+            raise ValueError("axis_pairs: the pairs of three axes")
+        axis_pairs = (ctypes.c_int32 * 3)(*axis_pairs)
+    _check(lib().pkv_chunk_append(pool, _ptr(k), int(k_stride), _ptr(v), int(v_stride), _ptr(q), int(q_stride),
+                                  _ptr(q_out), _ptr(q_norm), _ptr(k_norm), float(eps), _ptr(slots_dev), _ptr(pos_dev),
+                                  int(pos_stride), axis_pairs, int(T), _ptr(rope_table), max_pos, _ptr(dev_err_flag),
+                                  _stream(stream)), "pkv_chunk_append")
+
+
+def pkv_chunk_attention_workspace_bytes(B: int, T: int) -> int:
+    return int(lib().pkv_chunk_attention_workspace_bytes(B, T))
+
+
+def pkv_chunk_attention(pool, q, bt_dev, max_blocks: int, seq_lens_dev, starts_dev, B: int, T: int, scale: float,
+                        window: int, sinks: int, workspace, workspace_bytes: int, out, dev_err_flag=None, stream=None,
+                        options: int = 0) -> None:
+    _check(lib().pkv_chunk_attention(pool, _ptr(q), _ptr(bt_dev), max_blocks, _ptr(seq_lens_dev), _ptr(starts_dev),
+                                     B, int(T), float(scale), int(window), int(sinks), _ptr(workspace),
+                                     int(workspace_bytes), _ptr(out), _ptr(dev_err_flag), _stream(stream),
+                                     int(options)), "pkv_chunk_attention")
+
+
 # ---------------------------------------------------------------------------- read-bandwidth probes
 
 # every symbol include/pkv_probe.h declares (a measurement aid, not the decode path)
 EXPORTED_PROBE = ("pkv_probe_read_ldg", "pkv_probe_read_bulk")
 
-_lib_long = lib
+_lib_chunk = lib
 
 
 _bound = None
@@ -600,7 +670,7 @@ _bound = None
 def lib():  # noqa: F811 -- extends the loader with the probe signatures
     global _bound
     if _bound is None:
-        L = _lib_long()
+        L = _lib_chunk()
         for name in EXPORTED_PROBE:
             getattr(L, name).argtypes = [_vp, ctypes.c_size_t, _vp, _i32, _vp]
             getattr(L, name).restype = ctypes.c_int
