@@ -1,0 +1,158 @@
+// pkv_chunk_plan.cuh -- how the attention of chunks is cut into pieces of work, one run of them a CTA.
+// Not part of the ABI.
+//
+// A sequence's new tokens make items: 64 tokens and one KV head (two row tiles of 128 query rows that go
+// through the same pages); the odd last 32 tokens, or fewer, and two KV heads (a row tile each); a
+// single token and one KV head (kind kSingle, warp-level products: its 4 rows would leave a row tile
+// all but empty).  An item goes through `nt` key tiles of 128 tokens and costs nt * tile + item.  All items laid
+// end to end make a line of length W, and CTA c of G works off what lies between c W / G and (c + 1) W / G: the
+// work is even whatever the lengths are, and an item that crosses a border is cut between
+// key tiles (not next to its ends: cut()), its parts joined by whoever finishes last.  At most one cut item begins and
+// at most one goes on in a CTA, which bounds the partial results to two a CTA.
+#pragma once
+
+#include <cstdint>
+
+#include "pkv_internal.h"
+
+namespace pkv {
+namespace plan {
+
+constexpr int kTileTokens = 128;   // of a key tile
+constexpr int kRowTokens = 32;     // of a row tile
+constexpr int kLeast = 2;          // key tiles of a part
+
+enum Kind { kEnd = 0, kPair = 1, kHeads = 2, kSingle = 3 };
+
+// What the kinds of items cost, in a common unit.
+struct Costs {
+    int tile[4], item[4];
+};
+
+#define PKV_HD __host__ __device__ __forceinline__
+
+PKV_HD int64_t imin(int64_t a, int64_t b) { return a < b ? a : b; }
+PKV_HD int64_t imax(int64_t a, int64_t b) { return a > b ? a : b; }
+
+// The pages that the tokens at positions first .. last attend to: entry i is page i below `sink`, i -
+// sink + from behind it.
+struct PageList {
+    int sink, from, count;
+    PKV_HD int page(int i) const { return i < sink ? i : i - sink + from; }
+    PKV_HD int tiles() const { return (count + kTileTokens / kPage - 1) / (kTileTokens / kPage); }
+};
+
+PKV_HD PageList page_list(int first, int last, int window, int sinks)
+{
+    PageList x;
+    x.from = window && first + 1 > window ? (first + 1 - window) / kPage : 0;
+    x.sink = (int)imin(((int64_t)sinks + kPage - 1) / kPage, x.from);
+    x.count = x.sink + last / kPage - x.from + 1;
+    return x;
+}
+
+// The items of one sequence of n new tokens, the first at position c.
+struct Sequence {
+    int n, c, window, sinks;
+    int pairs;       // items of 64 tokens a head; the last may be short
+    bool rest;       // and one of 32 or fewer for every two heads
+    int flat;        // key tiles of a pair once the window leaves the beginning (no window: beyond reach)
+    int tile, item;  // costs of pairs
+
+    PKV_HD Sequence(int n_, int c_, int window_, int sinks_, const Costs &k)
+        : n(n_), c(c_), window(window_), sinks(sinks_), tile(k.tile[kPair]), item(k.item[kPair])
+    {
+        const int rows = n == 1 ? 0 : (n + kRowTokens - 1) / kRowTokens;
+        pairs = rows / 2;
+        rest = (rows & 1) != 0;
+        flat = 1 << 30;
+        if (window) {
+            const int64_t lo = (int64_t)c + 1 - window;  // (floor of a negative number)
+            const int64_t from = lo >= 0 ? lo / kPage : -((-lo + kPage - 1) / kPage);
+            const int64_t span = ((int64_t)c + 2 * kRowTokens - 1) / kPage - from + 1;
+            const int64_t pages = ((int64_t)sinks + kPage - 1) / kPage + span;
+            flat = (int)imin((pages + kTileTokens / kPage - 1) / (kTileTokens / kPage), 1 << 30);
+        }
+    }
+    // Pages of pair r, of the rest, of a single token.
+    PKV_HD PageList pair_pages(int r) const
+    {
+        return page_list(c + 64 * r, c + (int)imin((int64_t)64 * r + 63, n - 1), window, sinks);
+    }
+    PKV_HD PageList rest_pages() const { return page_list(c + 64 * pairs, c + n - 1, window, sinks); }
+    PKV_HD PageList single_pages() const { return page_list(c, c, window, sinks); }
+
+    // Cost of the first r pairs of a head, none of them the last: a pair's tiles are min((c + 63 + 64 r) /
+    // 128 + 1, flat), two at a time one more each.
+    PKV_HD int64_t before(int r) const
+    {
+        const int64_t a = (int64_t)c + 63;
+        int64_t turn = (int64_t)128 * (flat - 1) - a;  // pairs below turn / 64 still grow
+        turn = turn <= 0 ? 0 : (turn + 63) / 64;
+        const int64_t grow = imin(turn, r), m = grow / 2, e = grow & 1;
+        const int64_t a0 = a / 128, a1 = (a + 64) / 128;
+        const int64_t tiles = m * (a0 + a1) + m * (m - 1) + e * (a0 + m) + grow + (r - grow) * flat;
+        return tiles * tile + (int64_t)r * item;
+    }
+    PKV_HD int64_t pair_cost(int r) const { return (int64_t)pair_pages(r).tiles() * tile + item; }
+    // Of all pairs of a head.
+    PKV_HD int64_t head_cost() const { return pairs ? before(pairs - 1) + pair_cost(pairs - 1) : 0; }
+    PKV_HD int64_t rest_cost(const Costs &k) const
+    {
+        return rest ? (int64_t)rest_pages().tiles() * k.tile[kHeads] + k.item[kHeads] : 0;
+    }
+    PKV_HD int64_t single_cost(const Costs &k) const
+    {
+        return n == 1 ? (int64_t)single_pages().tiles() * k.tile[kSingle] + k.item[kSingle] : 0;
+    }
+    PKV_HD int64_t cost(const Costs &k) const
+    {
+        return kHkv * (head_cost() + single_cost(k)) + kHkv / 2 * rest_cost(k);
+    }
+};
+
+// The line's borders: CTA c has border(c) .. border(c + 1).
+struct Line {
+    int64_t length;
+    int ctas;
+    PKV_HD int64_t border(int c) const { return length * c / ctas; }
+    // The first CTA whose end is not below x.
+    PKV_HD int ending_from(int64_t x) const { return (int)((x * ctas + length - 1) / length) - 1; }
+};
+
+// Key tiles of an item before a border that lies t into it.
+PKV_HD int cut(int64_t t, int nt, int tile, int item)
+{
+    if (t >= (int64_t)nt * tile + item)
+        return nt;
+    if (t < item + (int64_t)kLeast * tile)
+        return 0;
+    const int64_t j = (t - item) / tile;
+    return j > nt - kLeast ? nt : (int)j;
+}
+
+// The CTAs that take part in an item that begins at s: first .. first + count - 1.
+struct Parts {
+    int first, count;
+};
+
+PKV_HD Parts parts_of(const Line &line, int64_t s, int nt, int tile, int item)
+{
+    const int64_t cost = (int64_t)nt * tile + item;
+    const int64_t some = imin(cost, item + (int64_t)kLeast * tile);                          // cut() > 0 from here
+    const int64_t all = imin(cost, imax(some, item + (int64_t)(nt - kLeast + 1) * tile));    // == nt from here
+    Parts p;
+    p.first = line.ending_from(s + some);
+    p.count = line.ending_from(s + all) - p.first + 1;
+    return p;
+}
+
+// The CTAs a line is worth: parts that cost as much to begin as to do are not.
+PKV_HD Line line_of(int64_t length, int most, int least)
+{
+    const int64_t n = length / least;
+    return {length, (int)imax(1, imin(n, most))};
+}
+
+}  // namespace plan
+}  // namespace pkv

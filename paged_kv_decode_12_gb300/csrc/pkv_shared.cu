@@ -22,14 +22,13 @@
 #include <cmath>
 
 #include "pkv_step.cuh"
-#include "pkv_tc.cuh"
+#include "pkv_tiles.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kTilePages = 8;                       // pages of one key tile: 128 tokens
-constexpr int kHalf = kTilePages * kPage / 2;       // its halves
-constexpr int kRowTile = 128;                       // query rows of one tensor-core tile
+using namespace tiles;
+
 constexpr int kTileSeqs = kRowTile / kGroup;        // 32 sequences x the 4 heads of a KV head
 
 // The groups of a call: group i is sequences starts[i] .. starts[i + 1] - 1, its prefix
@@ -94,14 +93,11 @@ struct OwnPages {
 
 // ------------------------------------------------------------------ the prefix on tensor cores
 
-constexpr int kStageSize = kTilePages * kStageBytes;           // 32 KiB: 8 x (K rows, V rows)
-constexpr int kRawSize = kTilePages * kFp8Unit;                // 17 KiB: FP8 units as they lie in the pages
 constexpr int kRaws = 2;                                       // of them in flight
 constexpr int kLoader = 8, kIssuer = 9, kConverter = 12;       // warps: 2 x 4 softmax, loader, two issuers, (FP8) four
 constexpr int kConverters = 4;                                 // converters
 constexpr int kOutRow = 32 * 4 + 16;                           // half an output row, padded to other banks
 constexpr int kOutSize = 2 * kRowTile * kOutRow;               // 36 KiB: of every row
-constexpr int kScales = 3 * kTilePages * kPage;                // row scales of a tile: K's, V's, 1 / V's
 constexpr int kCols = 512;                                     // tensor memory, all of it
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColL = 448;  // + 128 / 64 / 32 / 16 for the second tile
 constexpr int kOnesSize = 16 * 128;                            // BF16 pages: 16 rows of ones, for the sums
@@ -304,21 +300,6 @@ __device__ __forceinline__ void prefix_loader(const CUtensorMap *tmap, const Pre
             (void)mbar_wait_warp(&full[i % kRing], (i / kRing) & 1);
 }
 
-// Two E4M3 codes as BF16 (exact: 4 significant bits, exponents in range; NaN stays NaN).
-__device__ __forceinline__ uint32_t bf16x2_of_f16x2(uint32_t h)
-{
-    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-    return pack_bf16x2(f.x, f.y);
-}
-
-__device__ __forceinline__ void bf16_of_e4m3x4(uint32_t w, uint32_t &lo, uint32_t &hi)
-{
-    uint32_t a, b;
-    fp8::e4m3x4_to_f16x2(w, a, b);
-    lo = bf16x2_of_f16x2(a);
-    hi = bf16x2_of_f16x2(b);
-}
-
 // Converters (FP8; 128 threads): raw units into a stage of the BF16 layout.  The codes become
 // BF16 as they are; the row scales go to the scores and the weights instead of the rows, so
 // that nothing is rounded here.
@@ -335,46 +316,7 @@ __device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint
             if (!tc::wait_warp(&bars.raw_full[rs], (seq / kRaws) & 1, &bars.stop) ||
                 (seq >= kStages && !tc::wait_warp(&bars.empty[st], (seq / kStages - 1) & 1, &bars.stop)))
                 return;
-            const uint8_t *raw = raws + rs * kRawSize;
-            uint8_t *dst = stages + st * kStageSize;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // K: 16 codes of a row, two chunks of 8 values
-                const int u = t + 128 * k, page = u / 64, row = u % 64 / 4, part = u % 4;
-                const uint4 c = *reinterpret_cast<const uint4 *>(raw + page * kFp8Unit + row * kD + part * 16);
-                uint4 lo, hi;
-                bf16_of_e4m3x4(c.x, lo.x, lo.y);
-                bf16_of_e4m3x4(c.y, lo.z, lo.w);
-                bf16_of_e4m3x4(c.z, hi.x, hi.y);
-                bf16_of_e4m3x4(c.w, hi.z, hi.w);
-                *reinterpret_cast<uint4 *>(dst + page * kStageBytes + swz(row, 2 * part)) = lo;
-                *reinterpret_cast<uint4 *>(dst + page * kStageBytes + swz(row, 2 * part + 1)) = hi;
-            }
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {  // V: 8 dims of the tokens 2 pair, 2 pair + 1, codes alternating
-                const int u = t + 128 * k, page = u / 64, pair = u % 64 / 8, at = u % 8, chunk = at ^ ((2 * pair) & 7);
-                const uint4 c = *reinterpret_cast<const uint4 *>(raw + page * kFp8Unit + fp8::kFp8Tile + pair * 2 * kD + at * 16);
-                uint4 even, odd;
-                bf16_of_e4m3x4(__byte_perm(c.x, c.y, 0x6420), even.x, even.y);
-                bf16_of_e4m3x4(__byte_perm(c.z, c.w, 0x6420), even.z, even.w);
-                bf16_of_e4m3x4(__byte_perm(c.x, c.y, 0x7531), odd.x, odd.y);
-                bf16_of_e4m3x4(__byte_perm(c.z, c.w, 0x7531), odd.z, odd.w);
-                uint8_t *v = dst + page * kStageBytes + kTileBytes;
-                *reinterpret_cast<uint4 *>(v + swz(2 * pair, chunk)) = even;
-                *reinterpret_cast<uint4 *>(v + swz(2 * pair + 1, chunk)) = odd;
-            }
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {  // thread = (page, slot)
-                const int page = t / kPage, slot = t % kPage;
-                const float f = reinterpret_cast<const float *>(raw + page * kFp8Unit + kFp8UnitCodes)[kv * kPage + slot];
-                float *to = bars.scales[st] + slot / 8 * 64 + page * 8 + slot % 8;
-                if (kv) {  // (a scale below 2^-100, of rows of nothing, as 2^-100: weights are counted by its inverse)
-                    const float v = fabsf(f) < 0x1p-100f ? 0x1p-100f : f;
-                    to[128] = v;
-                    to[256] = __frcp_rn(v);
-                } else {
-                    to[0] = f * a.scale_log2;
-                }
-            }
+            convert_tile(raws + rs * kRawSize, stages + st * kStageSize, bars.scales[st], a.scale_log2, t);
             if (t == 0)
                 bars.bad[st] = bars.raw_bad[rs];
             fence_proxy_async_smem();
@@ -385,57 +327,6 @@ __device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint
             }
         }
     }
-}
-
-// Issuer (a converged warp, one elected thread of which issues): the matrix products of every
-// item.  A key tile goes through in two halves of 64 tokens (slots 0..7 and 8..15 of its 8
-// pages), each with scores of its own in tensor memory: while the softmax of one half runs, the
-// other half's weights meet the values and its columns take the next tile's scores.
-__device__ __forceinline__ void issue_scores(uint32_t k, uint32_t s, uint32_t q, uint64_t *done)
-{
-    // S[128 x 64] = Q K^T: columns 8 p + i are slot 8 h + i of page p (page stride 4 KiB)
-    constexpr uint32_t kIdesc = tc::instr_desc(64, true, false), kHi = tc::smem_desc_hi(kStageBytes);
-    const uint32_t lo = tc::smem_desc_lo(k, kStageBytes);
-    if (tc::elect()) {
-        tc::mma_ts<false>(s, q, lo, kHi, kIdesc);
-#pragma unroll
-        for (int i = 1; i < kD / 16; ++i)
-            tc::mma_ts<true>(s, q + i * 8, lo + i * 2, kHi, kIdesc);
-        tc::commit(done);
-    }
-    __syncwarp();
-}
-
-template <bool FIRST, bool SUM>
-__device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p, uint32_t ones, uint32_t l,
-                                             uint64_t *free_stage, int uses, uint64_t *done, uint64_t *last)
-{
-    // O[128 x 64] += P V: 16 columns of P are 8 slots of two pages
-    constexpr uint32_t kIdesc = tc::instr_desc(64, true, true), kHi = tc::smem_desc_hi(kStageBytes);
-    const uint32_t lo = tc::smem_desc_lo(v, kStageBytes);
-    if (tc::elect()) {
-        tc::mma_ts<!FIRST>(o, p, lo, kHi, kIdesc);
-#pragma unroll
-        for (int i = 1; i < kHalf / 16; ++i)
-            tc::mma_ts<true>(o, p + i * 8, lo + i * (2 * kStageBytes / 16), kHi, kIdesc);
-        if constexpr (SUM) {  // L[128 x 16] += P 1
-            constexpr uint32_t kOnes = tc::instr_desc(16, true, false), kOnesHi = tc::smem_desc_hi(1024);
-            const uint32_t one = tc::smem_desc_lo(ones, 1024);
-            tc::mma_ts<!FIRST>(l, p, one, kOnesHi, kOnes);
-#pragma unroll
-            for (int i = 1; i < kHalf / 16; ++i)
-                tc::mma_ts<true>(l, p + i * 8, one, kOnesHi, kOnes);
-        }
-        tc::commit(done);
-        if (last)
-            tc::commit(last);
-        if (free_stage) {
-            tc::commit(free_stage);
-            if (uses > 1)
-                tc::commit(free_stage);
-        }
-    }
-    __syncwarp();
 }
 
 // Each row tile has an issuer warp of its own, so that one's waits pass while the other's
@@ -504,113 +395,22 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
     }
 }
 
-// What turns 64 scores into exponents and weights into the second product's operand: one
-// factor, or (FP8) a factor and a scale for every column.
-struct OneFactor {
-    static constexpr bool kSum = false;  // the sum is made by the matrix instruction
-    float c;
-    __device__ __forceinline__ float2 factor(int) const { return make_float2(c, c); }
-    __device__ __forceinline__ float2 weight(int, float2 e) const { return e; }
-    __device__ __forceinline__ float2 counted(int, float2 e, uint32_t) const { return e; }
-};
-
-struct RowScales {
-    static constexpr bool kSum = true;
-    const float2 *k, *v, *inverse;  // 32 pairs of columns
-    __device__ __forceinline__ float2 factor(int i) const { return k[i]; }
-    __device__ __forceinline__ float2 weight(int i, float2 e) const { return tc::mul2(e, v[i]); }
-    // The weight that the product holds: what was rounded, without V's scale again.
-    __device__ __forceinline__ float2 counted(int i, float2, uint32_t p) const
-    {
-        return tc::mul2(make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), inverse[i]);
-    }
-};
-
-// 32 scores of one query row (columns 32 k ..) as weights 2^(S c - m): their sum, and the weights
-// in pairs rounded to BF16 (half a step, 2^-8) for the second product: what the matrix instruction
-// takes beside BF16 values.  MASK: columns of pages from `pages` on weigh nothing.  Four chains of
-// sums, so that no chain's latency is the time of the whole.
-//
-// BF16 pages: the softmax's sum is of the weights as rounded, made by the matrix instruction too (L
-// += P 1, 16 equal columns), so that the quotient has none of their rounding where few weights make
-// it.  256 sequences behind 32768 tokens: error 0.0017 in 94 us, where the sum of the unrounded
-// weights, which this function returns, gives 0.0023 in 92, and unpacking the rounded ones took 108.
-// FP8 pages: what is rounded is the weight times V's row scale; the sum takes it times the scale's
-// inverse (error 0.0017 instead of 0.0023; 72 sequences in 5 groups 32 us instead of 31).
-template <bool MASK, class Scale>
-__device__ __forceinline__ float make_weights(uint32_t ts, int k, const Scale &sc, int pages, float m, uint32_t (&pk)[16])
-{
-    uint32_t w[32];
-    tc::ld32(ts + k * 32, w);
-    float2 sum[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        sum[i] = make_float2(0.f, 0.f);
-    const float2 m2 = make_float2(-m, -m);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float2 x =
-            tc::fma2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i), m2);
-        float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-        if (MASK && !(k * 4 + i / 4 < pages))
-            e = make_float2(0.f, 0.f);
-        const float2 p = sc.weight(k * 16 + i, e);
-        pk[i] = pack_bf16x2(p.x, p.y);
-        sum[i % 4] = tc::add2(sum[i % 4], sc.counted(k * 16 + i, e, pk[i]));
-    }
-    const float2 s = tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3]));
-    return s.x + s.y;
-}
-
-// Their maximum, times the factors.
-template <bool MASK, class Scale>
-__device__ __forceinline__ float max_score(uint32_t ts, int k, const Scale &sc, int pages)
-{
-    uint32_t w[32];
-    tc::ld32(ts + k * 32, w);
-    float mx = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float2 x = tc::mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i));
-        if (!MASK || k * 4 + i / 4 < pages)
-            mx = tc::max3(mx, x.x, x.y);
-    }
-    return mx;
-}
-
-// The reference m of a row's softmax is its first half tile's maximum, and it stays until a
-// half tile's weights sum to 2^64 or more: FP32 and BF16 hold 2^127, so m, l and O remain a
-// valid log-sum-exp triple that far above m, and no maximum is taken on the way.  (Moving m for
-// every score 2^8 above it, as narrower types need, made most half tiles of 32 rows rescale O.)
-// O is finite for values up to 2^45: 2^64 times that, over at most 2^18 half tiles.
-constexpr float kMostWeight = 18446744073709551616.f;
-
-// An item's first half tile: the row's maximum.  (Not inlined: the loop would pay for its
-// registers; 256 sequences behind 32768 tokens 94.5 us instead of 95.1, though 4 behind 512 tokens
-// 7.5 instead of 7.2.)
-template <class Scale>
-__device__ __noinline__ float first_reference(uint32_t ts, Scale sc, int pages)
-{
-    return fmaxf(max_score<true>(ts, 0, sc, pages), max_score<true>(ts, 1, sc, pages));
-}
-
 // Half a key tile's scores of one query row become weights, in place: P is the first half of
-// S's columns.  MASK: only the first `pages` pages of the tile count.  Returns false if a wait
-// gave up.
-template <bool MASK, class Scale>
-__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, uint32_t tl, const Scale &sc, int pages, int before,
+// S's columns.  Returns false if a wait gave up.
+template <class Mask, class Scale>
+__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, uint32_t tl, const Scale &sc, const Mask &mask, int before,
                                              uint64_t *o_step, volatile int *stop, float &m, float &l)
 {
     uint32_t p0[16], p1[16];
-    float s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
+    float s = make_weights(ts, 0, sc, mask, m, p0) + make_weights(ts, 1, sc, mask, m, p1);
     const bool move = !(s < kMostWeight);
     if (__any_sync(kFull, move)) {
-        const float top = fmaxf(max_score<MASK>(ts, 0, sc, pages), max_score<MASK>(ts, 1, sc, pages));
+        const float top = fmaxf(max_score(ts, 0, sc, mask), max_score(ts, 1, sc, mask));
         const float mn = move ? fmaxf(top, m) : m;
         const float f = ex2_approx(m - mn);  // 1 where the reference stays
         m = mn;
         l *= f;
-        s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
+        s = make_weights(ts, 0, sc, mask, m, p0) + make_weights(ts, 1, sc, mask, m, p1);
         // Once the product before this one is done, nothing else touches O.  (These scores came
         // after the product before that, so the wait is one phase behind at most.)
         if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
@@ -717,12 +517,11 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
                 const int seq = loaded + x.order(s, j), st = seq % kStages;
                 const auto half = [&](const auto &sc) {
                     if (j == 0 && hf == 0)
-                        m = first_reference(ts, sc, pages);
+                        m = first_reference(ts, sc, FirstPages{pages});
                     return pages >= kTilePages
-                               ? softmax_half<false>(ts + hf * kHalf, to, tl, sc, kTilePages, before, &bars.o_step[s], &bars.stop,
-                                                     m, l)
-                               : softmax_half<true>(ts + hf * kHalf, to, tl, sc, pages, before, &bars.o_step[s], &bars.stop, m,
-                                                    l);
+                               ? softmax_half(ts + hf * kHalf, to, tl, sc, EveryColumn{}, before, &bars.o_step[s], &bars.stop, m, l)
+                               : softmax_half(ts + hf * kHalf, to, tl, sc, FirstPages{pages}, before, &bars.o_step[s], &bars.stop,
+                                              m, l);
                 };
                 bool go;
                 if constexpr (FP8) {
