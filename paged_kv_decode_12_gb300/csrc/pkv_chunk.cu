@@ -11,8 +11,8 @@
 //
 // Masks: only tiles in which some row does not attend to some token (the last ones, and a window's
 // first) are masked, by 64 bits a row and half tile.  A weight of 0 times a value that is not finite would
-// not be 0, so in those tiles values that nobody attends to are cleared in shared memory, and those that are not
-// finite too: rows that attend to one get NaN in its dimension at the end.
+// not be 0, so in those tiles an issuer warp (FP8: the warps that convert) looks for such values and clears them; rows that attend to one get NaN
+// in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us where 259 were without.)
 #include <cmath>
 
 #include "pkv_chunk_plan.cuh"
@@ -29,15 +29,20 @@ using plan::PageList;
 constexpr int kMaxRows = 4096;       // sequences of a call
 constexpr int kSms = 152;
 constexpr int kStages = 4, kRaws = 2, kItems = 4;
-constexpr int kLoader = 8, kIssuer = 9, kScheduler = 11, kConverter = 12;   // warps: 2 x 4 softmax, ...
-constexpr int kConverters = 4;
+constexpr int kLoader = 8, kIssuer = 9, kScheduler = 11, kPreparer = 12;   // warps: 2 x 4 softmax, ...
+constexpr int kPreparers = 4;
 constexpr int kTeam = 8;             // warps of a single token's pages
-constexpr int kOnesSize = 16 * 128;  // BF16 pages: 16 rows of ones, for the sums
+constexpr int kRowBytes = 128 + 16;  // a query or output row in shared memory, padded to other banks
+constexpr int kRowsSize = 2 * kRowTile * kRowBytes;
+static_assert(kStateFloats * 4 <= 32 * kRowBytes, "a warp's softmax state fits its rows");
+// What the weights are multiplied with for their sums, 16 columns of 64 places: ones; FP8: for every stage and half
+// the inverses of V's scales, as two BF16 numbers in the first two columns (the others do not matter).
+constexpr int sums_size(bool fp8) { return fp8 ? (2 * kStages + 1) * 1024 : 2048; }
 constexpr int kCols = 512;           // tensor memory, all of it
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColL = 448;  // + 128 / 64 / 32 / 16 for the second row tile
 
-constexpr int chunk_threads(bool fp8) { return fp8 ? (kConverter + kConverters) * 32 : kConverter * 32; }
-constexpr int consumers(bool fp8) { return fp8 ? 8 + 3 + kConverters : 8 + 3; }
+constexpr int chunk_threads(bool fp8) { return fp8 ? (kPreparer + kPreparers) * 32 : kPreparer * 32; }
+constexpr int consumers(bool fp8) { return fp8 ? 8 + 3 + kPreparers : 8 + 3; }  // warps that go through the items
 
 struct ChunkArgs {
     int num_pages;
@@ -64,7 +69,8 @@ struct Item {
     int sink, from, count; // its pages
     int j0, j1, nt;        // key tiles of the piece; of the whole item
     int first, parts, me;  // CTAs that share the item, and this one's place among them
-    int pad;
+    int plain, plain0, plain1;  // key tiles in which every row attends to every place: below plain, and plain0 .. plain1 - 1
+    int pad[3];
     __device__ __forceinline__ int page(int i) const { return i < sink ? i : i - sink + from; }
     __device__ __forceinline__ int loads() const { return (j1 - j0) * (kind == plan::kHeads ? 2 : 1); }
     // A row tile's first token within the item, its tokens, its KV head, and the place among the piece's loads of
@@ -73,16 +79,32 @@ struct Item {
     __device__ __forceinline__ int tokens(int s) const { return min(plan::kRowTokens, n - token(s)); }
     __device__ __forceinline__ int head(int s) const { return kind == plan::kHeads ? g + s : g; }
     __device__ __forceinline__ int order(int s, int j) const { return kind == plan::kHeads ? 2 * j + s : j; }
-    // Some row of the item does not attend to some place of key tile j.
-    __device__ __forceinline__ bool masked(int j, int window) const
+    __device__ __forceinline__ bool masked(int j) const { return j >= plain && (j < plain0 || j >= plain1); }
+    // Loads of the piece before its j-th key tile's first whose tiles are masked.
+    __device__ __forceinline__ int masked_loads(int j) const
     {
-        const int i = j * kTilePages;
-        return i + kTilePages > count || page(i + kTilePages - 1) * kPage + kPage - 1 > p0 ||
-               (window && (i < sink || page(i) * kPage < p0 + n - window));
+        const int n = masked_tiles(j0 + j) - masked_tiles(j0);
+        return kind == plan::kHeads ? 2 * n : n;
+    }
+    __device__ __forceinline__ int masked_tiles(int j) const
+    {
+        return j - min(j, plain) - (min(max(j, plain0), plain1) - plain0);
+    }
+    __device__ __forceinline__ void find_plain(int window, int sinks)
+    {
+        const int whole = (p0 + 1) / kPage;  // pages that end at or before the first token
+        plain1 = min(count, max(whole + sink - from, 0)) / kTilePages;
+        plain = plain0 = 0;
+        if (window) {
+            plain = min(sink, sinks / kPage) / kTilePages;  // entries from the first page on that the last token's window holds as a whole
+            const int entry = max(sink, sink - from + (max(p0 + n - window, 0) + kPage - 1) / kPage);
+            plain0 = (entry + kTilePages - 1) / kTilePages;
+        }
+        plain1 = max(plain1, plain0);
     }
 };
 
-// A value row that holds something not finite: the load it belongs to, and which dimensions.
+// A value row of a masked tile that holds something not finite: the load it belongs to, and which dimensions.
 struct Poison {
     int load;
     uint32_t lo, hi;
@@ -95,21 +117,21 @@ struct ChunkShared {
     uint64_t o_step[2];                          // one more product of weights and values is done
     uint64_t q_full[2], o_full[2];               // once an item: the queries are in / its last product is done
     uint64_t item_full[kItems], item_empty[kItems];
-    uint64_t group[3];                           // row tile s's warps (2: all eight) have come so far
+    uint64_t checked[kStages];                   // (BF16) the values of a masked load have been gone through
+    uint64_t group[4];                           // row tile s's warps (2: all eight; 3: the preparers) have come so far
     uint64_t drained[2];
     uint32_t tmem;
     int stop;                                    // a wait gave up
     int bad[kStages], raw_bad[kRaws];            // the tile has a bad page id
-    int noted[2];                                // the last load of row tile s with notes on values (see Poison)
+    int noted[kStages];                          // the last load into the stage with notes on values (see Poison)
     int last[3];                                 // group: this CTA finished the item last
     int taken[2][2];                             // [went on, begun][row tile]: the cut item's ticket is drawn
     int64_t length;                              // of the line
     int64_t warp_sums[16];
     alignas(16) Item items[kItems];
     Poison poison[kStages][kTilePages * kPage];
-    alignas(16) float states[kTeam][kStateFloats];
     int64_t sums[512];                           // costs of the sequences before each thread's
-    float scales[kStages][kScales];              // (FP8)
+    alignas(16) float scales[kStages][2][kTilePages * kPage];  // (FP8) row scales: K's times scale log2 e, V's
 };
 
 // ------------------------------------------------------------------ the plan
@@ -135,7 +157,7 @@ __device__ __forceinline__ Row row_of(const ChunkArgs &a, int b)
     const int s1 = a.starts[b + 1];
     x.ok = x.s0 >= 0 && s1 >= x.s0 && s1 <= a.T;
     x.n = x.ok ? s1 - x.s0 : 0;
-    x.L = x.n ? a.lens[b] : 0;
+    x.L = a.lens[b];
     return x;
 }
 
@@ -153,9 +175,8 @@ __device__ __forceinline__ int64_t row_cost(const ChunkArgs &a, const Row &x, co
 template <bool FP8>
 __device__ __forceinline__ void make_plan(const ChunkArgs &a, ChunkShared &sh)
 {
-    constexpr int kThreadsHere = chunk_threads(FP8);
     const Costs k = costs<FP8>();
-    const int per = (a.B + kThreadsHere - 1) / kThreadsHere;
+    const int per = (a.B + chunk_threads(FP8) - 1) / chunk_threads(FP8);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t sum = 0;
     bool bad = threadIdx.x == 0 && a.starts[0] != 0;
@@ -184,7 +205,7 @@ __device__ __forceinline__ void make_plan(const ChunkArgs &a, ChunkShared &sh)
         sh.warp_sums[warp] = upto;
     bad = __syncthreads_or(bad);
     int64_t before = upto - sum, all = 0;
-    for (int w = 0; w < kThreadsHere / 32; ++w) {
+    for (int w = 0; w < chunk_threads(FP8) / 32; ++w) {
         if (w < warp)
             before += sh.warp_sums[w];
         all += sh.warp_sums[w];
@@ -201,17 +222,16 @@ __device__ __forceinline__ void make_plan(const ChunkArgs &a, ChunkShared &sh)
 template <bool FP8, class Take>
 __device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkShared &sh, const Take &take)
 {
-    constexpr int kThreadsHere = chunk_threads(FP8);
     const Costs k = costs<FP8>();
     const plan::Line line = plan::line_of(sh.length, gridDim.x, kLeastCost);
     if (line.length == 0 || (int)blockIdx.x >= line.ctas)
         return;
-    const int lane = threadIdx.x & 31, per = (a.B + kThreadsHere - 1) / kThreadsHere;
+    const int lane = threadIdx.x & 31, per = (a.B + chunk_threads(FP8) - 1) / chunk_threads(FP8);
     const int64_t x0 = line.border(blockIdx.x), x1 = line.border(blockIdx.x + 1);
     int64_t x = x0;
     while (x < x1) {
         // the thread whose sequences hold x (the last whose sum is not above it), and the sequence
-        int lo = 0, hi = kThreadsHere;
+        int lo = 0, hi = chunk_threads(FP8);
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
             if (sh.sums[mid] <= x)
@@ -245,13 +265,13 @@ __device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkSh
             it.b = b;
             if (row.n == 1) {
                 it.kind = plan::kSingle;
-                it.g = (int)(y / single);
+                it.g = plan::eighth(y, single);
                 s = begin + it.g * single;
                 it.n = 1;
                 pages = seq.single_pages();
             } else if (y < kHkv * head) {
                 it.kind = plan::kPair;
-                it.g = (int)(y / head);
+                it.g = plan::eighth(y, head);
                 y -= it.g * head;
                 int r = seq.pairs - 1;
                 if (y < seq.before(r)) {  // the last r that does not begin behind y, by 32 tries at a time
@@ -270,7 +290,7 @@ __device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkSh
                 pages = seq.pair_pages(r);
             } else {
                 it.kind = plan::kHeads;
-                const int h = (int)((y - kHkv * head) / rest);
+                const int h = plan::eighth(y - kHkv * head, rest);
                 it.g = 2 * h;
                 s = begin + kHkv * head + h * rest;
                 token = 64 * seq.pairs;
@@ -290,7 +310,7 @@ __device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkSh
             it.first = parts.first;
             it.parts = parts.count;
             it.me = blockIdx.x - parts.first;
-            it.pad = 0;
+            it.find_plain(a.window, a.sinks);
             if (it.j0 < it.j1 && !take(it))
                 return;
             x = s + (int64_t)it.nt * tile + over;
@@ -378,7 +398,7 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
         const bool single = x.kind == plan::kSingle, through_raw = FP8 && !single;
         const int heads = x.kind == plan::kHeads ? 2 : 1;
         const uint64_t policy = single ? once_policy : shared_policy;
-        if (FP8 && single)  // the converters are done with every stage before
+        if (FP8 && single)  // the preparers are done with every stage before
             for (int i = max(raw - kRaws, 0); go && i < raw; ++i)
                 go = tc::wait_warp(&sh.raw_empty[i % kRaws], (i / kRaws) & 1, &sh.stop);
         int id4 = 0;  // lane l: the id of page l of the current run of 4 key tiles
@@ -414,7 +434,7 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
                     if (!through_raw && !single)
                         arrive_n(&sh.empty[st], given_in_advance(x.kind));
                     if (FP8 && single)
-                        arrive_n(full, kConverters - 1);
+                        arrive_n(full, kPreparers - 1);
                     mbar_arrive_expect_tx(full, size);
                 }
                 __syncwarp();
@@ -438,28 +458,91 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
     }
 }
 
-// ------------------------------------------------------------------ converters (FP8 row tiles; 128 threads)
+// ------------------------------------------------------------------ values of masked tiles
 
-__device__ __forceinline__ void converter(const ChunkArgs &a, const uint8_t *raws, uint8_t *stages, ChunkShared &sh)
+// The value rows of a masked tile by THREADS threads (`t` of them): a weight of 0 times a value that is not finite would
+// not be 0, so such values become zeros, and where somebody may attend to them their dimensions are noted.
+template <int THREADS>
+__device__ __forceinline__ void check_values(const Item &x, int j, uint8_t *stage, Poison *notes, int *noted, int load, int t)
 {
-    const int t = threadIdx.x - kConverter * 32, lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int key = t; key < kTilePages * kPage; key += THREADS) {
+        const int i = j * kTilePages + key / kPage, slot = key % kPage;
+        uint8_t *row = stage + key / kPage * kStageBytes + kTileBytes;
+        uint32_t hit = 0;  // an exponent of ones carries into the sign's place
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + swz(slot, c));
+            hit |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
+                   ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
+        }
+        if (!(hit & 0x80008000u))
+            continue;
+        uint32_t lo = 0, hi = 0;
+        for (int d = 0; d < kD; ++d) {
+            uint16_t *v = reinterpret_cast<uint16_t *>(row + swz(slot, d / 8)) + d % 8;
+            if ((*v & 0x7f80u) == 0x7f80u) {
+                (d < 32 ? lo : hi) |= 1u << (d & 31);
+                *v = 0;
+            }
+        }
+        if (i < x.count && x.page(i) * kPage + slot < x.p0 + x.n) {  // (what is behind the last token reaches nobody)
+            notes[key] = {load, lo, hi};
+            *noted = load;
+        }
+        fence_proxy_async_smem();
+    }
+}
+
+// ------------------------------------------------------------------ preparers (FP8 row tiles; 128 threads)
+
+// Units become BF16 values, and masked tiles are gone through.
+__device__ __forceinline__ void preparer(const ChunkArgs &a, const uint8_t *raws, uint8_t *stages, uint8_t *sums, ChunkShared &sh)
+{
+    const int t = threadIdx.x - kPreparer * 32, lane = threadIdx.x & 31;
     Feed feed(sh);
-    int seq = 0, raw = 0;
-    for (const Item *x; (x = feed.look()) != nullptr; feed.let_go()) {
-        const int n = x->loads(), kind = x->kind;
-        if (kind == plan::kSingle) {
+    int seq = 0, raw = 0, checks = 0;
+    for (const Item *p; (p = feed.look()) != nullptr; feed.let_go()) {
+        const Item x = *p;
+        const int n = x.loads();
+        if (x.kind == plan::kSingle) {
             seq += n;
             continue;
         }
         for (int i = 0; i < n; ++i, ++seq, ++raw) {
-            const int rs = raw % kRaws, st = seq % kStages;
+            const int j = x.j0 + (x.kind == plan::kHeads ? i / 2 : i), rs = raw % kRaws, st = seq % kStages;
             if (!tc::wait_warp(&sh.raw_full[rs], (raw / kRaws) & 1, &sh.stop) ||
                 (seq >= kStages && !tc::wait_warp(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)))
                 return;
-            convert_tile(raws + rs * kRawSize, stages + st * kStageSize, sh.scales[st], a.scale_log2, t);
+            const uint8_t *raw_tile = raws + rs * kRawSize;
+            uint8_t *stage = stages + st * kStageSize;
+            convert_codes(raw_tile, stage, t);
+            {  // row scales in the order of the scores' columns; thread = (page, slot)
+                const int page = t / kPage, slot = t % kPage, at = page * 8 + slot % 8;
+                const float *row = reinterpret_cast<const float *>(raw_tile + page * kFp8Unit + kFp8UnitCodes);
+                const float f = row[kPage + slot];
+                // (a scale below 2^-100, of rows of nothing, as 2^-100: weights are counted by its inverse;
+                // one that is not finite counts nothing: rows that attend to it are not finite by P)
+                const float v = fabsf(f) < 0x1p-100f ? 0x1p-100f : f;
+                const float inv = fabsf(v) < INFINITY ? __frcp_rn(v) : 0.f;
+                sh.scales[st][0][slot / 8 * kHalf + at] = row[slot] * a.scale_log2;
+                sh.scales[st][1][slot / 8 * kHalf + at] = v;
+                uint8_t *sum = sums + (st * 2 + slot / 8) * 1024 + slot % 8 * 2;
+                const __nv_bfloat16 hi = __float2bfloat16_rn(inv), lo = __float2bfloat16_rn(inv - __bfloat162float(hi));
+                *reinterpret_cast<__nv_bfloat16 *>(sum + page * 16) = hi;  // (row 0, row 1 of the swizzled operand)
+                *reinterpret_cast<__nv_bfloat16 *>(sum + 128 + (page ^ 1) * 16) = lo;
+            }
             if (t == 0) {
                 sh.bad[st] = sh.raw_bad[rs];
-                arrive_n(&sh.empty[st], given_in_advance(kind));
+                arrive_n(&sh.empty[st], given_in_advance(x.kind));
+            }
+            if (x.masked(j)) {  // (rows that other warps have written)
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(&sh.group[3]);
+                if (!tc::wait_warp(&sh.group[3], checks++ & 1, &sh.stop))
+                    return;
+                check_values<kPreparers * 32>(x, j, stage, sh.poison[st], &sh.noted[st], seq, t);
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -475,12 +558,13 @@ __device__ __forceinline__ void converter(const ChunkArgs &a, const uint8_t *raw
 
 // Each row tile has an issuer warp of its own, so that one's waits pass while the other's products run.
 template <bool FP8>
-__device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *ones, ChunkShared &sh, uint32_t tmem, int s)
+__device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, ChunkShared &sh, uint32_t tmem, int s)
 {
-    const uint32_t base = smem_addr(stages), one = smem_addr(ones), tl = tmem + kColL + s * 16;
+    const uint32_t base = smem_addr(stages), sum0 = smem_addr(sums), tl = tmem + kColL + s * 16;
     const uint32_t ts = tmem + kColS + s * 128, to = tmem + kColO + s * 64, tq = tmem + kColQ + s * 32;
     Feed feed(sh);
-    int loaded = 0, done = 0, used = 0;  // loads of earlier pieces, key tiles of this row tile, pieces with row tiles
+    // loads of earlier pieces, those of masked tiles, key tiles of this row tile, pieces with row tiles
+    int loaded = 0, checks = 0, done = 0, used = 0;
     for (const Item *p; (p = feed.look()) != nullptr; feed.let_go()) {
         const Item x = *p;
         if (x.kind != plan::kSingle) {
@@ -496,17 +580,32 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *ones, Chu
                 return true;
             };
             const auto output = [&](int j, int h) {
+                const int seq = loaded + x.order(s, j), st = seq % kStages;
+                if (!FP8 && h == 0 && x.masked(x.j0 + j)) {
+                    // (a pair's values, which both row tiles read, by the first one's issuer)
+                    const int check = checks + x.masked_loads(j) + (x.kind == plan::kHeads ? s : 0);
+                    uint64_t *checked = &sh.checked[check % kStages];
+                    if (x.kind == plan::kHeads || s == 0) {
+                        check_values<32>(x, x.j0 + j, stages + st * kStageSize, sh.poison[st], &sh.noted[st], seq,
+                                         threadIdx.x & 31);
+                        __syncwarp();
+                        if ((threadIdx.x & 31) == 0)
+                            tc::mbar_arrive(checked);
+                    }
+                    if (!tc::wait_warp(checked, (check / kStages) & 1, &sh.stop))
+                        return false;
+                }
                 if (!tc::wait_warp(&sh.p_full[s][h], (done + j) & 1, &sh.stop))
                     return false;
                 tc::fence_after();
-                const int st = (loaded + x.order(s, j)) % kStages;
                 const uint32_t v = base + st * kStageSize + kTileBytes + h * 1024, pw = ts + h * kHalf;
                 uint64_t *empty = h == 1 ? &sh.empty[st] : nullptr;
                 uint64_t *last = h == 1 && j + 1 == nt ? &sh.o_full[s] : nullptr;
+                const uint32_t sum = sum0 + (FP8 ? (st * 2 + h) * 1024 : 0);
                 if (j == 0 && h == 0)
-                    issue_output<true, !FP8>(v, to, pw, one, tl, empty, 1, &sh.o_step[s], last);
+                    issue_output<true, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
                 else
-                    issue_output<false, !FP8>(v, to, pw, one, tl, empty, 1, &sh.o_step[s], last);
+                    issue_output<false, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
                 return true;
             };
             bool go = tc::wait_warp(&sh.q_full[s], used & 1, &sh.stop);
@@ -524,6 +623,7 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *ones, Chu
                 break;
             ++used;
             done += nt;
+            checks += x.masked_loads(nt);
         }
         loaded += x.loads();
     }
@@ -541,7 +641,7 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *ones, Chu
 __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 8)) - 1; }
 
 // What a row at position p attends to in half hf of key tile j.
-__device__ __forceinline__ ColumnBits columns(const Item &x, int j, int hf, int p, int window, int sinks)
+__device__ __forceinline__ uint2 columns(const Item &x, int j, int hf, int p, int window, int sinks)
 {
     uint32_t w[2] = {0, 0};
     const int lo = window ? max(p + 1 - window, 0) : 0;
@@ -553,107 +653,178 @@ __device__ __forceinline__ ColumnBits columns(const Item &x, int j, int hf, int 
             bits = 0;
         w[i / 4] |= bits << (i % 4 * 8);
     }
-    return {w[0], w[1]};
+    return make_uint2(w[0], w[1]);
 }
 
-// The value rows of a masked tile, one a thread of the row tile's 128: rows that nobody attends to become zeros, and
-// values that are not finite too, their dimensions noted.  True if this thread's row has a note.
-// The other row tile of a pair may do the same at the same time.  A note is written before anything is
-// cleared, and read after the values: who finds a value cleared finds the note, so that every note is whole.
-__device__ __forceinline__ bool clear_values(const Item &x, int j, uint8_t *stage, Poison *notes, int load)
+// The dimensions of noted values that a row attends to in half hf of the tile.
+__device__ __noinline__ void reached(uint2 mask, const Poison *notes, int hf, int load, uint32_t &lo, uint32_t &hi)
 {
-    const int t = threadIdx.x & 127, i = j * kTilePages + t / kPage, slot = t % kPage;
-    uint8_t *row = stage + t / kPage * kStageBytes + kTileBytes;
-    const bool outside = i >= x.count || x.page(i) * kPage + slot > x.p0 + x.n - 1;
-    bool noted = false;
-    if (outside) {
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            *reinterpret_cast<uint4 *>(row + swz(slot, c)) = make_uint4(0, 0, 0, 0);
-    } else {
-        uint32_t hit = 0;  // an exponent of ones carries into the sign's place
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4 *>(row + swz(slot, c));
-            hit |= ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                   ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
-        }
-        volatile Poison *note = &notes[t];
-        uint32_t lo = 0, hi = 0;
-        if (hit & 0x80008000u)
-            for (int d = 0; d < kD; ++d)
-                if ((*reinterpret_cast<volatile uint16_t *>(row + swz(slot, d / 8) + d % 8 * 2) & 0x7f80u) == 0x7f80u)
-                    (d < 32 ? lo : hi) |= 1u << (d & 31);
-        __threadfence_block();
-        if (note->load == load) {
-            lo |= note->lo;
-            hi |= note->hi;
-        }
-        noted = (lo | hi) != 0;
-        if (hit & 0x80008000u) {
-            note->lo = lo;
-            note->hi = hi;
-            __threadfence_block();
-            note->load = load;
-            __threadfence_block();
-            for (int d = 0; d < kD; ++d)
-                if ((d < 32 ? lo : hi) >> (d & 31) & 1u)
-                    *reinterpret_cast<volatile uint16_t *>(row + swz(slot, d / 8) + d % 8 * 2) = 0;
+    for (int i = 0; i < kHalf; ++i) {
+        const Poison &note = notes[i / 8 * kPage + 8 * hf + i % 8];
+        if (((i < 32 ? mask.x : mask.y) >> (i & 31) & 1u) && note.load == load) {
+            lo |= note.lo;
+            hi |= note.hi;
         }
     }
-    fence_proxy_async_smem();
-    return noted;
+}
+
+// What half a key tile's scores of one query row need besides themselves: the factor of all of them, or (FP8) the row
+// scales of the 64 columns, K's (times the factor) and V's; the columns that count; where S, O and the sums are.
+struct HalfRow {
+    uint32_t ts, to, tl;
+    float c;
+    const float4 *ks, *vs;
+    uint2 mask;
+    template <bool MASKED>
+    __device__ __forceinline__ void drop(int i, float2 &x, float to_) const  // columns 2 i, 2 i + 1
+    {
+        if (MASKED) {
+            const uint32_t w = i < 16 ? mask.x : mask.y;
+            x.x = w & (1u << (2 * i & 31)) ? x.x : to_;
+            x.y = w & (2u << (2 * i & 31)) ? x.y : to_;
+        }
+    }
+};
+
+// The maximum of the scores that count, times the factors.
+template <bool FP8, bool MASKED>
+__device__ __noinline__ float top_score(HalfRow h)
+{
+    float mx = -INFINITY;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t w[32];
+        tc::ld32(h.ts + q * 32, w);
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float4 f = FP8 ? h.ks[q * 8 + i / 2] : make_float4(h.c, h.c, h.c, h.c);
+            float2 x = tc::mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), make_float2(f.x, f.y));
+            float2 y = tc::mul2(make_float2(__uint_as_float(w[2 * i + 2]), __uint_as_float(w[2 * i + 3])), make_float2(f.z, f.w));
+            h.drop<MASKED>(q * 16 + i, x, -INFINITY);
+            h.drop<MASKED>(q * 16 + i + 1, y, -INFINITY);
+            mx = tc::max3(tc::max3(mx, x.x, x.y), y.x, y.y);
+        }
+    }
+    return mx;
+}
+
+// How far a reference lies above the maximum that it is taken from, and the weight that moves it.  BF16 pages: 2, which
+// one bit of the rounded weights shows (as a maximum over them it took 268 us where this takes 253: 2048 tokens behind
+// 14000); so it lies 2^60 above, and weights down to 2^-66 of the first ones' largest count.  (2^32
+// above: outliers among the keys move it, 305 us for 16 prompts of 2048 where 239 were.)  FP8 pages: the
+// weights are multiplied with V's scales, which may be small, so it lies at the maximum, and 2^64 moves it.
+template <bool FP8>
+constexpr float kAbove = FP8 ? 0.f : 60.f;
+
+// What has become of a half's weights besides themselves: whether some are too large or not numbers (m has to move).
+template <bool FP8>
+struct Excess {
+    uint32_t bits = 0;  // BF16: an exponent's first bit is 2 or more
+    float most = 0.f;
+    __device__ __forceinline__ bool any() const { return FP8 ? !(most < kMostWeight) : (bits & 0x40004000u) != 0; }
+};
+
+// 32 scores (columns 32 q ..) as weights 2^(S c - m), in pairs rounded to BF16 (half a step, 2^-8): what the matrix
+// instruction takes beside BF16 values.
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ void weigh(const HalfRow &h, int q, const uint32_t (&w)[32], float m, uint32_t *p, Excess<FP8> &ex)
+{
+    const float2 m2 = make_float2(-m, -m);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+        const int at = q * 16 + i;
+        const float4 f = FP8 ? h.ks[at / 2] : make_float4(h.c, h.c, h.c, h.c);
+        const float2 x =
+            tc::fma2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), make_float2(f.x, f.y), m2);
+        const float2 y =
+            tc::fma2(make_float2(__uint_as_float(w[2 * i + 2]), __uint_as_float(w[2 * i + 3])), make_float2(f.z, f.w), m2);
+        float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y)), g = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+        h.drop<MASKED>(at, e, 0.f);
+        h.drop<MASKED>(at + 1, g, 0.f);
+        if (FP8) {
+            ex.most = tc::max3(tc::max3(ex.most, e.x, e.y), g.x, g.y);
+            const float4 v = h.vs[at / 2];
+            e = tc::mul2(e, make_float2(v.x, v.y));
+            g = tc::mul2(g, make_float2(v.z, v.w));
+            h.drop<MASKED>(at, e, 0.f);  // (the scale may be anything)
+            h.drop<MASKED>(at + 1, g, 0.f);
+        }
+        p[i] = pack_bf16x2(e.x, e.y);
+        p[i + 1] = pack_bf16x2(g.x, g.y);
+        if (!FP8)
+            ex.bits |= p[i] | p[i + 1];
+    }
+}
+
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ bool half_weights(const HalfRow &h, float m, uint32_t (&p)[32])
+{
+    Excess<FP8> ex;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t w[32];
+        tc::ld32(h.ts + q * 32, w);
+        weigh<FP8, MASKED>(h, q, w, m, p + q * 16, ex);
+    }
+    return ex.any();
+}
+
+// The reference of the rows with `move` moves to the maximum of their scores, and what they have summed up so far with
+// it; then the weights.  (If a wait gives up here the next one does.)
+template <bool FP8, bool MASKED>
+__device__ __noinline__ float move_reference(HalfRow h, bool move, float m, uint64_t *o_step, int before, volatile int *stop)
+{
+    const float top = top_score<FP8, MASKED>(h);
+    const float mn = move ? fmaxf(top + kAbove<FP8>, m) : m;
+    const float f = move ? ex2_approx(m - mn) : 1.f;
+    // Once the product before this one is done, nothing else touches O.  (These scores came
+    // after the product before that, so the wait is one phase behind at most.)
+    if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
+        return m;
+    tc::fence_after();
+#pragma unroll 1
+    for (int k = 0; k < 5; ++k) {  // (O's 64 columns and the sums' 16)
+        uint32_t o[16];
+        const uint32_t at = k < 4 ? h.to + k * 16 : h.tl;
+        tc::ld16(at, o);
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+        tc::st16(at, o);
+    }
+    uint32_t p[32];
+    (void)half_weights<FP8, MASKED>(h, mn, p);
+    tc::st32(h.ts, p);
+    return mn;
+}
+
+// A row's first reference: of the half tile's scores.
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ void first_reference(const HalfRow &h, float &m)
+{
+    if (__any_sync(kFull, m == -INFINITY)) {
+        const float top = top_score<FP8, MASKED>(h);
+        if (m == -INFINITY)
+            m = top + kAbove<FP8>;
+    }
 }
 
 // Half a key tile's scores of one query row become weights, in place (P is the first half of S's columns).  The
-// reference m is the row's first scores' maximum (see kMostWeight); -inf: nothing attended to so far.
-template <class Mask, class Scale>
-__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, uint32_t tl, const Scale &sc, const Mask &mask, int before,
-                                             uint64_t *o_step, volatile int *stop, float &m, float &l)
+// reference m is taken from the row's first scores' maximum and rarely moves (see kMostWeight); -inf: nothing
+// attended to so far.  The softmax's sum is of the weights as rounded, made by the matrix instruction (see make_weights).
+// What is rarely taken is in functions of their own, which load the scores again: kept in registers for a second round
+// over them, they cost every half their spills (2048 tokens behind 14000: 354 us where this took 266).
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ void softmax_half(const HalfRow &h, int before, uint64_t *o_step, volatile int *stop, float &m)
 {
-    if (__any_sync(kFull, m == -INFINITY)) {
-        const float top = first_reference(ts, sc, mask);
-        if (m == -INFINITY)
-            m = top;
-    }
-    uint32_t p0[16], p1[16];
-    float s = make_weights(ts, 0, sc, mask, m, p0) + make_weights(ts, 1, sc, mask, m, p1);
-    const bool move = !(s < kMostWeight);
-    if (__any_sync(kFull, move)) {
-        const float top = fmaxf(max_score(ts, 0, sc, mask), max_score(ts, 1, sc, mask));
-        const float mn = move ? fmaxf(top, m) : m;
-        const float f = move ? ex2_approx(m - mn) : 1.f;
-        m = mn;
-        l *= f;
-        s = make_weights(ts, 0, sc, mask, m, p0) + make_weights(ts, 1, sc, mask, m, p1);
-        // Once the product before this one is done, nothing else touches O.  (These scores came
-        // after the product before that, so the wait is one phase behind at most.)
-        if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
-            return false;
-        tc::fence_after();
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            uint32_t o[16];
-            tc::ld16(to + k * 16, o);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tc::st16(to + k * 16, o);
-        }
-        if constexpr (!Scale::kSum) {
-            uint32_t x[16];
-            tc::ld16(tl, x);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-            tc::st16(tl, x);
-        }
-    }
-    l += s;
-    tc::st16(ts, p0);  // columns 2i, 2i + 1 of S are column i of P
-    tc::st16(ts + 16, p1);
+    first_reference<FP8, MASKED>(h, m);
+    uint32_t p[32];
+    const bool move = half_weights<FP8, MASKED>(h, m, p);
+    if (__any_sync(kFull, move))
+        m = move_reference<FP8, MASKED>(h, move, m, o_step, before, stop);
+    else
+        tc::st32(h.ts, p);  // columns 2i, 2i + 1 of S are column i of P
     tc::wait_st();
-    return true;
 }
 
 // Where the partials of part i of an item lie: rows of row tile s.
@@ -669,15 +840,16 @@ template <bool FP8>
 struct Softmax {
     const ChunkArgs &a;
     ChunkShared &sh;
-    uint8_t *stages;
+    uint8_t *stages, *rows;  // (the warp's rows)
     int s, warp, lane, r;
     uint32_t ts, to, tq, tl;
-    int loaded = 0, done = 0, used = 0;
-    bool queried = false;  // the current item's queries are in tensor memory
+    int loaded = 0, checks = 0, done = 0, used = 0;
+    int fetched = -1, queried = -1;  // the item whose queries are in shared memory (or on their way), in tensor memory
     int met[2] = {0, 0};   // times the row tile's warps, and all eight, have met
 
-    __device__ __forceinline__ Softmax(const ChunkArgs &a_, ChunkShared &sh_, uint8_t *stages_, uint32_t tmem)
-        : a(a_), sh(sh_), stages(stages_), warp(threadIdx.x >> 5), lane(threadIdx.x & 31)
+    __device__ __forceinline__ Softmax(const ChunkArgs &a_, ChunkShared &sh_, uint8_t *stages_, uint8_t *rows_, uint32_t tmem)
+        : a(a_), sh(sh_), stages(stages_), rows(rows_ + (threadIdx.x >> 5) * 32 * kRowBytes), warp(threadIdx.x >> 5),
+          lane(threadIdx.x & 31)
     {
         s = warp >> 2;
         r = (warp & 3) * 32 + lane;
@@ -724,21 +896,39 @@ struct Softmax {
         return true;
     }
 
-    __device__ __forceinline__ size_t row_at(const Item &x) const
+    // First of the 4 rows of the warp's i-th token.
+    __device__ __forceinline__ size_t rows_at(const Item &x, int i) const
     {
-        return ((size_t)(x.t0 + x.token(s) + r / kGroup) * kHq + x.head(s) * kGroup + r % kGroup) * kD;
+        return ((size_t)(x.t0 + x.token(s) + (warp & 3) * 8 + i) * kHq + x.head(s) * kGroup) * kD;
     }
+    // Of the warp's 8 tokens, those there are.
+    __device__ __forceinline__ int live_tokens(const Item &x) const { return x.tokens(s) - (warp & 3) * 8; }
 
-    // An item's query rows into tensor memory: 64 values, two to a column.  (Every product of the
-    // previous item with its queries is done when its last scores are there.)
-    __device__ __forceinline__ void queries(const Item &x)
+    // An item's query rows on their way to the warp's rows in shared memory: a token's four heads lie side by side.
+    __device__ __forceinline__ void fetch(const Item &x)
     {
-        const bool live = r / kGroup < x.tokens(s);
-        uint32_t w[32];
-        const uint4 *src = reinterpret_cast<const uint4 *>(a.q + row_at(x));
+        const int live = live_tokens(x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const uint4 v = live ? src[i] : make_uint4(0, 0, 0, 0);
+            const uint32_t dst = smem_addr(rows + (i * kGroup + lane / 8) * kRowBytes + lane % 8 * 16);
+            const uint16_t *src = a.q + rows_at(x, i < live ? i : 0) + lane * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(live > 0 ? src : a.q),
+                         "r"(i < live ? 16 : 0)
+                         : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+
+    // From there into tensor memory: 64 values, two to a column.  (Every product of the previous item
+    // with its queries is done when its last scores are there.)
+    __device__ __forceinline__ void queries()
+    {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(rows + lane * kRowBytes + i * 16);
             w[4 * i] = v.x;
             w[4 * i + 1] = v.y;
             w[4 * i + 2] = v.z;
@@ -752,177 +942,288 @@ struct Softmax {
             tc::mbar_arrive(&sh.q_full[s]);
     }
 
-    // A piece of row tiles; false if a wait gave up.
-    __device__ __forceinline__ bool tiles_piece(Feed &feed, const Item &x)
+    // The warp's rows in shared memory (128 bytes each) to where `dst(i)` says the i-th token's first row begins, `step`
+    // 16-byte chunks from row to row: whole lines.
+    template <class Dst>
+    __device__ __forceinline__ void store_rows(int live, int step, const Dst &dst) const
     {
-        if (!queried)
-            queries(x);
-        queried = false;
-        const int live = x.tokens(s), nt = x.j1 - x.j0;
-        const bool idle = (warp & 3) * 8 >= live;  // no row of the warp is a query: it only keeps step
-        const int pos = x.p0 + x.token(s) + min(r / kGroup, live - 1);
-        float m = -INFINITY, l = 0.f;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < live)
+                __stcg(dst(i) + lane / 8 * step + lane % 8,
+                       *reinterpret_cast<const uint4 *>(rows + (i * kGroup + lane / 8) * kRowBytes + lane % 8 * 16));
+        __syncwarp();
+    }
+
+    // Half hf of the piece's j-th key tile, whose load is in stage st.
+    __device__ __forceinline__ HalfRow half_row(int st, int hf) const
+    {
+        HalfRow h;
+        h.ts = ts + hf * kHalf;
+        h.to = to;
+        h.tl = tl;
+        h.c = a.scale_log2;
+        h.ks = reinterpret_cast<const float4 *>(sh.scales[st][0] + hf * kHalf);
+        h.vs = reinterpret_cast<const float4 *>(sh.scales[st][1] + hf * kHalf);
+        h.mask = make_uint2(0, 0);
+        return h;
+    }
+
+    __device__ __forceinline__ void weights_there(int hf)
+    {
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0)
+            tc::mbar_arrive(&sh.p_full[s][hf]);
+    }
+
+    // A masked key tile.
+    __device__ __forceinline__ bool masked_tile(const Item &x, int j, int pos, float &m, int &bad, uint32_t &nan_lo,
+                                                uint32_t &nan_hi)
+    {
+        const int seq = loaded + x.order(s, j), st = seq % kStages;
+        if (FP8)  // what this thread reads of the stage itself
+            if (!tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+                return false;
+#pragma unroll 1
+        for (int hf = 0; hf < 2; ++hf) {
+            if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
+                return false;
+            tc::fence_after();
+            HalfRow h = half_row(st, hf);
+            h.mask = columns(x, x.j0 + j, hf, pos, a.window, a.sinks);
+            softmax_half<FP8, true>(h, 2 * (done + j) + hf, &sh.o_step[s], &sh.stop, m);
+            if (hf == 1) {  // (until its weights are there, the stage is this tile's)
+                bad |= *(volatile int *)&sh.bad[st];
+                const int check = checks + x.masked_loads(j) + (x.kind == plan::kHeads ? s : 0);
+                if (!FP8 && !tc::wait_warp(&sh.checked[check % kStages], (check / kStages) & 1, &sh.stop))
+                    return false;
+                if (*(volatile int *)&sh.noted[st] == seq) {
+                    reached(h.mask, sh.poison[st], 1, seq, nan_lo, nan_hi);
+                    reached(columns(x, x.j0 + j, 0, pos, a.window, a.sinks), sh.poison[st], 0, seq, nan_lo, nan_hi);
+                }
+            }
+            weights_there(hf);
+        }
+        return true;
+    }
+
+    // Key tiles j0 .. j1 - 1 of the piece, in which every row attends to every place.  The scores come 32 at a time,
+    // the second on their way while the first become weights (2048 tokens behind 14000: 233 us where 64 at a
+    // time took 255; the next half's first on their way as well: 282, registers that go round a loop).
+    __device__ __forceinline__ bool plain_tiles(const Item &x, int j0, int j1, float &m, int &bad)
+    {
+#pragma unroll 1
+        for (int k = 2 * j0; k < 2 * j1; ++k) {
+            const int j = k >> 1, hf = k & 1, seq = loaded + x.order(s, j), st = seq % kStages;
+            if (FP8 && hf == 0 && !tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+                return false;  // (what this thread reads of the stage itself)
+            if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
+                return false;
+            tc::fence_after();
+            const HalfRow h = half_row(st, hf);
+            uint32_t w0[32], w1[32], p[32];
+            tc::ld32(h.ts, w0);
+            if (k == 2 * j0)
+                first_reference<FP8, false>(h, m);
+            tc::ld32_begin(h.ts + 32, w1);
+            Excess<FP8> ex;
+            weigh<FP8, false>(h, 0, w0, m, p, ex);
+            tc::loads_done(w1);
+            weigh<FP8, false>(h, 1, w1, m, p + 16, ex);
+            if (hf == 1)  // (until its weights are there, the stage is this tile's)
+                bad |= *(volatile int *)&sh.bad[st];
+            const bool move = ex.any();
+            if (__any_sync(kFull, move))
+                m = move_reference<FP8, false>(h, move, m, &sh.o_step[s], 2 * (done + j) + hf, &sh.stop);
+            else
+                tc::st32(h.ts, p);  // columns 2i, 2i + 1 of S are column i of P
+            tc::wait_st();
+            weights_there(hf);
+        }
+        return true;
+    }
+
+    // A piece of row tiles; false if a wait gave up.
+    __device__ __forceinline__ bool tiles_piece(Feed &feed, const Item &it)
+    {
+        const Item x = it;
+        if (queried != feed.n) {
+            if (fetched != feed.n)
+                fetch(x);
+            queries();
+            const Item *y = feed.look(1);
+            if (y && y->kind != plan::kSingle) {
+                fetch(*y);
+                fetched = feed.n + 1;
+            }
+        }
+        const int live = live_tokens(x), nt = x.j1 - x.j0;
+        const bool idle = live <= 0;  // no row of the warp is a query: it only keeps step
+        const int pos = x.p0 + x.token(s) + min(r / kGroup, x.tokens(s) - 1);
+        float m = -INFINITY;
         int bad = 0;
         uint32_t nan_lo = 0, nan_hi = 0;
-        for (int j = 0; j < nt; ++j) {
-            const int seq = loaded + x.order(s, j), st = seq % kStages;
-            const bool masked = x.masked(x.j0 + j, a.window);
-            if (a.expire && s == 0 && used == 0 && j == 0 && blockIdx.x == 0) {
-                *(volatile int *)&sh.stop = 1;
-                return false;
-            }
-            if (FP8 || masked)  // what this thread reads of the stage itself
-                if (!tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
-                    return false;
-            bool noted = false;
-            if (masked) {
-                if (clear_values(x, x.j0 + j, stages + st * kStageSize, sh.poison[st], seq))
-                    sh.noted[s] = seq;
-                if (!meet(false))
-                    return false;
-                noted = *(volatile int *)&sh.noted[s] == seq;
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
-                    return false;
-                if (!idle) {
-                    tc::fence_after();
-                    const int before = 2 * (done + j) + hf;  // products of this row tile so far
-                    const auto half = [&](const auto &sc) {
-                        uint64_t *step = &sh.o_step[s];
-                        if (!masked)
-                            return softmax_half(ts + hf * kHalf, to, tl, sc, EveryColumn{}, before, step, &sh.stop, m, l);
-                        const ColumnBits mask = columns(x, x.j0 + j, hf, pos, a.window, a.sinks);
-                        if (noted) {
-                            for (int i = 0; i < kHalf; ++i)
-                                if ((i < 32 ? mask.w0 : mask.w1) >> (i & 31) & 1u) {
-                                    const Poison &note = sh.poison[st][i / 8 * kPage + 8 * hf + i % 8];
-                                    if (note.load == seq) {
-                                        nan_lo |= note.lo;
-                                        nan_hi |= note.hi;
-                                    }
-                                }
-                        }
-                        return softmax_half(ts + hf * kHalf, to, tl, sc, mask, before, step, &sh.stop, m, l);
-                    };
-                    bool go;
-                    if constexpr (FP8) {
-                        const float2 *sc = reinterpret_cast<const float2 *>(sh.scales[st]) + hf * 32;
-                        go = half(RowScales{sc, sc + 64, sc + 128});
-                    } else {
-                        go = half(OneFactor{a.scale_log2});
-                    }
-                    if (!go)
+        if (a.expire && s == 0 && used == 0 && blockIdx.x == 0) {
+            *(volatile int *)&sh.stop = 1;
+            return false;
+        }
+        for (int j = 0; j < nt;) {
+            if (idle) {
+                for (int hf = 0; hf < 2; ++hf) {
+                    if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
                         return false;
-                    if (hf == 0)
-                        bad |= *(volatile int *)&sh.bad[st];
-                    tc::fence_before();
+                    if (lane == 0)
+                        tc::mbar_arrive(&sh.p_full[s][hf]);
                 }
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(&sh.p_full[s][hf]);
+                ++j;
+            } else if (x.masked(x.j0 + j)) {
+                if (!masked_tile(x, j, pos, m, bad, nan_lo, nan_hi))
+                    return false;
+                ++j;
+            } else {
+                const int end = min(nt, (x.j0 + j < x.plain ? x.plain : x.plain1) - x.j0);
+                if (!plain_tiles(x, j, end, m, bad))
+                    return false;
+                j = end;
             }
         }
         // the next item's first scores are made while this one's last product and its output end
         const Item *y = feed.look(1);
         if (y && y->kind != plan::kSingle) {
-            queries(*y);
-            queried = true;
+            if (fetched != feed.n + 1)
+                fetch(*y);
+            queries();
+            queried = feed.n + 1;
         }
         if (!tc::wait_warp(&sh.o_full[s], used & 1, &sh.stop))
             return false;
         tc::fence_after();
-        if constexpr (!FP8) {
+        float l;
+        {
             uint32_t sums[16];
             tc::ld16(tl, sums);
-            l = __uint_as_float(sums[0]);
+            l = __uint_as_float(sums[0]) + (FP8 ? __uint_as_float(sums[1]) : 0.f);
         }
         if (bad && r == 0 && a.err)
             atomicOr(a.err, PKV_DEVERR_PAGE_RANGE);
-        const bool mine = r / kGroup < live;
-        uint32_t o[2][32];
-        tc::ld32(to, o[0]);
-        tc::ld32(to + 32, o[1]);
+        uint32_t o[64];
+        tc::ld64(to, o);
         if (nan_lo | nan_hi) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                if (nan_lo >> i & 1u)
-                    o[0][i] = 0x7fffffffu;
-                if (nan_hi >> i & 1u)
-                    o[1][i] = 0x7fffffffu;
-            }
+            for (int i = 0; i < 64; ++i)
+                if ((i < 32 ? nan_lo : nan_hi) >> (i & 31) & 1u)
+                    o[i] = 0x7fffffffu;
         }
+        uint4 *own = reinterpret_cast<uint4 *>(rows + lane * kRowBytes);
         if (x.parts == 1) {
-            if (mine)
-                store_row(x, reinterpret_cast<const float *>(o[0]), bad ? 0.f : inverse_sum(l), bad);
-        } else {
-            const size_t at = part_rows(x, x.me, s) + r;
-            if (mine) {
-                float4 *to4 = reinterpret_cast<float4 *>(a.part_o + at * kD);
+            const float f = inverse_sum(l);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const uint32_t *v = &o[i / 8][i % 8 * 4];
-                    __stcg(to4 + i, make_float4(__uint_as_float(v[0]), __uint_as_float(v[1]), __uint_as_float(v[2]),
-                                                __uint_as_float(v[3])));
-                }
-                __stcg(a.part_ml + at, make_float2(bad ? INFINITY : m, l));
+            for (int i = 0; i < 8; ++i) {
+                uint32_t v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    v[k] = bad ? 0u : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
+                own[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
+            store_rows(live, 8, [&](int i) { return reinterpret_cast<uint4 *>(a.out + rows_at(x, i)); });
+        } else {
+            const size_t at = part_rows(x, x.me, s) + (warp & 3) * 32;
+#pragma unroll
+            for (int q2 = 0; q2 < 2; ++q2) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    own[i] = make_uint4(o[32 * q2 + 4 * i], o[32 * q2 + 4 * i + 1], o[32 * q2 + 4 * i + 2],
+                                        o[32 * q2 + 4 * i + 3]);
+                store_rows(live, 16, [&](int i) {
+                    return reinterpret_cast<uint4 *>(a.part_o + (at + i * kGroup) * kD) + 8 * q2;
+                });
+            }
+            if (lane / kGroup < live)
+                __stcg(a.part_ml + at + lane, make_float2(bad ? INFINITY : m, l));
             bool last;
             if (!draw_ticket(x, false, last))
                 return false;
-            if (last && mine)
-                join(x);
+            if (last)
+                join(x, live);
+        }
+        if (queried == feed.n + 1) {
+            const Item *z = feed.look(2);
+            if (z && z->kind != plan::kSingle) {
+                fetch(*z);
+                fetched = feed.n + 2;
+            }
         }
         loaded += x.loads();
+        checks += x.masked_loads(nt);
         done += nt;
         ++used;
         return true;
     }
 
-    __device__ __forceinline__ void store_row(const Item &x, const float *o, float f, bool bad) const
+    // The warp's rows of a cut item, of all parts: two rows at a time, 16 lanes each, 16 bytes a lane, 16 rows'
+    // loads of a part on their way at once.
+    __device__ __forceinline__ void join(const Item &x, int live) const
     {
-        uint4 *dst = reinterpret_cast<uint4 *>(a.out + row_at(x));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            uint4 v = make_uint4(pack_bf16x2(o[8 * i] * f, o[8 * i + 1] * f), pack_bf16x2(o[8 * i + 2] * f, o[8 * i + 3] * f),
-                                 pack_bf16x2(o[8 * i + 4] * f, o[8 * i + 5] * f),
-                                 pack_bf16x2(o[8 * i + 6] * f, o[8 * i + 7] * f));
-            dst[i] = bad ? make_uint4(0, 0, 0, 0) : v;
-        }
-    }
-
-    // This thread's row of a cut item, of all parts.
-    __device__ __forceinline__ void join(const Item &x) const
-    {
-        float M = -INFINITY;
+        if (live <= 0)
+            return;
+        const int w0 = (warp & 3) * 32;
+        float M = -INFINITY;  // of row `lane`
         for (int i = 0; i < x.parts; ++i)
-            M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, i, s) + r).x);
-        float o[kD], l = 0.f;
+            M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, i, s) + w0 + lane).x);
+#pragma unroll 1
+        for (int k0 = 0; k0 < 16; k0 += 8) {
+            float l = 0.f;
+            float4 o[8];
 #pragma unroll
-        for (int i = 0; i < kD; ++i)
-            o[i] = 0.f;
-        for (int i = 0; i < x.parts; ++i) {
-            const size_t at = part_rows(x, i, s) + r;
-            const float2 ml = __ldcg(a.part_ml + at);
-            const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-            if (ml.x == -INFINITY)
-                continue;
-            l = fmaf(f, ml.y, l);
-            const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kD);
+            for (int k = 0; k < 8; ++k)
+                o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+            for (int i = 0; i < x.parts; ++i) {
+                const size_t at = part_rows(x, i, s) + w0;
+                const float2 ml = __ldcg(a.part_ml + at + lane);
+                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kD) + k0 * 32 + lane;
+                float4 v[8];
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float4 v = __ldcg(src + c);
-                o[4 * c] = fmaf(f, v.x, o[4 * c]);
-                o[4 * c + 1] = fmaf(f, v.y, o[4 * c + 1]);
-                o[4 * c + 2] = fmaf(f, v.z, o[4 * c + 2]);
-                o[4 * c + 3] = fmaf(f, v.w, o[4 * c + 3]);
+                for (int k = 0; k < 8; ++k)
+                    v[k] = __ldcg(src + k * 32);
+                const bool none = ml.x == -INFINITY;  // (and then nothing may be wrong with it)
+                const float f = none ? -1.f : ex2_approx(ml.x - M);
+                l = none ? l : fmaf(f, ml.y, l);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float g = __shfl_sync(kFull, f, 2 * (k0 + k) + lane / 16);
+                    if (!(g < 0.f)) {
+                        o[k].x = fmaf(g, v[k].x, o[k].x);
+                        o[k].y = fmaf(g, v[k].y, o[k].y);
+                        o[k].z = fmaf(g, v[k].z, o[k].z);
+                        o[k].w = fmaf(g, v[k].w, o[k].w);
+                    }
+                }
+            }
+            const float inv = inverse_sum(l);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int row = 2 * (k0 + k) + lane / 16;
+                const float g = __shfl_sync(kFull, inv, row), top = __shfl_sync(kFull, M, row);
+                uint2 v = make_uint2(pack_bf16x2(o[k].x * g, o[k].y * g), pack_bf16x2(o[k].z * g, o[k].w * g));
+                if (top == INFINITY)
+                    v = make_uint2(0, 0);
+                if (row / kGroup < live)
+                    *reinterpret_cast<uint2 *>(a.out + rows_at(x, row / kGroup) + row % kGroup * kD + lane % 16 * 4) = v;
             }
         }
-        store_row(x, o, inverse_sum(l), M == INFINITY);
     }
 
     // ---- a single token: the 8 warps take a page each of every key tile
+
+    // Warp i's softmax state, in its rows (no queries are on their way there: those of an item are fetched
+    // when the one before it, of row tiles too, begins or ends).
+    __device__ __forceinline__ float *state(int i) const
+    {
+        return reinterpret_cast<float *>(rows + (i - warp) * 32 * kRowBytes);
+    }
 
     __device__ __forceinline__ bool single_piece(const Item &x)
     {
@@ -961,19 +1262,19 @@ struct Softmax {
             if (lane == 0)
                 tc::mbar_arrive(&sh.empty[st]);
         }
-        w.store_state(sh.states[warp]);
+        w.store_state(state(warp));
         if (!meet(true))
             return false;
         const int hl = threadIdx.x >> 6, d = threadIdx.x & 63;
         float M = -INFINITY, l = 0.f, o = 0.f;
 #pragma unroll
         for (int i = 0; i < kTeam; ++i)
-            M = fmaxf(M, sh.states[i][hl]);
+            M = fmaxf(M, state(i)[hl]);
 #pragma unroll
         for (int i = 0; i < kTeam; ++i) {
-            const float mi = sh.states[i][hl], f = mi == -INFINITY ? 0.f : ex2_approx(mi - M);
-            l = fmaf(f, sh.states[i][4 + hl], l);
-            o = fmaf(f, sh.states[i][8 + hl * kD + d], o);
+            const float mi = state(i)[hl], f = mi == -INFINITY ? 0.f : ex2_approx(mi - M);
+            l = fmaf(f, state(i)[4 + hl], l);
+            o = fmaf(f, state(i)[8 + hl * kD + d], o);
         }
         if (!meet(true))  // the states may be written again
             return false;
@@ -1016,7 +1317,8 @@ struct Softmax {
         Feed feed(sh);
         for (const Item *x; (x = feed.look()) != nullptr; feed.let_go())
             if (!(x->kind == plan::kSingle ? single_piece(*x) : tiles_piece(feed, *x)))
-                return;
+                break;
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
 };
 
@@ -1029,17 +1331,20 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded address: the compiler keeps shared-memory instructions)
     uint8_t *stages = smem_raw + (-smem_addr(smem_raw) & 1023u);
-    uint8_t *raws = stages + kStages * kStageSize;  // (BF16 pages: the ones)
-    ChunkShared &sh = *reinterpret_cast<ChunkShared *>(raws + (FP8 ? kRaws * kRawSize : kOnesSize));
+    uint8_t *sums = stages + kStages * kStageSize;
+    uint8_t *rows = sums + sums_size(FP8), *raws = rows + kRowsSize;
+    ChunkShared &sh = *reinterpret_cast<ChunkShared *>(raws + (FP8 ? kRaws * kRawSize : 0));
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
-            mbar_init(&sh.full[i], FP8 ? kConverters : 1);
+            mbar_init(&sh.full[i], FP8 ? kPreparers : 1);
             mbar_init(&sh.empty[i], kTeam);
+            mbar_init(&sh.checked[i], 1);
+            sh.noted[i] = -1;
         }
         for (int i = 0; i < kRaws; ++i) {
             mbar_init(&sh.raw_full[i], 1);
-            mbar_init(&sh.raw_empty[i], kConverters);
+            mbar_init(&sh.raw_empty[i], kPreparers);
         }
         for (int s = 0; s < 2; ++s) {
             for (int h = 0; h < 2; ++h) {
@@ -1051,9 +1356,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
             mbar_init(&sh.o_full[s], 1);
             mbar_init(&sh.drained[s], 1);
             mbar_init(&sh.group[s], 4);
-            sh.noted[s] = -1;
         }
         mbar_init(&sh.group[2], kTeam);
+        mbar_init(&sh.group[3], kPreparers);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
             mbar_init(&sh.item_empty[i], consumers(FP8));
@@ -1067,8 +1372,8 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
     for (int i = threadIdx.x; i < kStages * kTilePages * kPage; i += chunk_threads(FP8))
         (&sh.poison[0][0])[i].load = -1;
     if (!FP8) {
-        for (int i = threadIdx.x; i < kOnesSize / 4; i += chunk_threads(FP8))
-            reinterpret_cast<uint32_t *>(raws)[i] = 0x3f803f80u;
+        for (int i = threadIdx.x; i < sums_size(FP8) / 4; i += chunk_threads(FP8))
+            reinterpret_cast<uint32_t *>(sums)[i] = 0x3f803f80u;
         fence_proxy_async_smem();
     }
     grid_dependency_wait();
@@ -1083,18 +1388,18 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
     if (warp < kLoader) {
         if constexpr (FP8)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
-        Softmax<FP8>(a, sh, stages, tmem).run();
+        Softmax<FP8>(a, sh, stages, rows, tmem).run();
     } else {
         if constexpr (FP8)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == kLoader)
             loader<FP8>(&tmap, a, stages, raws, sh);
         else if (warp < kIssuer + 2)
-            issuer<FP8>(stages, raws, sh, tmem, warp - kIssuer);
+            issuer<FP8>(stages, sums, sh, tmem, warp - kIssuer);
         else if (warp == kScheduler)
             scheduler<FP8>(a, sh);
         else if (FP8)
-            converter(a, raws, stages, sh);
+            preparer(a, raws, stages, sums, sh);
     }
     __syncthreads();
     if (sh.stop && warp == kScheduler) {
@@ -1134,7 +1439,8 @@ int launch_chunk(const pkv_pool *pool, const ChunkArgs &a, cudaStream_t s, bool 
     const CUtensorMap *tmap = pool_tensor_map(pool);
     if (!tmap)
         return PKV_ERR_CUDA;
-    constexpr int smem = 1024 + kStages * kStageSize + (FP8 ? kRaws * kRawSize : kOnesSize) + (int)sizeof(ChunkShared);
+    constexpr int smem = 1024 + kStages * kStageSize + sums_size(FP8) + kRowsSize + (FP8 ? kRaws * kRawSize : 0) +
+                         (int)sizeof(ChunkShared);
     static_assert(smem <= 227 * 1024, "shared memory of an SM");
     static PerDeviceOnce attr;
     if (const int st = ensure_smem_attr(attr, chunk_kernel<FP8>, smem); st != PKV_OK)

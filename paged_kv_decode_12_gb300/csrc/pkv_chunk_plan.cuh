@@ -51,6 +51,23 @@ PKV_HD PageList page_list(int first, int last, int window, int sinks)
     return x;
 }
 
+// a / b of numbers that are not negative (in 32 bits where they fit: a short line is a short call).
+PKV_HD int64_t divide(int64_t a, int64_t b)
+{
+    if (((uint64_t)a | (uint64_t)b) >> 32)
+        return a / b;
+    return (uint32_t)a / (uint32_t)b;
+}
+
+// a / b for a result below 8, as it is known to be, by comparisons.
+PKV_HD int eighth(int64_t a, int64_t b)
+{
+    int n = 0;
+    for (int i = 1; i < 8; ++i)
+        n += a >= i * b;
+    return n;
+}
+
 // The items of one sequence of n new tokens, the first at position c.
 struct Sequence {
     int n, c, window, sinks;
@@ -115,9 +132,9 @@ struct Sequence {
 struct Line {
     int64_t length;
     int ctas;
-    PKV_HD int64_t border(int c) const { return length * c / ctas; }
+    PKV_HD int64_t border(int c) const { return divide(length * c, ctas); }
     // The first CTA whose end is not below x.
-    PKV_HD int ending_from(int64_t x) const { return (int)((x * ctas + length - 1) / length) - 1; }
+    PKV_HD int ending_from(int64_t x) const { return (int)divide(x * ctas + length - 1, length) - 1; }
 };
 
 // Key tiles of an item before a border that lies t into it.

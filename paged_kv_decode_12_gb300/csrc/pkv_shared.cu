@@ -316,7 +316,8 @@ __device__ __forceinline__ void prefix_converter(const PrefixArgs &a, const uint
             if (!tc::wait_warp(&bars.raw_full[rs], (seq / kRaws) & 1, &bars.stop) ||
                 (seq >= kStages && !tc::wait_warp(&bars.empty[st], (seq / kStages - 1) & 1, &bars.stop)))
                 return;
-            convert_tile(raws + rs * kRawSize, stages + st * kStageSize, bars.scales[st], a.scale_log2, t);
+            convert_codes(raws + rs * kRawSize, stages + st * kStageSize, t);
+            convert_scales(raws + rs * kRawSize, bars.scales[st], a.scale_log2, t);
             if (t == 0)
                 bars.bad[st] = bars.raw_bad[rs];
             fence_proxy_async_smem();

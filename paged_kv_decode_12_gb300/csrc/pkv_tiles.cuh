@@ -33,9 +33,8 @@ __device__ __forceinline__ void bf16_of_e4m3x4(uint32_t w, uint32_t &lo, uint32_
     hi = bf16x2_of_f16x2(b);
 }
 
-// One tile of raw units into a stage of the BF16 layout, and its row scales ([K (times scale log2 e), V, 1 /
-// V][half][64] in the order of the scores' columns), by 128 threads.
-__device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, float *scales, float scale_log2, int t)
+// One tile of raw units into a stage of the BF16 layout, by 128 threads.
+__device__ __forceinline__ void convert_codes(const uint8_t *raw, uint8_t *dst, int t)
 {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {  // K: 16 codes of a row, two chunks of 8 values
@@ -62,6 +61,11 @@ __device__ __forceinline__ void convert_tile(const uint8_t *raw, uint8_t *dst, f
         *reinterpret_cast<uint4 *>(v + swz(2 * pair, chunk)) = even;
         *reinterpret_cast<uint4 *>(v + swz(2 * pair + 1, chunk)) = odd;
     }
+}
+
+// Its row scales, [K (times scale log2 e), V, 1 / V][half][64] in the order of the scores' columns.
+__device__ __forceinline__ void convert_scales(const uint8_t *raw, float *scales, float scale_log2, int t)
+{
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {  // thread = (page, slot)
         const int page = t / kPage, slot = t % kPage;
@@ -95,7 +99,8 @@ __device__ __forceinline__ void issue_scores(uint32_t k, uint32_t s, uint32_t q,
     __syncwarp();
 }
 
-template <bool FIRST, bool SUM>
+// SUM: L += P times 16 columns beside V (of ones; or, STEP bytes / 16 apart for every 16 rows of P, of anything).
+template <bool FIRST, bool SUM, int STEP = 0>
 __device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p, uint32_t ones, uint32_t l,
                                              uint64_t *free_stage, int uses, uint64_t *done, uint64_t *last)
 {
@@ -113,7 +118,7 @@ __device__ __forceinline__ void issue_output(uint32_t v, uint32_t o, uint32_t p,
             tc::mma_ts<!FIRST>(l, p, one, kOnesHi, kOnes);
 #pragma unroll
             for (int i = 1; i < kHalf / 16; ++i)
-                tc::mma_ts<true>(l, p + i * 8, one, kOnesHi, kOnes);
+                tc::mma_ts<true>(l, p + i * 8, one + i * STEP, kOnesHi, kOnes);
         }
         tc::commit(done);
         if (last)
