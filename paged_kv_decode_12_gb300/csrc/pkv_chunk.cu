@@ -39,6 +39,7 @@ static_assert(kStateFloats * 4 <= 32 * kRowBytes, "a warp's softmax state fits i
 // the inverses of V's scales, as two BF16 numbers in the first two columns (the others do not matter).
 constexpr int sums_size(bool fp8) { return fp8 ? (2 * kStages + 1) * 1024 : 2048; }
 constexpr int kCols = 512;           // tensor memory, all of it
+constexpr int kTokenRow = kHq * kD;  // elements of a token's query rows
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColL = 448;  // + 128 / 64 / 32 / 16 for the second row tile
 
 constexpr int chunk_threads(bool fp8) { return fp8 ? (kPreparer + kPreparers) * 32 : kPreparer * 32; }
@@ -70,14 +71,14 @@ struct Item {
     int j0, j1, nt;        // key tiles of the piece; of the whole item
     int first, parts, me;  // CTAs that share the item, and this one's place among them
     int plain, plain0, plain1;  // key tiles in which every row attends to every place: below plain, and plain0 .. plain1 - 1
-    int pad[3];
+    int pad;
+    int64_t row;           // first query row, in elements
     __device__ __forceinline__ int page(int i) const { return i < sink ? i : i - sink + from; }
     __device__ __forceinline__ int loads() const { return (j1 - j0) * (kind == plan::kHeads ? 2 : 1); }
     // A row tile's first token within the item, its tokens, its KV head, and the place among the piece's loads of
     // the piece's j-th key tile.
     __device__ __forceinline__ int token(int s) const { return kind == plan::kPair ? 32 * s : 0; }
     __device__ __forceinline__ int tokens(int s) const { return min(plan::kRowTokens, n - token(s)); }
-    __device__ __forceinline__ int head(int s) const { return kind == plan::kHeads ? g + s : g; }
     __device__ __forceinline__ int order(int s, int j) const { return kind == plan::kHeads ? 2 * j + s : j; }
     __device__ __forceinline__ bool masked(int j) const { return j >= plain && (j < plain0 || j >= plain1); }
     // Loads of the piece before its j-th key tile's first whose tiles are masked.
@@ -133,6 +134,18 @@ struct ChunkShared {
     int64_t sums[512];                           // costs of the sequences before each thread's
     alignas(16) float scales[kStages][2][kTilePages * kPage];  // (FP8) row scales: K's times scale log2 e, V's
 };
+
+// tc::wait_warp, whose polling is out of the way: it is waited in many places, and code that is rarely run next to
+// what is run often costs instruction fetches.
+__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *stop)
+{
+    return tc::wait_warp(bar, parity, stop);
+}
+
+__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *stop)
+{
+    return tc::try_warp(bar, parity) || wait_long(bar, parity, stop);
+}
 
 // ------------------------------------------------------------------ the plan
 
@@ -218,16 +231,32 @@ __device__ __forceinline__ void make_plan(const ChunkArgs &a, ChunkShared &sh)
     }
 }
 
-// The pieces of this CTA's run, in order, by a whole warp; `take(item)` may end it by returning false.
-template <bool FP8, class Take>
-__device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkShared &sh, const Take &take)
+// A piece for the other warps, `n` so far; false if a wait gave up.
+__device__ __forceinline__ bool give(ChunkShared &sh, const Item &it, int &n)
 {
+    const int at = n % kItems;
+    if (n >= kItems && !wait_for(&sh.item_empty[at], (n / kItems - 1) & 1, &sh.stop))
+        return false;
+    if ((threadIdx.x & 31) == 0) {
+        sh.items[at] = it;
+        tc::mbar_arrive(&sh.item_full[at]);
+    }
+    __syncwarp();
+    ++n;
+    return true;
+}
+
+// The pieces of this CTA's run, in order, by a whole warp, given to the others; or (`over`: something gave up) the
+// tickets of cut items that were not drawn, so that the next call finds zeros.
+template <bool FP8>
+__device__ __noinline__ void pieces(const ChunkArgs &a, ChunkShared &sh, bool over)
+{
+    int given = 0;
     const Costs k = costs<FP8>();
     const plan::Line line = plan::line_of(sh.length, gridDim.x, kLeastCost);
-    if (line.length == 0 || (int)blockIdx.x >= line.ctas)
-        return;
     const int lane = threadIdx.x & 31, per = (a.B + chunk_threads(FP8) - 1) / chunk_threads(FP8);
-    const int64_t x0 = line.border(blockIdx.x), x1 = line.border(blockIdx.x + 1);
+    const bool work = line.length > 0 && (int)blockIdx.x < line.ctas;
+    const int64_t x0 = work ? line.border(blockIdx.x) : 0, x1 = work ? line.border(blockIdx.x + 1) : 0;
     int64_t x = x0;
     while (x < x1) {
         // the thread whose sequences hold x (the last whose sum is not above it), and the sequence
@@ -250,7 +279,7 @@ __device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkSh
         }
         const unsigned behind = __ballot_sync(kFull, sh.sums[lo] + upto > x);
         if (!behind)
-            return;  // (not reached: the sums add up to the length)
+            break;  // (not reached: the sums add up to the length)
         const int at = __ffs(behind) - 1, b = lo * per + at;
         const int64_t begin = sh.sums[lo] + __shfl_sync(kFull, upto - mine, at), end = sh.sums[lo] + __shfl_sync(kFull, upto, at);
         const Row row = row_of(a, b);
@@ -303,42 +332,31 @@ __device__ __forceinline__ void for_each_piece(const ChunkArgs &a, const ChunkSh
             it.from = pages.from;
             it.count = pages.count;
             it.nt = pages.tiles();
-            const int tile = k.tile[it.kind], over = k.item[it.kind];
-            it.j0 = x0 <= s ? 0 : plan::cut(x0 - s, it.nt, tile, over);
-            it.j1 = plan::cut(x1 - s, it.nt, tile, over);
-            const plan::Parts parts = plan::parts_of(line, s, it.nt, tile, over);
+            const int tile = k.tile[it.kind], item = k.item[it.kind];
+            it.j0 = x0 <= s ? 0 : plan::cut(x0 - s, it.nt, tile, item);
+            it.j1 = plan::cut(x1 - s, it.nt, tile, item);
+            const plan::Parts parts = plan::parts_of(line, s, it.nt, tile, item);
             it.first = parts.first;
             it.parts = parts.count;
             it.me = blockIdx.x - parts.first;
             it.find_plain(a.window, a.sinks);
-            if (it.j0 < it.j1 && !take(it))
-                return;
-            x = s + (int64_t)it.nt * tile + over;
+            it.row = ((int64_t)it.t0 * kHq + it.g * kGroup) * kD;
+            if (it.j0 < it.j1) {
+                if (!over) {
+                    if (!give(sh, it, given))
+                        return;
+                } else if (it.parts > 1 && lane == 0) {
+                    for (int r = 0; r < (it.kind == plan::kSingle ? 1 : 2); ++r)
+                        if (!sh.taken[it.me == 0][r] && atomicAdd(&a.tickets[it.first * 2 + r], 1) == it.parts - 1)
+                            a.tickets[it.first * 2 + r] = 0;
+                }
+            }
+            x = s + (int64_t)it.nt * tile + item;
         }
     }
-}
-
-template <bool FP8>
-__device__ __forceinline__ void scheduler(const ChunkArgs &a, ChunkShared &sh)
-{
-    int n = 0;
-    const auto give = [&](const Item &it) {
-        const int at = n % kItems;
-        if (n >= kItems && !tc::wait_warp(&sh.item_empty[at], (n / kItems - 1) & 1, &sh.stop))
-            return false;
-        if ((threadIdx.x & 31) == 0) {
-            sh.items[at] = it;
-            tc::mbar_arrive(&sh.item_full[at]);
-        }
-        __syncwarp();
-        ++n;
-        return true;
-    };
-    bool open = true;
-    for_each_piece<FP8>(a, sh, [&](const Item &it) { return open = give(it); });
-    if (open) {
+    if (!over) {
         Item end = {};
-        (void)give(end);
+        (void)give(sh, end, given);
     }
 }
 
@@ -351,7 +369,7 @@ struct Feed {
     __device__ __forceinline__ const Item *look(int ahead = 0)
     {
         const int at = (n + ahead) % kItems;
-        if (!tc::wait_warp(&sh.item_full[at], ((n + ahead) / kItems) & 1, &sh.stop))
+        if (!wait_for(&sh.item_full[at], ((n + ahead) / kItems) & 1, &sh.stop))
             return nullptr;
         return sh.items[at].kind == plan::kEnd ? nullptr : &sh.items[at];
     }
@@ -400,7 +418,7 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
         const uint64_t policy = single ? once_policy : shared_policy;
         if (FP8 && single)  // the preparers are done with every stage before
             for (int i = max(raw - kRaws, 0); go && i < raw; ++i)
-                go = tc::wait_warp(&sh.raw_empty[i % kRaws], (i / kRaws) & 1, &sh.stop);
+                go = wait_for(&sh.raw_empty[i % kRaws], (i / kRaws) & 1, &sh.stop);
         int id4 = 0;  // lane l: the id of page l of the current run of 4 key tiles
         unsigned bad4 = 0;
         for (int j = x.j0; j < x.j1 && go; ++j) {
@@ -418,11 +436,11 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
                 const int st = through_raw ? raw % kRaws : seq % kStages;
                 uint64_t *full = through_raw ? &sh.raw_full[st] : &sh.full[st];
                 if (through_raw) {
-                    if (raw >= kRaws && !tc::wait_warp(&sh.raw_empty[st], (raw / kRaws - 1) & 1, &sh.stop)) {
+                    if (raw >= kRaws && !wait_for(&sh.raw_empty[st], (raw / kRaws - 1) & 1, &sh.stop)) {
                         go = false;
                         break;
                     }
-                } else if (seq >= kStages && !tc::wait_warp(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)) {
+                } else if (seq >= kStages && !wait_for(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)) {
                     go = false;
                     break;
                 }
@@ -511,8 +529,8 @@ __device__ __forceinline__ void preparer(const ChunkArgs &a, const uint8_t *raws
         }
         for (int i = 0; i < n; ++i, ++seq, ++raw) {
             const int j = x.j0 + (x.kind == plan::kHeads ? i / 2 : i), rs = raw % kRaws, st = seq % kStages;
-            if (!tc::wait_warp(&sh.raw_full[rs], (raw / kRaws) & 1, &sh.stop) ||
-                (seq >= kStages && !tc::wait_warp(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)))
+            if (!wait_for(&sh.raw_full[rs], (raw / kRaws) & 1, &sh.stop) ||
+                (seq >= kStages && !wait_for(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)))
                 return;
             const uint8_t *raw_tile = raws + rs * kRawSize;
             uint8_t *stage = stages + st * kStageSize;
@@ -540,7 +558,7 @@ __device__ __forceinline__ void preparer(const ChunkArgs &a, const uint8_t *raws
                 __syncwarp();
                 if (lane == 0)
                     tc::mbar_arrive(&sh.group[3]);
-                if (!tc::wait_warp(&sh.group[3], checks++ & 1, &sh.stop))
+                if (!wait_for(&sh.group[3], checks++ & 1, &sh.stop))
                     return;
                 check_values<kPreparers * 32>(x, j, stage, sh.poison[st], &sh.noted[st], seq, t);
             }
@@ -572,7 +590,7 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, Chu
             const auto scores = [&](int j, int h) {
                 const int seq = loaded + x.order(s, j), st = seq % kStages;
                 if (h == 0) {
-                    if (!tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+                    if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
                         return false;
                     tc::fence_after();
                 }
@@ -592,10 +610,10 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, Chu
                         if ((threadIdx.x & 31) == 0)
                             tc::mbar_arrive(checked);
                     }
-                    if (!tc::wait_warp(checked, (check / kStages) & 1, &sh.stop))
+                    if (!wait_for(checked, (check / kStages) & 1, &sh.stop))
                         return false;
                 }
-                if (!tc::wait_warp(&sh.p_full[s][h], (done + j) & 1, &sh.stop))
+                if (!wait_for(&sh.p_full[s][h], (done + j) & 1, &sh.stop))
                     return false;
                 tc::fence_after();
                 const uint32_t v = base + st * kStageSize + kTileBytes + h * 1024, pw = ts + h * kHalf;
@@ -608,7 +626,7 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, Chu
                     issue_output<false, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
                 return true;
             };
-            bool go = tc::wait_warp(&sh.q_full[s], used & 1, &sh.stop);
+            bool go = wait_for(&sh.q_full[s], used & 1, &sh.stop);
             tc::fence_after();
             go = go && scores(0, 0) && scores(0, 1);
             for (int j = 0; j < nt && go; ++j)
@@ -644,12 +662,14 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0
 __device__ __forceinline__ uint2 columns(const Item &x, int j, int hf, int p, int window, int sinks)
 {
     uint32_t w[2] = {0, 0};
-    const int lo = window ? max(p + 1 - window, 0) : 0;
+    const int lo = window ? max(p + 1 - window, 0) : 0, at = j * kTilePages;
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
-        const int at = j * kTilePages + i, first = x.page(at) * kPage + 8 * hf;
-        uint32_t bits = low_bits(p + 1 - first) & (~low_bits(lo - first) | low_bits(sinks - first));
-        if (at >= x.count)
+        const int first = x.page(at + i) * kPage + 8 * hf;
+        uint32_t bits = low_bits(p + 1 - first);
+        if (window)
+            bits &= ~low_bits(lo - first) | low_bits(sinks - first);
+        if (at + i >= x.count)
             bits = 0;
         w[i / 4] |= bits << (i % 4 * 8);
     }
@@ -779,7 +799,7 @@ __device__ __noinline__ float move_reference(HalfRow h, bool move, float m, uint
     const float f = move ? ex2_approx(m - mn) : 1.f;
     // Once the product before this one is done, nothing else touches O.  (These scores came
     // after the product before that, so the wait is one phase behind at most.)
-    if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
+    if (!wait_for(o_step, (before - 1) & 1, stop))
         return m;
     tc::fence_after();
 #pragma unroll 1
@@ -867,7 +887,7 @@ struct Softmax {
         __syncwarp();
         if (lane == 0)
             tc::mbar_arrive(bar);
-        return tc::wait_warp(bar, met[all]++ & 1, &sh.stop);
+        return wait_for(bar, met[all]++ & 1, &sh.stop);
     }
 
     // Ticket of a cut item, whose partials all threads of the group have written: `last` for the group that
@@ -896,10 +916,11 @@ struct Softmax {
         return true;
     }
 
-    // First of the 4 rows of the warp's i-th token.
-    __device__ __forceinline__ size_t rows_at(const Item &x, int i) const
+    // First of the 4 rows of the warp's first token; the next token's are kTokenRow further on.
+    __device__ __forceinline__ int64_t rows_at(const Item &x) const
     {
-        return ((size_t)(x.t0 + x.token(s) + (warp & 3) * 8 + i) * kHq + x.head(s) * kGroup) * kD;
+        return x.row + (s == 0 ? 0 : x.kind == plan::kPair ? plan::kRowTokens * kTokenRow : kGroup * kD) +
+               (warp & 3) * 8 * kTokenRow;
     }
     // Of the warp's 8 tokens, those there are.
     __device__ __forceinline__ int live_tokens(const Item &x) const { return x.tokens(s) - (warp & 3) * 8; }
@@ -908,14 +929,13 @@ struct Softmax {
     __device__ __forceinline__ void fetch(const Item &x)
     {
         const int live = live_tokens(x);
+        const uint16_t *src = a.q + (live > 0 ? rows_at(x) + lane * 8 : 0);
+        const uint32_t dst = smem_addr(rows) + lane / 8 * kRowBytes + lane % 8 * 16;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t dst = smem_addr(rows + (i * kGroup + lane / 8) * kRowBytes + lane % 8 * 16);
-            const uint16_t *src = a.q + rows_at(x, i < live ? i : 0) + lane * 8;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(live > 0 ? src : a.q),
-                         "r"(i < live ? 16 : 0)
+        for (int i = 0; i < 8; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * kGroup * kRowBytes),
+                         "l"(src + (i < live ? i * kTokenRow : 0)), "r"(i < live ? 16 : 0)
                          : "memory");
-        }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
 
@@ -942,17 +962,17 @@ struct Softmax {
             tc::mbar_arrive(&sh.q_full[s]);
     }
 
-    // The warp's rows in shared memory (128 bytes each) to where `dst(i)` says the i-th token's first row begins, `step`
-    // 16-byte chunks from row to row: whole lines.
-    template <class Dst>
-    __device__ __forceinline__ void store_rows(int live, int step, const Dst &dst) const
+    // The warp's rows in shared memory (128 bytes each) to `dst`, the next token's four `token` 16-byte chunks
+    // further on and a token's `row` apart: whole lines.
+    __device__ __forceinline__ void store_rows(int live, uint4 *dst, int token, int row) const
     {
         __syncwarp();
+        dst += lane / 8 * row + lane % 8;
+        const uint8_t *src = rows + lane / 8 * kRowBytes + lane % 8 * 16;
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (i < live)
-                __stcg(dst(i) + lane / 8 * step + lane % 8,
-                       *reinterpret_cast<const uint4 *>(rows + (i * kGroup + lane / 8) * kRowBytes + lane % 8 * 16));
+                __stcg(dst + i * token, *reinterpret_cast<const uint4 *>(src + i * kGroup * kRowBytes));
         __syncwarp();
     }
 
@@ -984,11 +1004,11 @@ struct Softmax {
     {
         const int seq = loaded + x.order(s, j), st = seq % kStages;
         if (FP8)  // what this thread reads of the stage itself
-            if (!tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+            if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
                 return false;
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
-            if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
+            if (!wait_for(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
                 return false;
             tc::fence_after();
             HalfRow h = half_row(st, hf);
@@ -997,7 +1017,7 @@ struct Softmax {
             if (hf == 1) {  // (until its weights are there, the stage is this tile's)
                 bad |= *(volatile int *)&sh.bad[st];
                 const int check = checks + x.masked_loads(j) + (x.kind == plan::kHeads ? s : 0);
-                if (!FP8 && !tc::wait_warp(&sh.checked[check % kStages], (check / kStages) & 1, &sh.stop))
+                if (!FP8 && !wait_for(&sh.checked[check % kStages], (check / kStages) & 1, &sh.stop))
                     return false;
                 if (*(volatile int *)&sh.noted[st] == seq) {
                     reached(h.mask, sh.poison[st], 1, seq, nan_lo, nan_hi);
@@ -1017,9 +1037,9 @@ struct Softmax {
 #pragma unroll 1
         for (int k = 2 * j0; k < 2 * j1; ++k) {
             const int j = k >> 1, hf = k & 1, seq = loaded + x.order(s, j), st = seq % kStages;
-            if (FP8 && hf == 0 && !tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+            if (FP8 && hf == 0 && !wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
                 return false;  // (what this thread reads of the stage itself)
-            if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
+            if (!wait_for(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
                 return false;
             tc::fence_after();
             const HalfRow h = half_row(st, hf);
@@ -1072,7 +1092,7 @@ struct Softmax {
         for (int j = 0; j < nt;) {
             if (idle) {
                 for (int hf = 0; hf < 2; ++hf) {
-                    if (!tc::wait_warp(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
+                    if (!wait_for(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
                         return false;
                     if (lane == 0)
                         tc::mbar_arrive(&sh.p_full[s][hf]);
@@ -1097,7 +1117,7 @@ struct Softmax {
             queries();
             queried = feed.n + 1;
         }
-        if (!tc::wait_warp(&sh.o_full[s], used & 1, &sh.stop))
+        if (!wait_for(&sh.o_full[s], used & 1, &sh.stop))
             return false;
         tc::fence_after();
         float l;
@@ -1127,7 +1147,7 @@ struct Softmax {
                     v[k] = bad ? 0u : pack_bf16x2(__uint_as_float(o[8 * i + 2 * k]) * f, __uint_as_float(o[8 * i + 2 * k + 1]) * f);
                 own[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
-            store_rows(live, 8, [&](int i) { return reinterpret_cast<uint4 *>(a.out + rows_at(x, i)); });
+            store_rows(live, reinterpret_cast<uint4 *>(a.out + rows_at(x)), kTokenRow / 8, 8);
         } else {
             const size_t at = part_rows(x, x.me, s) + (warp & 3) * 32;
 #pragma unroll
@@ -1136,9 +1156,7 @@ struct Softmax {
                 for (int i = 0; i < 8; ++i)
                     own[i] = make_uint4(o[32 * q2 + 4 * i], o[32 * q2 + 4 * i + 1], o[32 * q2 + 4 * i + 2],
                                         o[32 * q2 + 4 * i + 3]);
-                store_rows(live, 16, [&](int i) {
-                    return reinterpret_cast<uint4 *>(a.part_o + (at + i * kGroup) * kD) + 8 * q2;
-                });
+                store_rows(live, reinterpret_cast<uint4 *>(a.part_o + at * kD) + 8 * q2, kGroup * kD / 4, kD / 4);
             }
             if (lane / kGroup < live)
                 __stcg(a.part_ml + at + lane, make_float2(bad ? INFINITY : m, l));
@@ -1211,7 +1229,8 @@ struct Softmax {
                 if (top == INFINITY)
                     v = make_uint2(0, 0);
                 if (row / kGroup < live)
-                    *reinterpret_cast<uint2 *>(a.out + rows_at(x, row / kGroup) + row % kGroup * kD + lane % 16 * 4) = v;
+                    *reinterpret_cast<uint2 *>(a.out + rows_at(x) + row / kGroup * kTokenRow + row % kGroup * kD +
+                                               lane % 16 * 4) = v;
             }
         }
     }
@@ -1242,7 +1261,7 @@ struct Softmax {
                 *(volatile int *)&sh.stop = 1;
                 return false;
             }
-            if (!tc::wait_warp(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+            if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
                 return false;
             bad |= *(volatile int *)&sh.bad[st];
             const int i = j * kTilePages + warp;
@@ -1397,21 +1416,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
         else if (warp < kIssuer + 2)
             issuer<FP8>(stages, sums, sh, tmem, warp - kIssuer);
         else if (warp == kScheduler)
-            scheduler<FP8>(a, sh);
+            pieces<FP8>(a, sh, false);
         else if (FP8)
             preparer(a, raws, stages, sums, sh);
     }
     __syncthreads();
     if (sh.stop && warp == kScheduler) {
-        // the tickets that were not drawn, so that the next call finds zeros
-        for_each_piece<FP8>(a, sh, [&](const Item &x) {
-            const int which = x.me == 0;
-            if (x.parts > 1 && (threadIdx.x & 31) == 0)
-                for (int s = 0; s < (x.kind == plan::kSingle ? 1 : 2); ++s)
-                    if (!sh.taken[which][s] && atomicAdd(&a.tickets[x.first * 2 + s], 1) == x.parts - 1)
-                        a.tickets[x.first * 2 + s] = 0;
-            return true;
-        });
+        pieces<FP8>(a, sh, true);
         if ((threadIdx.x & 31) == 0 && a.err)
             atomicOr(a.err, PKV_DEVERR_TIMEOUT);
     }
