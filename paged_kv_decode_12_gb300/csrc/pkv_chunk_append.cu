@@ -9,9 +9,12 @@
 // next to the exact one (but for about 2^-40 of it), then rounded to BF16, so that FP8 rows, whose scale
 // is their rounded maximum, come out as from 64 bits.
 //
-// A warp takes tokens one by one: 8 lanes a head, 4 pairs a lane (8-byte loads, whole sectors), four
-// heads at once, 8 rounds for the query and 2 for the keys.  A lane's 4 table entries serve all of a token's
-// heads.
+// Query rows, which nothing is derived from but their BF16 values, do with one FP32 part: within 2^-20 before
+// that rounding, cancellation or not (turn_query_row).
+//
+// A warp takes a token, or some of its rounds: 8 lanes a head, 4 pairs a lane (8-byte loads, whole sectors), four
+// heads at once, 8 rounds for the query and 2 for the keys and values.  A lane's 4 table entries serve all of its
+// rounds.
 #include <cuda_bf16.h>
 
 #include "pkv_fp8.cuh"
@@ -134,6 +137,47 @@ __device__ __forceinline__ void turn_row(float (&x1)[4], float (&x2)[4], const f
     }
 }
 
+// The same of a query row, with norm: rotation by fused multiply-adds whose first product's remainder is kept (Kahan's
+// difference of products: what cancels, cancels exactly), sum and factor in FP32.
+__device__ __forceinline__ void turn_query_row(float (&x1)[4], float (&x2)[4], const float (&w1)[4], const float (&w2)[4],
+                                               float eps, const float4 (&cs)[4])
+{
+    const auto factor = [&](float e) {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            s = fmaf(x1[i], x1[i], fmaf(x2[i], x2[i], s));
+#pragma unroll
+        for (int off = 1; off < 8; off <<= 1)
+            s += __shfl_xor_sync(kFull, s, off);
+        return rsqrtf(fmaf(s, 1.f / kD, e));
+    };
+    float f = factor(eps);
+    const bool out = !(f > 0.f);  // (the 8 lanes of a head alike) the squares left FP32's range: once more, scaled down
+    if (__any_sync(kFull, out)) {
+        if (out) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x1[i] *= 0x1p-80f;
+                x2[i] *= 0x1p-80f;
+            }
+        }
+        const float g = factor(0.f);
+        if (out)
+            f = g;
+    }
+    const auto turned = [](float a, float b, float ch, float cl, float sh, float sl) {  // a c + b s
+        const float p = __fmul_rn(b, sh), e = __fmaf_rn(b, sh, -p);
+        return __fadd_rn(__fmaf_rn(a, ch, p), __fmaf_rn(a, cl, __fmaf_rn(b, sl, e)));
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = x1[i] * w1[i], b = x2[i] * w2[i];
+        x1[i] = turned(a, -b, cs[i].x, cs[i].z, cs[i].y, cs[i].w) * f;
+        x2[i] = turned(b, a, cs[i].x, cs[i].z, cs[i].y, cs[i].w) * f;
+    }
+}
+
 __device__ __forceinline__ uint2 pack4(const float (&x)[4])
 {
     return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
@@ -152,13 +196,23 @@ __device__ __forceinline__ float row_scale8(const float (&x1)[4], const float (&
     return fp8::row_scale(m);
 }
 
-__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float scale)
+// E4M3 codes of x / scale, the quotient as FP32 division rounds it: from the rounded reciprocal, one step with
+// the remainder gives the rounded quotient (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  A scale whose reciprocal leaves the range takes the division.
+__device__ __forceinline__ uint32_t codes4(const float (&x)[4], float scale, float inv)
 {
-    uint32_t c = 0;
+    float q[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        c |= fp8::e4m3_code(__fdiv_rn(x[i], scale)) << (8 * i);
-    return c;
+    for (int i = 0; i < 4; ++i) {
+        const float y = __fmul_rn(x[i], inv);
+        q[i] = __fmaf_rn(__fmaf_rn(-y, scale, x[i]), inv, y);
+    }
+    if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            q[i] = __fdiv_rn(x[i], scale);
+    }
+    return fp8::e4m3x2_of(q[0], q[1]) | fp8::e4m3x2_of(q[2], q[3]) << 16;
 }
 
 // One token: `part` of `parts` takes the rounds part, part + parts, ... of 10 (8 of four query heads, 2 of four KV heads).
@@ -202,7 +256,10 @@ __device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int 
             float x1[4], x2[4];
             load4(src + r * 4 * kD, x1);
             load4(src + r * 4 * kD + kD / 2, x2);
-            turn_row<NORM>(x1, x2, w1, w2, a.eps, cs);
+            if constexpr (NORM)
+                turn_query_row(x1, x2, w1, w2, a.eps, cs);
+            else
+                turn_row<false>(x1, x2, w1, w2, a.eps, cs);
             *reinterpret_cast<uint2 *>(dst + r * 4 * kD) = pack4(x1);
             *reinterpret_cast<uint2 *>(dst + r * 4 * kD + kD / 2) = pack4(x2);
         }
@@ -235,13 +292,13 @@ __device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int 
                 x1[i] = fp8::bf16_round(x1[i]);
                 x2[i] = fp8::bf16_round(x2[i]);
             }
-            const float ks = row_scale8(x1, x2);
-            *reinterpret_cast<uint32_t *>(unit + slot * kD + 4 * j) = codes4(x1, ks);
-            *reinterpret_cast<uint32_t *>(unit + slot * kD + kD / 2 + 4 * j) = codes4(x2, ks);
+            const float ks = row_scale8(x1, x2), ki = __frcp_rn(ks);
+            *reinterpret_cast<uint32_t *>(unit + slot * kD + 4 * j) = codes4(x1, ks, ki);
+            *reinterpret_cast<uint32_t *>(unit + slot * kD + kD / 2 + 4 * j) = codes4(x2, ks, ki);
             float y1[4] = {bf16lo(v1.x), bf16hi(v1.x), bf16lo(v1.y), bf16hi(v1.y)};
             float y2[4] = {bf16lo(v2.x), bf16hi(v2.x), bf16lo(v2.y), bf16hi(v2.y)};
-            const float vs = row_scale8(y1, y2);
-            const uint32_t c1 = codes4(y1, vs), c2 = codes4(y2, vs);
+            const float vs = row_scale8(y1, y2), vi = __frcp_rn(vs);
+            const uint32_t c1 = codes4(y1, vs, vi), c2 = codes4(y2, vs, vi);
             uint8_t *vt = unit + fp8::kFp8Tile;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -267,10 +324,16 @@ __global__ void __launch_bounds__(kRowsWarps * 32) chunk_append_kernel(ChunkAppe
         token_rows<FP8, NORM>(a, t, w - t * parts, parts);
 }
 
+// Few tokens are shared by several warps each, so that their rounds overlap: enough of them for 32 warps an SM.
+constexpr int kEnoughWarps = 152 * 32;
+
 template <bool FP8, bool NORM>
 int launch_chunk_append(const ChunkAppendArgs &a, cudaStream_t s)
 {
-    const int parts = 1;
+    int parts = 1;
+    for (const int p : {2, 5, 10})
+        if ((int64_t)a.T * parts < kEnoughWarps)
+            parts = p;
     const int64_t warps = (int64_t)a.T * parts;
     return launch_kernel(chunk_append_kernel<FP8, NORM>, dim3((unsigned)((warps + kRowsWarps - 1) / kRowsWarps)),
                          dim3(kRowsWarps * 32), 0, s, true, a, parts);

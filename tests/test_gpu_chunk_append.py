@@ -3,7 +3,11 @@
 Every value is rounded to FP32 (2^-24 of it), then to BF16: |got - want| is at most that, half a step of
 want (2^(e - 8) for 2^e <= |want| < 2^(e + 1)) and 2^-36 of the row's largest for the arithmetic before it (two
 FP32 parts).  (Where the FP32 number lies between two BF16 values, the even one is taken: half a step
-alone would be too little.)  Values and codes have to be equal."""
+alone would be too little.)  Values and codes have to be equal.
+
+Query rows with norms have one FP32 part: their value before BF16 is off by 2^-24 for each of: the rotation's fused sum,
+its second sum, 1 / sqrt (2 units in the last place: 2 * 2^-23), half of the 11 additions of squares (8 in a row,
+then 3), the addition of eps and half of it, the product: below 16 * 2^-24 = 2^-20."""
 import numpy as np
 import pytest
 import torch
@@ -47,9 +51,9 @@ def formula(x, w, eps, pos, axes):
     return np.concatenate([z.real, z.imag], -1)
 
 
-def rounded_once(got, want, what):
+def rounded_once(got, want, what, before=2.0 ** -24):
     half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want), 2.0 ** -126))) - 8)
-    off = half + 2.0 ** -24 * np.abs(want) + 2.0 ** -36 * np.abs(want).max(-1, keepdims=True)
+    off = half + before * np.abs(want) + 2.0 ** -36 * np.abs(want).max(-1, keepdims=True)
     bad = ~(np.abs(got.double().numpy() - want) <= off)
     assert not bad.any(), (what, np.argwhere(bad)[:3].tolist(), got.double().numpy()[bad][:3], want[bad][:3])
 
@@ -97,7 +101,8 @@ class Case:
         host = self.cache.host.copy()                                          # all NaN
         if with_q:
             got = self.out.cpu()
-            rounded_once(got[n], formula(self.q[n], self.qw, self.eps, pos, self.axes), "q")
+            rounded_once(got[n], formula(self.q[n], self.qw, self.eps, pos, self.axes), "q",
+                         2.0 ** -20 if self.norm else 2.0 ** -24)
             rest = np.setdiff1d(np.arange(self.T), n)
             if padding is not None:
                 assert (got[rest] == padding).all()
@@ -205,7 +210,7 @@ def test_rows_that_are_not_finite_stay_to_themselves(rope):
         keep = [(t, h) for t in range(8) for h in range(x.shape[1]) if (t, h) not in ((2, 1), (3, 2))]
         t, h = np.array(keep).T
         want = formula(full, w, c.eps, c.pos, None)
-        rounded_once(x[t, h], want[t, h], "rows")
+        rounded_once(x[t, h], want[t, h], "rows", 2.0 ** -20)
     c.cache.close()
 
 
