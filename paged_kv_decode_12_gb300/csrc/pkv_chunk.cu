@@ -409,22 +409,32 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
     const uint64_t once_policy = l2_evict_first_policy();
     Feed feed(sh);
     int seq = 0, raw = 0;  // stages and raw units filled so far
+    int ahead = -1, first4 = 0;  // the item whose first ids are there
     bool go = true;
     for (const Item *p; go && (p = feed.look()) != nullptr; feed.let_go()) {
         const Item x = *p;
-        const int32_t *row = a.bt + (size_t)x.b * a.max_blocks;
         const bool single = x.kind == plan::kSingle, through_raw = FP8 && !single;
         const int heads = x.kind == plan::kHeads ? 2 : 1;
         const uint64_t policy = single ? once_policy : shared_policy;
         if (FP8 && single)  // the preparers are done with every stage before
             for (int i = max(raw - kRaws, 0); go && i < raw; ++i)
                 go = wait_for(&sh.raw_empty[i % kRaws], (i / kRaws) & 1, &sh.stop);
-        int id4 = 0;  // lane l: the id of page l of the current run of 4 key tiles
+        // lane l: the id of page l of the current run of 4 key tiles, and of the next run: their loads are a run ahead
+        const auto ids_of = [&](const Item &y, int j) {
+            return (a.bt + (size_t)y.b * a.max_blocks)[y.page(min(j * kTilePages + lane, y.count - 1))];
+        };
+        int id4 = 0, next4 = ahead == feed.n ? first4 : ids_of(x, x.j0);
         unsigned bad4 = 0;
         for (int j = x.j0; j < x.j1 && go; ++j) {
             const int in4 = (j - x.j0) & 3;
             if (in4 == 0) {
-                id4 = row[x.page(min(j * kTilePages + lane, x.count - 1))];
+                id4 = next4;
+                if (j + 4 < x.j1) {
+                    next4 = ids_of(x, j + 4);
+                } else if (const Item *y = feed.look(1)) {  // (of the next item: it is there long before)
+                    first4 = ids_of(*y, y->j0);
+                    ahead = feed.n + 1;
+                }
                 const bool out = id4 < 0 || id4 >= a.num_pages;
                 bad4 = __ballot_sync(kFull, out);
                 if (out)
@@ -1244,8 +1254,9 @@ struct Softmax {
         return reinterpret_cast<float *>(rows + (i - warp) * 32 * kRowBytes);
     }
 
-    __device__ __forceinline__ bool single_piece(const Item &x)
+    __device__ __forceinline__ bool single_piece(const Item &item)
     {
+        const Item x = item;
         std::conditional_t<FP8, fp8::Fp8MmaWarp, MmaWarp> w;
         const uint16_t *q = a.q + ((size_t)x.t0 * kHq + x.g * kGroup) * kD;
         if constexpr (FP8)
@@ -1255,31 +1266,49 @@ struct Softmax {
         constexpr int kUnit = FP8 ? kFp8Unit : kStageBytes;
         const int p = x.p0, lo = a.window ? max(p + 1 - a.window, 0) : 0;
         int bad = 0;
-        for (int j = x.j0; j < x.j1; ++j) {
-            const int seq = loaded + j - x.j0, st = seq % kStages;
-            if (a.expire && used == 0 && seq == 0 && blockIdx.x == 0) {
-                *(volatile int *)&sh.stop = 1;
-                return false;
-            }
-            if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
-                return false;
-            bad |= *(volatile int *)&sh.bad[st];
-            const int i = j * kTilePages + warp;
-            if (i < x.count) {
-                const uint8_t *page = stages + st * kStageSize + warp * kUnit;
-                const int first = x.page(i) * kPage;
-                const uint32_t upto = p + 1 - first >= kPage ? 0xffffu : (1u << (p + 1 - first)) - 1;
-                const uint32_t below = (1u << min(max(lo - first, 0), kPage)) - 1;
-                const uint32_t sunk = (1u << min(max(a.sinks - first, 0), kPage)) - 1;
-                const uint32_t bits = upto & (~below | sunk);
-                if (bits == 0xffffu)
-                    w.page(page, EveryToken{});
-                else if (bits)
-                    w.page(page, TokenSet{bits});
-            }
+        // The places of page `at` that are attended to.
+        const auto bits_of = [&](int at) {
+            const int first = x.page(at) * kPage;
+            const uint32_t upto = p + 1 - first >= kPage ? 0xffffu : (1u << (p + 1 - first)) - 1;
+            const uint32_t below = (1u << min(max(lo - first, 0), kPage)) - 1;
+            const uint32_t sunk = (1u << min(max(a.sinks - first, 0), kPage)) - 1;
+            return upto & (~below | sunk);
+        };
+        const auto done_with = [&](int st) {
             __syncwarp();
             if (lane == 0)
                 tc::mbar_arrive(&sh.empty[st]);
+        };
+        if (a.expire && used == 0 && loaded == 0 && blockIdx.x == 0) {
+            *(volatile int *)&sh.stop = 1;
+            return false;
+        }
+        for (int j = x.j0; j < x.j1; ++j) {
+            const int seq = loaded + j - x.j0, st = seq % kStages;
+            if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
+                return false;
+            bad |= *(volatile int *)&sh.bad[st];
+            const uint8_t *page = stages + st * kStageSize + warp * kUnit;
+            const int at = j * kTilePages + warp;
+            if constexpr (FP8) {
+                // two tiles at a time, where both are plain
+                if (j + 1 < x.j1 && !x.masked(j) && !x.masked(j + 1)) {
+                    const int next = (seq + 1) % kStages;
+                    if (!wait_for(&sh.full[next], ((seq + 1) / kStages) & 1, &sh.stop))
+                        return false;
+                    bad |= *(volatile int *)&sh.bad[next];
+                    w.two_pages(page, stages + next * kStageSize + warp * kUnit);
+                    done_with(st);
+                    done_with(next);
+                    ++j;
+                    continue;
+                }
+            }
+            if (!x.masked(j))
+                w.page(page, EveryToken{});
+            else if (const uint32_t bits = at < x.count ? bits_of(at) : 0)
+                w.page(page, TokenSet{bits});
+            done_with(st);
         }
         w.store_state(state(warp));
         if (!meet(true))

@@ -24,7 +24,7 @@ namespace {
 
 using namespace dev;
 
-constexpr int kRowsWarps = 8;
+constexpr int kRowsWarps = 4, kRowsCtas = 8;  // of an SM: 64 registers a thread
 constexpr int kMaxAxes = 3;
 
 struct ChunkAppendArgs {
@@ -314,7 +314,7 @@ __device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int 
 }
 
 template <bool FP8, bool NORM>
-__global__ void __launch_bounds__(kRowsWarps * 32) chunk_append_kernel(ChunkAppendArgs a, int parts)
+__global__ void __launch_bounds__(kRowsWarps * 32, kRowsCtas) chunk_append_kernel(ChunkAppendArgs a, int parts)
 {
     grid_dependency_wait();
     allow_dependent_launch();
