@@ -21,7 +21,8 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["pkv_host.cpp", "pkv_sched.cpp", "pkv_layers.cpp", "pkv_append.cu", "pkv_decode.cu", "pkv_step.cu",
            "pkv_fp8.cu", "pkv_probe.cu", "pkv_window.cu", "pkv_shared.cu", "pkv_scored.cu", "pkv_evict.cu",
-           "pkv_chunk_tables.cu", "pkv_chunk_append.cu", "pkv_chunk.cu"]
+           "pkv_chunk_tables.cu", "pkv_chunk_append.cu", "pkv_chunk.cu",
+           "pkv_chunk_single.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

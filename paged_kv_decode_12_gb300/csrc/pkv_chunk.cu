@@ -5,9 +5,8 @@
 // 32 tokens and the 4 query heads of a KV head are 128 rows that meet the same keys: S = Q K^T and O += P V
 // on the tensor cores (tcgen05), Q, S, P and O in tensor memory, K and V in shared memory as TMA brought the
 // pages.  A CTA has two such row tiles at a time, each with four softmax warps (a thread a row) and an issuer
-// warp, so that one's products fill the other's exponentials.  A sequence's single new token is 4 rows: its
-// pages go through warp-level products (the decode kernels' policies), a page a warp, from the same ring of
-// stages.  pkv_chunk_plan.cuh says how the work is cut into one run for every CTA.
+// warp, so that one's products fill the other's exponentials.  Where there are many sequences, those that bring
+// a single token, 4 rows a KV head, are left to a kernel of their own (pkv_chunk_single.cu).  pkv_chunk_plan.cuh says how the work is cut into one run for every CTA.
 //
 // Masks: only tiles in which some row does not attend to some token (the last ones, and a window's
 // first) are masked, by 64 bits a row and half tile.  A weight of 0 times a value that is not finite would
@@ -15,93 +14,36 @@
 // in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us where 259 were without.)
 #include <cmath>
 
-#include "pkv_chunk_plan.cuh"
+#include "pkv_chunk_run.cuh"
 #include "pkv_tiles.cuh"
 
 namespace pkv {
+namespace chunk {
 namespace {
 
-using namespace dev;
 using namespace tiles;
-using plan::Costs;
-using plan::PageList;
 
-constexpr int kMaxRows = 4096;       // sequences of a call
-constexpr int kSms = 152;
-constexpr int kStages = 4, kRaws = 2, kItems = 4;
+constexpr int kStages = 4, kRaws = 2;
 constexpr int kLoader = 8, kIssuer = 9, kScheduler = 11, kPreparer = 12;   // warps: 2 x 4 softmax, ...
 constexpr int kPreparers = 4;
-constexpr int kTeam = 8;             // warps of a single token's pages
 constexpr int kRowBytes = 128 + 16;  // a query or output row in shared memory, padded to other banks
 constexpr int kRowsSize = 2 * kRowTile * kRowBytes;
-static_assert(kStateFloats * 4 <= 32 * kRowBytes, "a warp's softmax state fits its rows");
 // What the weights are multiplied with for their sums, 16 columns of 64 places: ones; FP8: for every stage and half
 // the inverses of V's scales, as two BF16 numbers in the first two columns (the others do not matter).
 constexpr int sums_size(bool fp8) { return fp8 ? (2 * kStages + 1) * 1024 : 2048; }
 constexpr int kCols = 512;           // tensor memory, all of it
-constexpr int kTokenRow = kHq * kD;  // elements of a token's query rows
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColL = 448;  // + 128 / 64 / 32 / 16 for the second row tile
 
-constexpr int chunk_threads(bool fp8) { return fp8 ? (kPreparer + kPreparers) * 32 : kPreparer * 32; }
-constexpr int consumers(bool fp8) { return fp8 ? 8 + 3 + kPreparers : 8 + 3; }  // warps that go through the items
-
-struct ChunkArgs {
-    int num_pages;
-    const uint16_t *q;
-    const int32_t *bt;
-    int max_blocks;
-    const int32_t *lens, *starts;
-    int B, T;
-    float scale_log2;
-    int window, sinks;
-    uint16_t *out;
-    int32_t *err;
-    int *tickets;    // [CTA][row tile], zero between launches
-    float2 *part_ml; // [CTA][went on, begun][row tile][128] (m, l)
-    float *part_o;   // [CTA][went on, begun][row tile][128][64]
-    int expire;      // testing aid (PKV_STEP_TEST_EXPIRE_WAIT)
-};
-
-// A piece of work, as the scheduler hands it to the other warps.
-struct Item {
-    int kind;
-    int b, g;              // sequence, (first) KV head
-    int t0, n, p0;         // first token, tokens, position of the first
-    int sink, from, count; // its pages
-    int j0, j1, nt;        // key tiles of the piece; of the whole item
-    int first, parts, me;  // CTAs that share the item, and this one's place among them
-    int plain, plain0, plain1;  // key tiles in which every row attends to every place: below plain, and plain0 .. plain1 - 1
-    int pad;
-    int64_t row;           // first query row, in elements
-    __device__ __forceinline__ int page(int i) const { return i < sink ? i : i - sink + from; }
-    __device__ __forceinline__ int loads() const { return (j1 - j0) * (kind == plan::kHeads ? 2 : 1); }
-    // A row tile's first token within the item, its tokens, its KV head, and the place among the piece's loads of
-    // the piece's j-th key tile.
-    __device__ __forceinline__ int token(int s) const { return kind == plan::kPair ? 32 * s : 0; }
-    __device__ __forceinline__ int tokens(int s) const { return min(plan::kRowTokens, n - token(s)); }
-    __device__ __forceinline__ int order(int s, int j) const { return kind == plan::kHeads ? 2 * j + s : j; }
-    __device__ __forceinline__ bool masked(int j) const { return j >= plain && (j < plain0 || j >= plain1); }
-    // Loads of the piece before its j-th key tile's first whose tiles are masked.
-    __device__ __forceinline__ int masked_loads(int j) const
+template <bool FP8>
+struct TileRun {
+    static constexpr int kThreads = (FP8 ? kPreparer + kPreparers : kPreparer) * 32;
+    static constexpr int kConsumers = FP8 ? 8 + 3 + kPreparers : 8 + 3;
+    static constexpr bool kSingles = false;
+    static constexpr int kLeast = 64;  // of a CTA's run
+    // in eighths of the time of a BF16 key tile of two row tiles
+    static __device__ __forceinline__ Costs costs()
     {
-        const int n = masked_tiles(j0 + j) - masked_tiles(j0);
-        return kind == plan::kHeads ? 2 * n : n;
-    }
-    __device__ __forceinline__ int masked_tiles(int j) const
-    {
-        return j - min(j, plain) - (min(max(j, plain0), plain1) - plain0);
-    }
-    __device__ __forceinline__ void find_plain(int window, int sinks)
-    {
-        const int whole = (p0 + 1) / kPage;  // pages that end at or before the first token
-        plain1 = min(count, max(whole + sink - from, 0)) / kTilePages;
-        plain = plain0 = 0;
-        if (window) {
-            plain = min(sink, sinks / kPage) / kTilePages;  // entries from the first page on that the last token's window holds as a whole
-            const int entry = max(sink, sink - from + (max(p0 + n - window, 0) + kPage - 1) / kPage);
-            plain0 = (entry + kTilePages - 1) / kTilePages;
-        }
-        plain1 = max(plain1, plain0);
+        return FP8 ? Costs{{0, 14, 16, 0}, {0, 30, 30, 0}} : Costs{{0, 8, 9, 0}, {0, 24, 24, 0}};
     }
 };
 
@@ -111,314 +53,50 @@ struct Poison {
     uint32_t lo, hi;
 };
 
-struct ChunkShared {
+struct ChunkShared : RunShared {
     uint64_t full[kStages], empty[kStages];      // a stage holds its pages / has been read by all
     uint64_t raw_full[kRaws], raw_empty[kRaws];  // the same of the raw units
     uint64_t s_full[2][2], p_full[2][2];         // [row tile][half]: scores are in tensor memory / weights are
     uint64_t o_step[2];                          // one more product of weights and values is done
     uint64_t q_full[2], o_full[2];               // once an item: the queries are in / its last product is done
-    uint64_t item_full[kItems], item_empty[kItems];
     uint64_t checked[kStages];                   // (BF16) the values of a masked load have been gone through
-    uint64_t group[4];                           // row tile s's warps (2: all eight; 3: the preparers) have come so far
+    uint64_t group[3];                           // row tile s's warps (2: the preparers) have come so far
     uint64_t drained[2];
     uint32_t tmem;
-    int stop;                                    // a wait gave up
     int bad[kStages], raw_bad[kRaws];            // the tile has a bad page id
     int noted[kStages];                          // the last load into the stage with notes on values (see Poison)
-    int last[3];                                 // group: this CTA finished the item last
-    int taken[2][2];                             // [went on, begun][row tile]: the cut item's ticket is drawn
-    int64_t length;                              // of the line
-    int64_t warp_sums[16];
-    alignas(16) Item items[kItems];
+    int last[2];                                 // row tile s: this CTA finished the item last
     Poison poison[kStages][kTilePages * kPage];
-    int64_t sums[512];                           // costs of the sequences before each thread's
+    int64_t sums[(kPreparer + kPreparers) * 32];
     alignas(16) float scales[kStages][2][kTilePages * kPage];  // (FP8) row scales: K's times scale log2 e, V's
 };
 
-// tc::wait_warp, whose polling is out of the way: it is waited in many places, and code that is rarely run next to
-// what is run often costs instruction fetches.
-__device__ __forceinline__ bool wait_long(uint64_t *bar, uint32_t parity, volatile int *stop)
-{
-    return tc::wait_warp(bar, parity, stop);
-}
-
-__device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, volatile int *stop)
-{
-    return tc::try_warp(bar, parity) || wait_long(bar, parity, stop);
-}
-
-// ------------------------------------------------------------------ the plan
-
-template <bool FP8>
-__device__ __forceinline__ Costs costs()
-{
-    // in eighths of the time of a BF16 key tile of two row tiles
-    return FP8 ? Costs{{0, 14, 16, 3}, {0, 30, 30, 8}} : Costs{{0, 8, 9, 5}, {0, 24, 24, 8}};
-}
-constexpr int kLeastCost = 64;  // of a CTA's run
-
-struct Row {
-    int s0, n, L;
-    bool ok;
-};
-
-// Sequence b; not ok if its tokens or its length are out of range.
-__device__ __forceinline__ Row row_of(const ChunkArgs &a, int b)
-{
-    Row x;
-    x.s0 = a.starts[b];
-    const int s1 = a.starts[b + 1];
-    x.ok = x.s0 >= 0 && s1 >= x.s0 && s1 <= a.T;
-    x.n = x.ok ? s1 - x.s0 : 0;
-    x.L = a.lens[b];
-    return x;
-}
-
-__device__ __forceinline__ bool length_fits(const ChunkArgs &a, const Row &x)
-{
-    return x.L >= x.n && x.L <= a.max_blocks * kPage;
-}
-
-__device__ __forceinline__ int64_t row_cost(const ChunkArgs &a, const Row &x, const Costs &k)
-{
-    return x.n && length_fits(a, x) ? plan::Sequence(x.n, x.L - x.n, a.window, a.sinks, k).cost(k) : 0;
-}
-
-// All threads: the prefix sums of the sequences' costs, the rows that are refused.
-template <bool FP8>
-__device__ __forceinline__ void make_plan(const ChunkArgs &a, ChunkShared &sh)
-{
-    const Costs k = costs<FP8>();
-    const int per = (a.B + chunk_threads(FP8) - 1) / chunk_threads(FP8);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int64_t sum = 0;
-    bool bad = threadIdx.x == 0 && a.starts[0] != 0;
-    for (int i = 0; i < per; ++i) {
-        const int b = threadIdx.x * per + i;
-        if (b >= a.B)
-            break;
-        const Row x = row_of(a, b);
-        bad |= !x.ok;
-        if (x.n && !length_fits(a, x)) {  // zeros; the CTAs share the tokens
-            bad = true;
-            for (int t = blockIdx.x; t < x.n; t += gridDim.x)
-                for (int i2 = 0; i2 < kHq * kD / 8; ++i2)
-                    reinterpret_cast<uint4 *>(a.out + (size_t)(x.s0 + t) * kHq * kD)[i2] = make_uint4(0, 0, 0, 0);
-        }
-        sum += row_cost(a, x, k);
-    }
-    int64_t upto = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const int64_t y = __shfl_up_sync(kFull, upto, off);
-        if (lane >= off)
-            upto += y;
-    }
-    if (lane == 31)
-        sh.warp_sums[warp] = upto;
-    bad = __syncthreads_or(bad);
-    int64_t before = upto - sum, all = 0;
-    for (int w = 0; w < chunk_threads(FP8) / 32; ++w) {
-        if (w < warp)
-            before += sh.warp_sums[w];
-        all += sh.warp_sums[w];
-    }
-    sh.sums[threadIdx.x] = before;
-    if (threadIdx.x == 0) {
-        sh.length = all;
-        if (bad && blockIdx.x == 0 && a.err)
-            atomicOr(a.err, PKV_DEVERR_LENGTH);
-    }
-}
-
-// A piece for the other warps, `n` so far; false if a wait gave up.
-__device__ __forceinline__ bool give(ChunkShared &sh, const Item &it, int &n)
-{
-    const int at = n % kItems;
-    if (n >= kItems && !wait_for(&sh.item_empty[at], (n / kItems - 1) & 1, &sh.stop))
-        return false;
-    if ((threadIdx.x & 31) == 0) {
-        sh.items[at] = it;
-        tc::mbar_arrive(&sh.item_full[at]);
-    }
-    __syncwarp();
-    ++n;
-    return true;
-}
-
-// The pieces of this CTA's run, in order, by a whole warp, given to the others; or (`over`: something gave up) the
-// tickets of cut items that were not drawn, so that the next call finds zeros.
-template <bool FP8>
-__device__ __noinline__ void pieces(const ChunkArgs &a, ChunkShared &sh, bool over)
-{
-    int given = 0;
-    const Costs k = costs<FP8>();
-    const plan::Line line = plan::line_of(sh.length, gridDim.x, kLeastCost);
-    const int lane = threadIdx.x & 31, per = (a.B + chunk_threads(FP8) - 1) / chunk_threads(FP8);
-    const bool work = line.length > 0 && (int)blockIdx.x < line.ctas;
-    const int64_t x0 = work ? line.border(blockIdx.x) : 0, x1 = work ? line.border(blockIdx.x + 1) : 0;
-    int64_t x = x0;
-    while (x < x1) {
-        // the thread whose sequences hold x (the last whose sum is not above it), and the sequence
-        int lo = 0, hi = chunk_threads(FP8);
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (sh.sums[mid] <= x)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const int b0 = lo * per + lane;
-        const int64_t mine = lane < per && b0 < a.B ? row_cost(a, row_of(a, b0), k) : 0;
-        int64_t upto = mine;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(kFull, upto, off);
-            if (lane >= off)
-                upto += y;
-        }
-        const unsigned behind = __ballot_sync(kFull, sh.sums[lo] + upto > x);
-        if (!behind)
-            break;  // (not reached: the sums add up to the length)
-        const int at = __ffs(behind) - 1, b = lo * per + at;
-        const int64_t begin = sh.sums[lo] + __shfl_sync(kFull, upto - mine, at), end = sh.sums[lo] + __shfl_sync(kFull, upto, at);
-        const Row row = row_of(a, b);
-        const plan::Sequence seq(row.n, row.L - row.n, a.window, a.sinks, k);
-        const int64_t head = seq.head_cost(), rest = seq.rest_cost(k), single = seq.single_cost(k);
-        while (x < x1 && x < end) {
-            Item it;
-            PageList pages;
-            int64_t s;  // where the item begins
-            int64_t y = x - begin;
-            int token = 0;
-            it.b = b;
-            if (row.n == 1) {
-                it.kind = plan::kSingle;
-                it.g = plan::eighth(y, single);
-                s = begin + it.g * single;
-                it.n = 1;
-                pages = seq.single_pages();
-            } else if (y < kHkv * head) {
-                it.kind = plan::kPair;
-                it.g = plan::eighth(y, head);
-                y -= it.g * head;
-                int r = seq.pairs - 1;
-                if (y < seq.before(r)) {  // the last r that does not begin behind y, by 32 tries at a time
-                    int from = 0, to = r;
-                    while (to - from > 1) {
-                        const int step = (to - from + 31) / 32, probe = from + (lane + 1) * step;
-                        const int n = __popc(__ballot_sync(kFull, probe < to && seq.before(probe) <= y));
-                        from += n * step;
-                        to = min(to, from + step);
-                    }
-                    r = from;
-                }
-                s = begin + it.g * head + seq.before(r);
-                token = 64 * r;
-                it.n = min(64, row.n - token);
-                pages = seq.pair_pages(r);
-            } else {
-                it.kind = plan::kHeads;
-                const int h = plan::eighth(y - kHkv * head, rest);
-                it.g = 2 * h;
-                s = begin + kHkv * head + h * rest;
-                token = 64 * seq.pairs;
-                it.n = row.n - token;
-                pages = seq.rest_pages();
-            }
-            it.t0 = row.s0 + token;
-            it.p0 = row.L - row.n + token;
-            it.sink = pages.sink;
-            it.from = pages.from;
-            it.count = pages.count;
-            it.nt = pages.tiles();
-            const int tile = k.tile[it.kind], item = k.item[it.kind];
-            it.j0 = x0 <= s ? 0 : plan::cut(x0 - s, it.nt, tile, item);
-            it.j1 = plan::cut(x1 - s, it.nt, tile, item);
-            const plan::Parts parts = plan::parts_of(line, s, it.nt, tile, item);
-            it.first = parts.first;
-            it.parts = parts.count;
-            it.me = blockIdx.x - parts.first;
-            it.find_plain(a.window, a.sinks);
-            it.row = ((int64_t)it.t0 * kHq + it.g * kGroup) * kD;
-            if (it.j0 < it.j1) {
-                if (!over) {
-                    if (!give(sh, it, given))
-                        return;
-                } else if (it.parts > 1 && lane == 0) {
-                    for (int r = 0; r < (it.kind == plan::kSingle ? 1 : 2); ++r)
-                        if (!sh.taken[it.me == 0][r] && atomicAdd(&a.tickets[it.first * 2 + r], 1) == it.parts - 1)
-                            a.tickets[it.first * 2 + r] = 0;
-                }
-            }
-            x = s + (int64_t)it.nt * tile + item;
-        }
-    }
-    if (!over) {
-        Item end = {};
-        (void)give(sh, end, given);
-    }
-}
-
-// The items in order, as a warp of another role goes through them; one is held until it is let go.
-struct Feed {
-    ChunkShared &sh;
-    int n = 0;
-    __device__ __forceinline__ explicit Feed(ChunkShared &s) : sh(s) {}
-    // The item `ahead` of the current one, or null at the end (or after a wait that gave up).
-    __device__ __forceinline__ const Item *look(int ahead = 0)
-    {
-        const int at = (n + ahead) % kItems;
-        if (!wait_for(&sh.item_full[at], ((n + ahead) / kItems) & 1, &sh.stop))
-            return nullptr;
-        return sh.items[at].kind == plan::kEnd ? nullptr : &sh.items[at];
-    }
-    __device__ __forceinline__ void let_go()
-    {
-        __syncwarp();
-        if ((threadIdx.x & 31) == 0)
-            tc::mbar_arrive(&sh.item_empty[n % kItems]);
-        ++n;
-    }
-};
-
-__device__ __forceinline__ void arrive_n(uint64_t *bar, int n)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
-}
-
-// A stage is free after kTeam arrivals: those of the team's warps, or the row tiles' last products and what whoever
-// fills the stage gives in advance for the others.
-__device__ __forceinline__ int given_in_advance(int kind)
-{
-    return kind == plan::kPair ? kTeam - 2 : kTeam - 1;
-}
+// A stage is free after two arrivals: those of both row tiles' last products, or of one and one that whoever fills the
+// stage gives in advance.
+__device__ __forceinline__ bool given_in_advance(int kind) { return kind != plan::kPair; }
 
 // ------------------------------------------------------------------ loader
 
-// The pages of every piece's key tiles into the ring of stages (FP8 row tiles: of raw units).  A tile that
-// the pages do not fill repeats the last one (its places are masked); a bad page id is replaced by page 0
-// and the tile marked.
+// The pages of every piece's key tiles into the ring of stages (FP8: of raw units).  A tile that the pages do not fill
+// repeats the last one (its places are masked); a bad page id is replaced by page 0 and the tile marked.
 template <bool FP8>
 __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs &a, uint8_t *stages, uint8_t *raws,
                                        ChunkShared &sh)
 {
+    constexpr int kRing = FP8 ? kRaws : kStages, kSize = FP8 ? kRawSize : kStageSize;
+    uint64_t *full = FP8 ? sh.raw_full : sh.full, *empty = FP8 ? sh.raw_empty : sh.empty;
+    int *marks = FP8 ? sh.raw_bad : sh.bad;
+    uint8_t *ring = FP8 ? raws : stages;
     const int lane = threadIdx.x & 31;
-    uint64_t shared_policy;  // row tiles' pages are read by several CTAs: no eviction hint
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(shared_policy));
-    const uint64_t once_policy = l2_evict_first_policy();
+    uint64_t policy;  // pages are read by several CTAs: no eviction hint
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
     Feed feed(sh);
-    int seq = 0, raw = 0;  // stages and raw units filled so far
+    int seq = 0;                 // key tiles loaded so far
     int ahead = -1, first4 = 0;  // the item whose first ids are there
     bool go = true;
     for (const Item *p; go && (p = feed.look()) != nullptr; feed.let_go()) {
         const Item x = *p;
-        const bool single = x.kind == plan::kSingle, through_raw = FP8 && !single;
         const int heads = x.kind == plan::kHeads ? 2 : 1;
-        const uint64_t policy = single ? once_policy : shared_policy;
-        if (FP8 && single)  // the preparers are done with every stage before
-            for (int i = max(raw - kRaws, 0); go && i < raw; ++i)
-                go = wait_for(&sh.raw_empty[i % kRaws], (i / kRaws) & 1, &sh.stop);
         // lane l: the id of page l of the current run of 4 key tiles, and of the next run: their loads are a run ahead
         const auto ids_of = [&](const Item &y, int j) {
             return (a.bt + (size_t)y.b * a.max_blocks)[y.page(min(j * kTilePages + lane, y.count - 1))];
@@ -442,48 +120,34 @@ __device__ __forceinline__ void loader(const CUtensorMap *tmap, const ChunkArgs 
             }
             const int id = __shfl_sync(kFull, id4, in4 * kTilePages + lane % kTilePages);
             const int bad = (bad4 >> (in4 * kTilePages)) & ((1u << kTilePages) - 1);
-            for (int h = 0; h < heads && go; ++h) {
-                const int st = through_raw ? raw % kRaws : seq % kStages;
-                uint64_t *full = through_raw ? &sh.raw_full[st] : &sh.full[st];
-                if (through_raw) {
-                    if (raw >= kRaws && !wait_for(&sh.raw_empty[st], (raw / kRaws - 1) & 1, &sh.stop)) {
-                        go = false;
-                        break;
-                    }
-                } else if (seq >= kStages && !wait_for(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)) {
+            for (int h = 0; h < heads; ++h) {
+                const int st = seq % kRing;
+                if (seq >= kRing && !wait_for(&empty[st], (seq / kRing - 1) & 1, &sh.stop)) {
                     go = false;
                     break;
                 }
-                fence_proxy_async_smem();  // (the place's readers and writers so far were threads)
-                const int size = FP8 ? kRawSize : kStageSize;
-                uint8_t *dst = through_raw ? raws + st * kRawSize : stages + st * kStageSize;
+                fence_proxy_async_smem();  // (the place's readers and writers so far may be threads)
+                uint8_t *dst = ring + st * kSize;
                 if (lane == 0) {
-                    (through_raw ? sh.raw_bad : sh.bad)[st] = bad;
-                    if (!through_raw && !single)
-                        arrive_n(&sh.empty[st], given_in_advance(x.kind));
-                    if (FP8 && single)
-                        arrive_n(full, kPreparers - 1);
-                    mbar_arrive_expect_tx(full, size);
+                    marks[st] = bad;
+                    if (!FP8 && given_in_advance(x.kind))
+                        tc::mbar_arrive(&empty[st]);
+                    mbar_arrive_expect_tx(&full[st], kSize);
                 }
                 __syncwarp();
                 if (lane < kTilePages) {
                     if (FP8)
-                        fp8::tma_load_unit(dst + lane * kFp8Unit, tmap, full, x.g + h, id, policy);
+                        fp8::tma_load_unit(dst + lane * kFp8Unit, tmap, &full[st], x.g + h, id, policy);
                     else
-                        tma_load_page_head(dst + lane * kStageBytes, tmap, full, x.g + h, id, policy);
+                        tma_load_page_head(dst + lane * kStageBytes, tmap, &full[st], x.g + h, id, policy);
                 }
-                if (through_raw)
-                    ++raw;
                 ++seq;
             }
         }
     }
-    if (*(volatile int *)&sh.stop) {  // let the copies in flight land (bounded)
-        for (int i = max(raw - kRaws, 0); i < raw; ++i)
-            (void)mbar_wait_warp(&sh.raw_full[i % kRaws], (i / kRaws) & 1);
-        for (int i = max(seq - kStages, 0); i < seq; ++i)  // (stages that nobody filled run out of polls)
-            (void)mbar_wait_warp(&sh.full[i % kStages], (i / kStages) & 1, FP8 ? 1u << 16 : kWaitLimit);
-    }
+    if (*(volatile int *)&sh.stop)  // let the copies in flight land (bounded)
+        for (int i = max(seq - kRing, 0); i < seq; ++i)
+            (void)mbar_wait_warp(&full[i % kRing], (i / kRing) & 1);
 }
 
 // ------------------------------------------------------------------ values of masked tiles
@@ -529,17 +193,13 @@ __device__ __forceinline__ void preparer(const ChunkArgs &a, const uint8_t *raws
 {
     const int t = threadIdx.x - kPreparer * 32, lane = threadIdx.x & 31;
     Feed feed(sh);
-    int seq = 0, raw = 0, checks = 0;
+    int seq = 0, checks = 0;
     for (const Item *p; (p = feed.look()) != nullptr; feed.let_go()) {
         const Item x = *p;
         const int n = x.loads();
-        if (x.kind == plan::kSingle) {
-            seq += n;
-            continue;
-        }
-        for (int i = 0; i < n; ++i, ++seq, ++raw) {
-            const int j = x.j0 + (x.kind == plan::kHeads ? i / 2 : i), rs = raw % kRaws, st = seq % kStages;
-            if (!wait_for(&sh.raw_full[rs], (raw / kRaws) & 1, &sh.stop) ||
+        for (int i = 0; i < n; ++i, ++seq) {
+            const int j = x.j0 + (x.kind == plan::kHeads ? i / 2 : i), rs = seq % kRaws, st = seq % kStages;
+            if (!wait_for(&sh.raw_full[rs], (seq / kRaws) & 1, &sh.stop) ||
                 (seq >= kStages && !wait_for(&sh.empty[st], (seq / kStages - 1) & 1, &sh.stop)))
                 return;
             const uint8_t *raw_tile = raws + rs * kRawSize;
@@ -562,13 +222,14 @@ __device__ __forceinline__ void preparer(const ChunkArgs &a, const uint8_t *raws
             }
             if (t == 0) {
                 sh.bad[st] = sh.raw_bad[rs];
-                arrive_n(&sh.empty[st], given_in_advance(x.kind));
+                if (given_in_advance(x.kind))
+                    tc::mbar_arrive(&sh.empty[st]);
             }
             if (x.masked(j)) {  // (rows that other warps have written)
                 __syncwarp();
                 if (lane == 0)
-                    tc::mbar_arrive(&sh.group[3]);
-                if (!wait_for(&sh.group[3], checks++ & 1, &sh.stop))
+                    tc::mbar_arrive(&sh.group[2]);
+                if (!wait_for(&sh.group[2], checks++ & 1, &sh.stop))
                     return;
                 check_values<kPreparers * 32>(x, j, stage, sh.poison[st], &sh.noted[st], seq, t);
             }
@@ -595,64 +256,62 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, Chu
     int loaded = 0, checks = 0, done = 0, used = 0;
     for (const Item *p; (p = feed.look()) != nullptr; feed.let_go()) {
         const Item x = *p;
-        if (x.kind != plan::kSingle) {
-            const int nt = x.j1 - x.j0;
-            const auto scores = [&](int j, int h) {
-                const int seq = loaded + x.order(s, j), st = seq % kStages;
-                if (h == 0) {
-                    if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
-                        return false;
-                    tc::fence_after();
-                }
-                issue_scores(base + st * kStageSize + h * 1024, ts + h * kHalf, tq, &sh.s_full[s][h]);
-                return true;
-            };
-            const auto output = [&](int j, int h) {
-                const int seq = loaded + x.order(s, j), st = seq % kStages;
-                if (!FP8 && h == 0 && x.masked(x.j0 + j)) {
-                    // (a pair's values, which both row tiles read, by the first one's issuer)
-                    const int check = checks + x.masked_loads(j) + (x.kind == plan::kHeads ? s : 0);
-                    uint64_t *checked = &sh.checked[check % kStages];
-                    if (x.kind == plan::kHeads || s == 0) {
-                        check_values<32>(x, x.j0 + j, stages + st * kStageSize, sh.poison[st], &sh.noted[st], seq,
-                                         threadIdx.x & 31);
-                        __syncwarp();
-                        if ((threadIdx.x & 31) == 0)
-                            tc::mbar_arrive(checked);
-                    }
-                    if (!wait_for(checked, (check / kStages) & 1, &sh.stop))
-                        return false;
-                }
-                if (!wait_for(&sh.p_full[s][h], (done + j) & 1, &sh.stop))
+        const int nt = x.j1 - x.j0;
+        const auto scores = [&](int j, int h) {
+            const int seq = loaded + x.order(s, j), st = seq % kStages;
+            if (h == 0) {
+                if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
                     return false;
                 tc::fence_after();
-                const uint32_t v = base + st * kStageSize + kTileBytes + h * 1024, pw = ts + h * kHalf;
-                uint64_t *empty = h == 1 ? &sh.empty[st] : nullptr;
-                uint64_t *last = h == 1 && j + 1 == nt ? &sh.o_full[s] : nullptr;
-                const uint32_t sum = sum0 + (FP8 ? (st * 2 + h) * 1024 : 0);
-                if (j == 0 && h == 0)
-                    issue_output<true, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
-                else
-                    issue_output<false, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
-                return true;
-            };
-            bool go = wait_for(&sh.q_full[s], used & 1, &sh.stop);
+            }
+            issue_scores(base + st * kStageSize + h * 1024, ts + h * kHalf, tq, &sh.s_full[s][h]);
+            return true;
+        };
+        const auto output = [&](int j, int h) {
+            const int seq = loaded + x.order(s, j), st = seq % kStages;
+            if (!FP8 && h == 0 && x.masked(x.j0 + j)) {
+                // (a pair's values, which both row tiles read, by the first one's issuer)
+                const int check = checks + x.masked_loads(j) + (x.kind == plan::kHeads ? s : 0);
+                uint64_t *checked = &sh.checked[check % kStages];
+                if (x.kind == plan::kHeads || s == 0) {
+                    check_values<32>(x, x.j0 + j, stages + st * kStageSize, sh.poison[st], &sh.noted[st], seq,
+                                     threadIdx.x & 31);
+                    __syncwarp();
+                    if ((threadIdx.x & 31) == 0)
+                        tc::mbar_arrive(checked);
+                }
+                if (!wait_for(checked, (check / kStages) & 1, &sh.stop))
+                    return false;
+            }
+            if (!wait_for(&sh.p_full[s][h], (done + j) & 1, &sh.stop))
+                return false;
             tc::fence_after();
-            go = go && scores(0, 0) && scores(0, 1);
-            for (int j = 0; j < nt && go; ++j)
+            const uint32_t v = base + st * kStageSize + kTileBytes + h * 1024, pw = ts + h * kHalf;
+            uint64_t *empty = h == 1 ? &sh.empty[st] : nullptr;
+            uint64_t *last = h == 1 && j + 1 == nt ? &sh.o_full[s] : nullptr;
+            const uint32_t sum = sum0 + (FP8 ? (st * 2 + h) * 1024 : 0);
+            if (j == 0 && h == 0)
+                issue_output<true, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
+            else
+                issue_output<false, true, FP8 ? 2 : 0>(v, to, pw, sum, tl, empty, 1, &sh.o_step[s], last);
+            return true;
+        };
+        bool go = wait_for(&sh.q_full[s], used & 1, &sh.stop);
+        tc::fence_after();
+        go = go && scores(0, 0) && scores(0, 1);
+        for (int j = 0; j < nt && go; ++j)
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (go) {
-                        go = output(j, h);
-                        if (go && j + 1 < nt)
-                            go = scores(j + 1, h);
-                    }
-            if (!go)
-                break;
-            ++used;
-            done += nt;
-            checks += x.masked_loads(nt);
-        }
+            for (int h = 0; h < 2; ++h)
+                if (go) {
+                    go = output(j, h);
+                    if (go && j + 1 < nt)
+                        go = scores(j + 1, h);
+                }
+        if (!go)
+            break;
+        ++used;
+        done += nt;
+        checks += x.masked_loads(nt);
         loaded += x.loads();
     }
     if (*(volatile int *)&sh.stop) {  // let the products in flight end (bounded)
@@ -863,7 +522,6 @@ __device__ __forceinline__ size_t part_rows(const Item &x, int i, int s)
     return ((size_t)((x.first + i) * 2 + (i == 0 ? 1 : 0)) * 2 + s) * kRowTile;
 }
 
-__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 // Softmax warps of row tile s: thread = query row (token r / 4 of the tile, head r % 4).
 template <bool FP8>
@@ -875,7 +533,7 @@ struct Softmax {
     uint32_t ts, to, tq, tl;
     int loaded = 0, checks = 0, done = 0, used = 0;
     int fetched = -1, queried = -1;  // the item whose queries are in shared memory (or on their way), in tensor memory
-    int met[2] = {0, 0};   // times the row tile's warps, and all eight, have met
+    int met = 0;                     // times the row tile's warps have met
 
     __device__ __forceinline__ Softmax(const ChunkArgs &a_, ChunkShared &sh_, uint8_t *stages_, uint8_t *rows_, uint32_t tmem)
         : a(a_), sh(sh_), stages(stages_), rows(rows_ + (threadIdx.x >> 5) * 32 * kRowBytes), warp(threadIdx.x >> 5),
@@ -890,37 +548,34 @@ struct Softmax {
         tl = at + kColL + s * 16;
     }
 
-    // The warps of the row tile (all: of both) wait for each other; false if that gave up.
-    __device__ __forceinline__ bool meet(bool all)
+    // The warps of the row tile wait for each other; false if that gave up.
+    __device__ __forceinline__ bool meet()
     {
-        uint64_t *bar = &sh.group[all ? 2 : s];
         __syncwarp();
         if (lane == 0)
-            tc::mbar_arrive(bar);
-        return wait_for(bar, met[all]++ & 1, &sh.stop);
+            tc::mbar_arrive(&sh.group[s]);
+        return wait_for(&sh.group[s], met++ & 1, &sh.stop);
     }
 
-    // Ticket of a cut item, whose partials all threads of the group have written: `last` for the group that
-    // finishes last and has everybody's partials to read.
-    __device__ __forceinline__ bool draw_ticket(const Item &x, bool all, bool &last)
+    // Ticket of a cut item, whose partials the row tile's threads have written: `last` for the one that
+    // finishes last and has everybody's partials to read.  False if a wait gave up.
+    __device__ __forceinline__ bool draw_ticket(const Item &x, bool &last)
     {
-        const int row_tile = all ? 0 : s;
         __threadfence();
-        if (!meet(all))
+        if (!meet())
             return false;
-        int *flag = &sh.last[all ? 2 : s];
-        if ((int)threadIdx.x == row_tile * 128) {
-            int *ticket = &a.tickets[x.first * 2 + row_tile];
+        if ((int)threadIdx.x == s * 128) {
+            int *ticket = &a.tickets[x.first * 2 + s];
             int drawn;
             asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(drawn) : "l"(ticket) : "memory");
-            sh.taken[x.me == 0][row_tile] = 1;
-            *flag = drawn == x.parts - 1;
+            sh.taken[x.me == 0][s] = 1;
+            sh.last[s] = drawn == x.parts - 1;
             if (drawn == x.parts - 1)
                 *ticket = 0;
         }
-        if (!meet(all))
+        if (!meet())
             return false;
-        last = *(volatile int *)flag != 0;
+        last = *(volatile int *)&sh.last[s] != 0;
         if (last)
             __threadfence();
         return true;
@@ -1084,7 +739,7 @@ struct Softmax {
                 fetch(x);
             queries();
             const Item *y = feed.look(1);
-            if (y && y->kind != plan::kSingle) {
+            if (y) {
                 fetch(*y);
                 fetched = feed.n + 1;
             }
@@ -1121,7 +776,7 @@ struct Softmax {
         }
         // the next item's first scores are made while this one's last product and its output end
         const Item *y = feed.look(1);
-        if (y && y->kind != plan::kSingle) {
+        if (y) {
             if (fetched != feed.n + 1)
                 fetch(*y);
             queries();
@@ -1171,14 +826,14 @@ struct Softmax {
             if (lane / kGroup < live)
                 __stcg(a.part_ml + at + lane, make_float2(bad ? INFINITY : m, l));
             bool last;
-            if (!draw_ticket(x, false, last))
+            if (!draw_ticket(x, last))
                 return false;
             if (last)
                 join(x, live);
         }
         if (queried == feed.n + 1) {
             const Item *z = feed.look(2);
-            if (z && z->kind != plan::kSingle) {
+            if (z) {
                 fetch(*z);
                 fetched = feed.n + 2;
             }
@@ -1245,126 +900,11 @@ struct Softmax {
         }
     }
 
-    // ---- a single token: the 8 warps take a page each of every key tile
-
-    // Warp i's softmax state, in its rows (no queries are on their way there: those of an item are fetched
-    // when the one before it, of row tiles too, begins or ends).
-    __device__ __forceinline__ float *state(int i) const
-    {
-        return reinterpret_cast<float *>(rows + (i - warp) * 32 * kRowBytes);
-    }
-
-    __device__ __forceinline__ bool single_piece(const Item &item)
-    {
-        const Item x = item;
-        std::conditional_t<FP8, fp8::Fp8MmaWarp, MmaWarp> w;
-        const uint16_t *q = a.q + ((size_t)x.t0 * kHq + x.g * kGroup) * kD;
-        if constexpr (FP8)
-            w.init(q, a.scale_log2, lane);
-        else
-            w.init(q, a.scale_log2, lane, nullptr);
-        constexpr int kUnit = FP8 ? kFp8Unit : kStageBytes;
-        const int p = x.p0, lo = a.window ? max(p + 1 - a.window, 0) : 0;
-        int bad = 0;
-        // The places of page `at` that are attended to.
-        const auto bits_of = [&](int at) {
-            const int first = x.page(at) * kPage;
-            const uint32_t upto = p + 1 - first >= kPage ? 0xffffu : (1u << (p + 1 - first)) - 1;
-            const uint32_t below = (1u << min(max(lo - first, 0), kPage)) - 1;
-            const uint32_t sunk = (1u << min(max(a.sinks - first, 0), kPage)) - 1;
-            return upto & (~below | sunk);
-        };
-        const auto done_with = [&](int st) {
-            __syncwarp();
-            if (lane == 0)
-                tc::mbar_arrive(&sh.empty[st]);
-        };
-        if (a.expire && used == 0 && loaded == 0 && blockIdx.x == 0) {
-            *(volatile int *)&sh.stop = 1;
-            return false;
-        }
-        for (int j = x.j0; j < x.j1; ++j) {
-            const int seq = loaded + j - x.j0, st = seq % kStages;
-            if (!wait_for(&sh.full[st], (seq / kStages) & 1, &sh.stop))
-                return false;
-            bad |= *(volatile int *)&sh.bad[st];
-            const uint8_t *page = stages + st * kStageSize + warp * kUnit;
-            const int at = j * kTilePages + warp;
-            if constexpr (FP8) {
-                // two tiles at a time, where both are plain
-                if (j + 1 < x.j1 && !x.masked(j) && !x.masked(j + 1)) {
-                    const int next = (seq + 1) % kStages;
-                    if (!wait_for(&sh.full[next], ((seq + 1) / kStages) & 1, &sh.stop))
-                        return false;
-                    bad |= *(volatile int *)&sh.bad[next];
-                    w.two_pages(page, stages + next * kStageSize + warp * kUnit);
-                    done_with(st);
-                    done_with(next);
-                    ++j;
-                    continue;
-                }
-            }
-            if (!x.masked(j))
-                w.page(page, EveryToken{});
-            else if (const uint32_t bits = at < x.count ? bits_of(at) : 0)
-                w.page(page, TokenSet{bits});
-            done_with(st);
-        }
-        w.store_state(state(warp));
-        if (!meet(true))
-            return false;
-        const int hl = threadIdx.x >> 6, d = threadIdx.x & 63;
-        float M = -INFINITY, l = 0.f, o = 0.f;
-#pragma unroll
-        for (int i = 0; i < kTeam; ++i)
-            M = fmaxf(M, state(i)[hl]);
-#pragma unroll
-        for (int i = 0; i < kTeam; ++i) {
-            const float mi = state(i)[hl], f = mi == -INFINITY ? 0.f : ex2_approx(mi - M);
-            l = fmaf(f, state(i)[4 + hl], l);
-            o = fmaf(f, state(i)[8 + hl * kD + d], o);
-        }
-        if (!meet(true))  // the states may be written again
-            return false;
-        if (bad && threadIdx.x == 0 && a.err)
-            atomicOr(a.err, PKV_DEVERR_PAGE_RANGE);
-        bool write = x.parts == 1;
-        if (!write) {
-            const size_t at = part_rows(x, x.me, 0) + hl;
-            __stcg(a.part_o + at * kD + d, o);
-            if (d == 0)
-                __stcg(a.part_ml + at, make_float2(bad ? INFINITY : M, l));
-            if (!draw_ticket(x, true, write))
-                return false;
-            if (write) {
-                M = -INFINITY;
-                for (int i = 0; i < x.parts; ++i)
-                    M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, i, 0) + hl).x);
-                bad = M == INFINITY;
-                l = o = 0.f;
-#pragma unroll 4
-                for (int i = 0; i < x.parts; ++i) {
-                    const size_t from = part_rows(x, i, 0) + hl;
-                    const float2 ml = __ldcg(a.part_ml + from);
-                    const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-                    l = fmaf(f, ml.y, l);
-                    o = fmaf(f, __ldcg(a.part_o + from * kD + d), o);
-                }
-            }
-        }
-        if (write) {
-            const __nv_bfloat16 v = __float2bfloat16_rn(bad ? 0.f : o * inverse_sum(l));
-            a.out[((size_t)x.t0 * kHq + x.g * kGroup + hl) * kD + d] = *reinterpret_cast<const uint16_t *>(&v);
-        }
-        loaded += x.j1 - x.j0;
-        return true;
-    }
-
     __device__ __forceinline__ void run()
     {
         Feed feed(sh);
         for (const Item *x; (x = feed.look()) != nullptr; feed.let_go())
-            if (!(x->kind == plan::kSingle ? single_piece(*x) : tiles_piece(feed, *x)))
+            if (!tiles_piece(feed, *x))
                 break;
         asm volatile("cp.async.wait_all;" ::: "memory");
     }
@@ -1373,8 +913,8 @@ struct Softmax {
 // ------------------------------------------------------------------ the kernel
 
 template <bool FP8>
-__global__ void __launch_bounds__(chunk_threads(FP8), 1)
-chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
+__global__ void __launch_bounds__(TileRun<FP8>::kThreads, 1)
+chunk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ ChunkArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
     // (an offset, not a rounded address: the compiler keeps shared-memory instructions)
@@ -1386,7 +926,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
     if (threadIdx.x == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&sh.full[i], FP8 ? kPreparers : 1);
-            mbar_init(&sh.empty[i], kTeam);
+            mbar_init(&sh.empty[i], 2);
             mbar_init(&sh.checked[i], 1);
             sh.noted[i] = -1;
         }
@@ -1405,11 +945,10 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
             mbar_init(&sh.drained[s], 1);
             mbar_init(&sh.group[s], 4);
         }
-        mbar_init(&sh.group[2], kTeam);
-        mbar_init(&sh.group[3], kPreparers);
+        mbar_init(&sh.group[2], kPreparers);
         for (int i = 0; i < kItems; ++i) {
             mbar_init(&sh.item_full[i], 1);
-            mbar_init(&sh.item_empty[i], consumers(FP8));
+            mbar_init(&sh.item_empty[i], TileRun<FP8>::kConsumers);
         }
         sh.stop = 0;
         sh.taken[0][0] = sh.taken[0][1] = sh.taken[1][0] = sh.taken[1][1] = 0;
@@ -1417,16 +956,16 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
     }
     if (warp == kIssuer)
         tc::alloc<kCols>(&sh.tmem);
-    for (int i = threadIdx.x; i < kStages * kTilePages * kPage; i += chunk_threads(FP8))
+    for (int i = threadIdx.x; i < kStages * kTilePages * kPage; i += TileRun<FP8>::kThreads)
         (&sh.poison[0][0])[i].load = -1;
     if (!FP8) {
-        for (int i = threadIdx.x; i < sums_size(FP8) / 4; i += chunk_threads(FP8))
+        for (int i = threadIdx.x; i < sums_size(FP8) / 4; i += TileRun<FP8>::kThreads)
             reinterpret_cast<uint32_t *>(sums)[i] = 0x3f803f80u;
         fence_proxy_async_smem();
     }
     grid_dependency_wait();
     allow_dependent_launch();
-    make_plan<FP8>(a, sh);
+    make_plan<TileRun<FP8>>(a, sh);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -1445,13 +984,13 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
         else if (warp < kIssuer + 2)
             issuer<FP8>(stages, sums, sh, tmem, warp - kIssuer);
         else if (warp == kScheduler)
-            pieces<FP8>(a, sh, false);
+            pieces<TileRun<FP8>>(a, sh, false);
         else if (FP8)
             preparer(a, raws, stages, sums, sh);
     }
     __syncthreads();
     if (sh.stop && warp == kScheduler) {
-        pieces<FP8>(a, sh, true);
+        pieces<TileRun<FP8>>(a, sh, true);
         if ((threadIdx.x & 31) == 0 && a.err)
             atomicOr(a.err, PKV_DEVERR_TIMEOUT);
     }
@@ -1459,9 +998,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, ChunkArgs a)
         tc::dealloc<kCols>(tmem);
 }
 
+// Workspace: the tile kernel's tickets and partials, then the single tokens'.
 struct ChunkWorkspace {
     size_t tickets, ml, o;
-    size_t total() const { return tickets + ml + o; }
+    size_t singles() const { return tickets + ml + o; }
+    size_t total() const { return singles() + single_workspace().total(); }
 };
 
 ChunkWorkspace chunk_workspace()
@@ -1472,6 +1013,9 @@ ChunkWorkspace chunk_workspace()
     w.o = (size_t)kSms * 4 * kRowTile * kD * sizeof(float);
     return w;
 }
+
+// Sequences from which on those with a single token are a kernel's of their own.
+constexpr int kApart = 16;
 
 template <bool FP8>
 int launch_chunk(const pkv_pool *pool, const ChunkArgs &a, cudaStream_t s, bool pdl)
@@ -1485,17 +1029,16 @@ int launch_chunk(const pkv_pool *pool, const ChunkArgs &a, cudaStream_t s, bool 
     static PerDeviceOnce attr;
     if (const int st = ensure_smem_attr(attr, chunk_kernel<FP8>, smem); st != PKV_OK)
         return st;
-    return launch_kernel(chunk_kernel<FP8>, dim3(kSms), dim3(chunk_threads(FP8)), smem, s, pdl, *tmap, a);
+    return launch_kernel(chunk_kernel<FP8>, dim3(kSms), dim3(TileRun<FP8>::kThreads), smem, s, pdl, *tmap, a);
 }
 
-bool chunk_args_ok(int B, int T) { return B >= 1 && B <= kMaxRows && T >= 1 && T <= INT32_MAX / 16; }
-
 }  // namespace
+}  // namespace chunk
 }  // namespace pkv
 
 extern "C" size_t pkv_chunk_attention_workspace_bytes(int B, int T)
 {
-    return pkv::chunk_args_ok(B, T) ? pkv::chunk_workspace().total() : 0;
+    return pkv::chunk::chunk_args_ok(B, T) ? pkv::chunk::chunk_workspace().total() : 0;
 }
 
 extern "C" int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
@@ -1504,6 +1047,7 @@ extern "C" int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, cons
                                    int32_t *dev_err_flag, void *cuda_stream, int options)
 {
     using namespace pkv;
+    using namespace pkv::chunk;
     if (!pool || !q || !bt_dev || !seq_lens_dev || !starts_dev || !workspace || !out || !chunk_args_ok(B, T))
         return PKV_ERR_INVALID_ARG;
     if (max_blocks < 1 || max_blocks > (1 << 20) || window < 0 || sinks < 0 || (sinks && !window))
@@ -1534,7 +1078,17 @@ extern "C" int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, cons
     a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + ws.tickets);
     a.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.tickets + ws.ml);
     a.expire = (options & PKV_STEP_TEST_EXPIRE_WAIT) ? 1 : 0;
+    a.apart = false;
+    a.refuses = true;
     cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
     const bool pdl = !(options & PKV_STEP_NO_PDL);
-    return pool->kv_format == PKV_KV_FP8 ? launch_chunk<true>(pool, a, s, pdl) : launch_chunk<false>(pool, a, s, pdl);
+    void *singles = static_cast<char *>(workspace) + ws.singles();
+    if (T == 1)
+        return launch_singles(pool, a, singles, s, pdl, false);
+    a.apart = B >= kApart;
+    a.refuses = true;
+    if (const int st = pool->kv_format == PKV_KV_FP8 ? launch_chunk<true>(pool, a, s, pdl) : launch_chunk<false>(pool, a, s, pdl);
+        st != PKV_OK || !a.apart)
+        return st;
+    return launch_singles(pool, a, singles, s, pdl, true);
 }

@@ -2,9 +2,8 @@
 // Not part of the ABI.
 //
 // A sequence's new tokens make items: 64 tokens and one KV head (two row tiles of 128 query rows that go
-// through the same pages); the odd last 32 tokens, or fewer, and two KV heads (a row tile each); a
-// single token and one KV head (kind kSingle, warp-level products: its 4 rows would leave a row tile
-// all but empty).  An item goes through `nt` key tiles of 128 tokens and costs nt * tile + item.  All items laid
+// through the same pages); the odd last 32 tokens, or fewer, and two KV heads (a row tile each); or, in a kernel
+// of their own, a sequence's single token and one KV head.  An item goes through `nt` key tiles of 128 tokens and costs nt * tile + item.  All items laid
 // end to end make a line of length W, and CTA c of G works off what lies between c W / G and (c + 1) W / G: the
 // work is even whatever the lengths are, and an item that crosses a border is cut between
 // key tiles (not next to its ends: cut()), its parts joined by whoever finishes last.  At most one cut item begins and
@@ -79,7 +78,7 @@ struct Sequence {
     PKV_HD Sequence(int n_, int c_, int window_, int sinks_, const Costs &k)
         : n(n_), c(c_), window(window_), sinks(sinks_), tile(k.tile[kPair]), item(k.item[kPair])
     {
-        const int rows = n == 1 ? 0 : (n + kRowTokens - 1) / kRowTokens;
+        const int rows = (n + kRowTokens - 1) / kRowTokens;
         pairs = rows / 2;
         rest = (rows & 1) != 0;
         flat = 1 << 30;
@@ -118,13 +117,10 @@ struct Sequence {
     {
         return rest ? (int64_t)rest_pages().tiles() * k.tile[kHeads] + k.item[kHeads] : 0;
     }
+    PKV_HD int64_t cost(const Costs &k) const { return kHkv * head_cost() + kHkv / 2 * rest_cost(k); }
     PKV_HD int64_t single_cost(const Costs &k) const
     {
-        return n == 1 ? (int64_t)single_pages().tiles() * k.tile[kSingle] + k.item[kSingle] : 0;
-    }
-    PKV_HD int64_t cost(const Costs &k) const
-    {
-        return kHkv * (head_cost() + single_cost(k)) + kHkv / 2 * rest_cost(k);
+        return (int64_t)single_pages().tiles() * k.tile[kSingle] + k.item[kSingle];
     }
 };
 

@@ -374,114 +374,6 @@ struct Fp8MmaWarpOf {
             mma_f16(o[i], a[i], b0, b1);
     }
 
-    // Two pages that are attended to as a whole, as one of 32 tokens: their chains of instructions fill each other's
-    // waits, and the reference, the scale reference and the rescale are looked at once.
-    __device__ __forceinline__ void two_pages(const uint8_t *unit0, const uint8_t *unit1)
-    {
-        static_assert(!FINE, "scores that are kept come page by page");
-        const int gid = lane >> 2, tig = lane & 3;
-        const uint8_t *unit[2] = {unit0, unit1};
-        float s[2][4] = {};
-        {
-            uint4 ka[2], kb[2];
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                ka[u] = *reinterpret_cast<const uint4 *>(unit[u] + gid * kD + 16 * tig);
-                kb[u] = *reinterpret_cast<const uint4 *>(unit[u] + (gid + 8) * kD + 16 * tig);
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    mma_e4m3(s[u], ka[u].x, kb[u].x, ka[u].y, kb[u].y, qt[t][0], qt[t][1]);
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    mma_e4m3(s[u], ka[u].z, kb[u].z, ka[u].w, kb[u].w, qt[t][2], qt[t][3]);
-            }
-        }
-        float x[2][4], z[2][4], sv[2][2];
-        float mz = -INFINITY;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const float *scales = reinterpret_cast<const float *>(unit[u] + kFp8UnitCodes);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float f = scales[gid + (i >> 1) * 8] * hf[i & 1];
-                x[u][i] = s[u][i] * f;
-                z[u][i] = fmaf(s[u][i], f, -m[i & 1]);
-                mz = fmaxf(mz, z[u][i]);
-            }
-            sv[u][0] = scales[kPage + gid];
-            sv[u][1] = scales[kPage + gid + 8];
-        }
-        float al[2] = {1.f, 1.f};
-        if (__any_sync(kFull, mz > kDeferLog2)) {
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float pm = fmaxf(fmaxf(x[0][e], x[0][2 + e]), fmaxf(x[1][e], x[1][2 + e]));
-#pragma unroll
-                for (int off = 4; off <= 16; off <<= 1)
-                    pm = fmaxf(pm, __shfl_xor_sync(kFull, pm, off));
-                const float mn = fmaxf(m[e], pm);
-                al[e] = ex2_approx(m[e] - mn);  // 0 on the first page (m = -inf)
-                m[e] = mn;
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    z[u][e] = x[u][e] - mn;
-                    z[u][2 + e] = x[u][2 + e] - mn;
-                }
-            }
-        }
-        float grow = 1.f, smax = fmaxf(fmaxf(sv[0][0], sv[0][1]), fmaxf(sv[1][0], sv[1][1]));
-        if (__any_sync(kFull, smax > sref)) {
-#pragma unroll
-            for (int off = 4; off <= 16; off <<= 1)
-                smax = fmaxf(smax, __shfl_xor_sync(kFull, smax, off));
-            const float inv = rcp_approx(smax);
-            grow = sref * inv;  // 0 on the first page
-            sref = smax;
-            sinv = inv;
-        }
-        const float c0 = al[0] * grow, c1 = al[1] * grow;
-        if (__any_sync(kFull, c0 != 1.f || c1 != 1.f)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                o[i][0] *= c0;
-                o[i][1] *= c1;
-                o[i][2] *= c0;
-                o[i][3] *= c1;
-            }
-        }
-        uint32_t b[2][2];
-        float sum[2] = {0.f, 0.f};
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const float p0 = ex2_approx(z[u][2 * q]), p1 = ex2_approx(z[u][2 * q + 1]), r = sv[u][q] * sinv;
-                sum[0] += p0;
-                sum[1] += p1;
-                b[u][q] = movmatrix_trans(pack_f16x2(p0 * r, p1 * r));
-            }
-        l[0] = fmaf(l[0], al[0], sum[0]);
-        l[1] = fmaf(l[1], al[1], sum[1]);
-        const uint32_t chunk = (uint32_t)((gid ^ (2 * tig)) << 4);
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint8_t *vt = unit[u] + kFp8Tile;
-            const uint4 u0 = *reinterpret_cast<const uint4 *>(vt + tig * 2 * kD + chunk);
-            const uint4 u1 = *reinterpret_cast<const uint4 *>(vt + (tig + 4) * 2 * kD + chunk);
-            const uint32_t w0[4] = {u0.x, u0.y, u0.z, u0.w}, w1[4] = {u1.x, u1.y, u1.z, u1.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t av[4];
-                e4m3x4_to_f16x2(w0[i], av[0], av[1]);
-                e4m3x4_to_f16x2(w1[i], av[2], av[3]);
-                mma_f16(o[i], av, b[u][0], b[u][1]);
-            }
-        }
-    }
-
     // m[4], l[4] (log2 domain) and o[4][64] (true units), the layout of the BF16 policies
     __device__ __forceinline__ void store_state(float *dst)
     {
