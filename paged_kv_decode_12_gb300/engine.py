@@ -34,6 +34,12 @@ prefix, ``attention_scored`` also gathers every cached token's weight, and ``evi
 caches to a budget by those weights (``append`` with ``slots`` then puts a token behind a cut
 cache: its position is no longer its slot).  ``pages_per_chunk=0`` leaves the size of the work
 units to the library in all of these (the step's, where it has a window).
+
+Chunks: a step whose sequences bring several new tokens each (prompts, pieces of prompts) beside
+those that bring one.  ``chunk_tables`` extends the block tables on the GPU from a list of pages
+(``take_pages``) and makes positions and slots, then every layer runs ``chunk_append`` (norms of the
+heads, rotation, the rows to their pages) and ``chunk_attention``.  All three can be captured and
+replayed with other lengths.
 """
 from __future__ import annotations
 
@@ -89,6 +95,7 @@ class DecodeEngine:
         self.attn_options = pkv.PKV_DECODE_SPLIT_MERGE | variant if split_merge else self.step_options
         self.bt = None
         self.bt_host = None
+        self._device_tables = False  # chunk_tables has run (or is in a graph): bt is ahead of bt_host
         self._extra_ws = {}   # workspaces of the shared, scored and evict calls, by call: [outgrown ones, current]
         self.chains = chains
         self.chain_bounds = chain_bounds(batch, chains)
@@ -498,6 +505,8 @@ class DecodeEngine:
         with torch.cuda.stream(s):
             if torch.cuda.is_current_stream_capturing():
                 raise RuntimeError("an eviction takes and gives back pages on the host: it cannot be captured")
+        if self._device_tables:
+            self.read_tables(stream)
         old = self.bt_host[layer]
         pages = (lens + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
         if ((old < 0) & (np.arange(self.max_blocks)[None, :] < pages[:, None])).any():
@@ -528,6 +537,87 @@ class DecodeEngine:
         self.bt_host = self.bt_host.copy()  # (the caller may hold the old tables)
         self.bt_host[layer] = dst
         return after
+
+    # ------------------------------------------------------------------ chunks of new tokens
+    def take_pages(self, n: int) -> torch.Tensor:
+        """``n`` pages of the pool as a list for ``chunk_tables`` (int32, on the device)."""
+        return torch.from_numpy(pkv.pkv_pool_alloc(self.pool, n)).to(self.device)
+
+    def read_tables(self, stream=None) -> np.ndarray:
+        """``bt_host`` from the device, where ``chunk_tables`` extends the tables, once the work on the
+        stream is done."""
+        with torch.cuda.stream(self._on(stream)):
+            self.bt_host = self.bt.cpu().numpy()
+        return self.bt_host
+
+    def _device_arrays(self, **arrays) -> None:
+        for name, (t, dtype, shape) in arrays.items():
+            if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or
+                    t.device.type != self.device.type):
+                raise ValueError(f"{name}: {dtype} {tuple(shape)}, contiguous, on the engine's device")
+
+    def chunk_tables(self, seq_lens_dev, new_dev, pages_dev, used_dev, starts, pos, slots, seq_lens_out=None,
+                     used_out=None, stream=None) -> None:
+        """pkv_chunk_tables of all layers: sequence b, of seq_lens[b] tokens, brings new[b]; the pages come
+        from ``pages_dev``, of which the first ``used_dev`` are taken.  Written: ``starts`` [batch + 1],
+        ``pos`` [T], ``slots`` int64 [layers][T] for T tokens at most, the lengths and the count of taken
+        pages (in place by default).  The engine has tables before (``set_tables``: -1 everywhere for
+        sequences without pages)."""
+        seq_lens_out = seq_lens_dev if seq_lens_out is None else seq_lens_out
+        used_out = used_dev if used_out is None else used_out
+        B, T, i32 = self.batch, pos.numel(), torch.int32
+        self._device_arrays(seq_lens=(seq_lens_dev, i32, (B,)), new=(new_dev, i32, (B,)),
+                            pages=(pages_dev, i32, (pages_dev.numel(),)), used=(used_dev, i32, (1,)),
+                            starts=(starts, i32, (B + 1,)), pos=(pos, i32, (T,)),
+                            slots=(slots, torch.int64, (self.layers, T)), seq_lens_out=(seq_lens_out, i32, (B,)),
+                            used_out=(used_out, i32, (1,)))
+        if self.bt is None:
+            raise ValueError("the engine has no tables to extend (set_tables)")
+        nbytes = pkv.pkv_chunk_tables_workspace_bytes(B)
+        workspace = self._workspace("chunk_tables", nbytes, stream)
+        pkv.pkv_chunk_tables(self.pool, seq_lens_dev, new_dev, B, self.bt, self.max_blocks, self.layers, pages_dev,
+                             pages_dev.numel(), used_dev, used_out, T, starts, seq_lens_out, pos, slots,
+                             workspace, nbytes, self.err, stream)
+        self._device_tables = True
+
+    def chunk_append(self, k, v, q, slots, pos, q_out=None, q_norm=None, k_norm=None, eps: float = 1e-5,
+                     axis_pairs=None, stream=None) -> None:
+        """pkv_chunk_append of one layer: rows k, v [T][8][64] and q [T][32][64], BF16, of tokens any distance
+        apart (a projection's columns), to ``slots`` int64 [T] (-1: padding).  ``pos`` int32 [T], or [3][T]
+        with ``axis_pairs``, the pairs that turn by each axis.  ``q_out`` [T][32][64]: the query (in place by
+        default)."""
+        T = k.shape[0]
+        q_out = q if q_out is None else q_out
+        for name, x, heads in (("k", k, wl.NUM_KV_HEADS), ("v", v, wl.NUM_KV_HEADS), ("q", q, wl.NUM_Q_HEADS),
+                               ("q_out", q_out, wl.NUM_Q_HEADS)):
+            if (x.dtype != torch.bfloat16 or tuple(x.shape) != (T, heads, wl.HEAD_DIM) or x.device.type != self.device.type or
+                    x.stride()[1:] != (wl.HEAD_DIM, 1)):
+                raise ValueError(f"{name}: bfloat16 [T][{heads}][{wl.HEAD_DIM}], a token's heads together, on the engine's device")
+        self._device_arrays(slots=(slots, torch.int64, (T,)),
+                            pos=(pos, torch.int32, (T,) if axis_pairs is None else (3, T)),
+                            **{name: (w, torch.bfloat16, (wl.HEAD_DIM,)) for name, w in (("q_norm", q_norm), ("k_norm", k_norm))
+                               if w is not None})
+        if not q_out.is_contiguous():
+            raise ValueError("q_out: contiguous (give one where q is not)")
+
+        def stride(x, heads):  # (of a single token it may be anything)
+            return x.stride(0) if T > 1 else heads * wl.HEAD_DIM
+
+        pkv.pkv_chunk_append(self.pool, k, stride(k, wl.NUM_KV_HEADS), v, stride(v, wl.NUM_KV_HEADS), q,
+                             stride(q, wl.NUM_Q_HEADS), q_out, q_norm, k_norm, eps, slots, pos, T, axis_pairs, T,
+                             self.rope, self.max_pos, self.err, stream)
+
+    def chunk_attention(self, layer: int, q, seq_lens_dev, starts, out, stream=None) -> None:
+        """pkv_chunk_attention of one layer, with the engine's window: q, out [T][32][64], lengths after the
+        append, ``starts`` as chunk_tables made them."""
+        T = q.shape[0]
+        self._device_arrays(q=(q, torch.bfloat16, (T, wl.NUM_Q_HEADS, wl.HEAD_DIM)), out=(out, torch.bfloat16, q.shape),
+                            seq_lens=(seq_lens_dev, torch.int32, (self.batch,)),
+                            starts=(starts, torch.int32, (self.batch + 1,)))
+        nbytes = pkv.pkv_chunk_attention_workspace_bytes(self.batch, T)
+        pkv.pkv_chunk_attention(self.pool, q, self.bt[layer], self.max_blocks, seq_lens_dev, starts, self.batch, T,
+                                self.scale, self.window, self.sinks, self._workspace("chunk_attention", nbytes, stream),
+                                nbytes, out, self.err, stream, self.step_options & pkv.PKV_STEP_NO_PDL)
 
     def check_errors(self):
         return pkv.pkv_check_device_error(self.err)
