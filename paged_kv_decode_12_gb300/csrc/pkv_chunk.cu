@@ -5,13 +5,14 @@
 // 32 tokens and the 4 query heads of a KV head are 128 rows that meet the same keys: S = Q K^T and O += P V
 // on the tensor cores (tcgen05), Q, S, P and O in tensor memory, K and V in shared memory as TMA brought the
 // pages.  A CTA has two such row tiles at a time, each with four softmax warps (a thread a row) and an issuer
-// warp, so that one's products fill the other's exponentials.  Where there are many sequences, those that bring
-// a single token, 4 rows a KV head, are left to a kernel of their own (pkv_chunk_single.cu).  pkv_chunk_plan.cuh says how the work is cut into one run for every CTA.
+// warp, so that one's products fill the other's exponentials.  Where there are many sequences, those that bring a
+// single token, 4 rows a KV head, are left to a kernel of their own (pkv_chunk_single.cu).  pkv_chunk_plan.cuh says
+// how the work is cut into one run for every CTA.
 //
 // Masks: only tiles in which some row does not attend to some token (the last ones, and a window's
 // first) are masked, by 64 bits a row and half tile.  A weight of 0 times a value that is not finite would
-// not be 0, so in those tiles an issuer warp (FP8: the warps that convert) looks for such values and clears them; rows that attend to one get NaN
-// in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us where 259 were without.)
+// not be 0, so in those tiles an issuer warp (FP8: the warps that convert) looks for such values and clears them; rows
+// that attend to one get NaN in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us where 259 were without.)
 #include <cmath>
 
 #include "pkv_chunk_run.cuh"
@@ -65,6 +66,7 @@ struct ChunkShared : RunShared {
     uint32_t tmem;
     int bad[kStages], raw_bad[kRaws];            // the tile has a bad page id
     int noted[kStages];                          // the last load into the stage with notes on values (see Poison)
+    int claimed;                                 // (BF16) pairs' masked loads up to here are being gone through
     int last[2];                                 // row tile s: this CTA finished the item last
     Poison poison[kStages][kTilePages * kPage];
     int64_t sums[(kPreparer + kPreparers) * 32];
@@ -267,13 +269,20 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, Chu
             issue_scores(base + st * kStageSize + h * 1024, ts + h * kHalf, tq, &sh.s_full[s][h]);
             return true;
         };
+        const auto first_at = [&](int check) {
+            int before = 0;
+            if ((threadIdx.x & 31) == 0)
+                before = atomicMax(&sh.claimed, check + 1);
+            return __shfl_sync(kFull, before, 0) <= check;
+        };
         const auto output = [&](int j, int h) {
             const int seq = loaded + x.order(s, j), st = seq % kStages;
             if (!FP8 && h == 0 && x.masked(x.j0 + j)) {
-                // (a pair's values, which both row tiles read, by the first one's issuer)
+                // (a pair's values, which both row tiles read, by the issuer that comes first; by the first row tile's,
+                // the second waited for it up to 6500 clocks an item)
                 const int check = checks + x.masked_loads(j) + (x.kind == plan::kHeads ? s : 0);
                 uint64_t *checked = &sh.checked[check % kStages];
-                if (x.kind == plan::kHeads || s == 0) {
+                if (x.kind == plan::kHeads || first_at(check)) {
                     check_values<32>(x, x.j0 + j, stages + st * kStageSize, sh.poison[st], &sh.noted[st], seq,
                                      threadIdx.x & 31);
                     __syncwarp();
@@ -331,13 +340,17 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0
 __device__ __forceinline__ uint2 columns(const Item &x, int j, int hf, int p, int window, int sinks)
 {
     uint32_t w[2] = {0, 0};
-    const int lo = window ? max(p + 1 - window, 0) : 0, at = j * kTilePages;
+    if (!window) {  // (the pages are those from the first one on, and the last holds p at the latest)
+#pragma unroll
+        for (int i = 0; i < kTilePages; ++i)
+            w[i / 4] |= low_bits(p + 1 - (j * kTilePages + i) * kPage - 8 * hf) << (i % 4 * 8);
+        return make_uint2(w[0], w[1]);
+    }
+    const int lo = max(p + 1 - window, 0), at = j * kTilePages;
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
         const int first = x.page(at + i) * kPage + 8 * hf;
-        uint32_t bits = low_bits(p + 1 - first);
-        if (window)
-            bits &= ~low_bits(lo - first) | low_bits(sinks - first);
+        uint32_t bits = low_bits(p + 1 - first) & (~low_bits(lo - first) | low_bits(sinks - first));
         if (at + i >= x.count)
             bits = 0;
         w[i / 4] |= bits << (i % 4 * 8);
@@ -561,7 +574,8 @@ struct Softmax {
     // finishes last and has everybody's partials to read.  False if a wait gave up.
     __device__ __forceinline__ bool draw_ticket(const Item &x, bool &last)
     {
-        __threadfence();
+        // (what the threads have written comes before their meeting, that before the ticket, and the
+        // ticket before whoever draws a later one: no fences besides)
         if (!meet())
             return false;
         if ((int)threadIdx.x == s * 128) {
@@ -576,8 +590,6 @@ struct Softmax {
         if (!meet())
             return false;
         last = *(volatile int *)&sh.last[s] != 0;
-        if (last)
-            __threadfence();
         return true;
     }
 
@@ -846,15 +858,19 @@ struct Softmax {
     }
 
     // The warp's rows of a cut item, of all parts: two rows at a time, 16 lanes each, 16 bytes a lane, 16 rows'
-    // loads of a part on their way at once.
+    // loads of two parts on their way at once.
     __device__ __forceinline__ void join(const Item &x, int live) const
     {
         if (live <= 0)
             return;
-        const int w0 = (warp & 3) * 32;
+        const int w0 = (warp & 3) * 32, last = x.parts - 1;
         float M = -INFINITY;  // of row `lane`
-        for (int i = 0; i < x.parts; ++i)
-            M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, i, s) + w0 + lane).x);
+#pragma unroll 1
+        for (int i = 0; i < x.parts; i += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, min(i + k, last), s) + w0 + lane).x);
+        }
 #pragma unroll 1
         for (int k0 = 0; k0 < 16; k0 += 8) {
             float l = 0.f;
@@ -863,25 +879,32 @@ struct Softmax {
             for (int k = 0; k < 8; ++k)
                 o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
-            for (int i = 0; i < x.parts; ++i) {
-                const size_t at = part_rows(x, i, s) + w0;
-                const float2 ml = __ldcg(a.part_ml + at + lane);
-                const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kD) + k0 * 32 + lane;
-                float4 v[8];
+            for (int i = 0; i < x.parts; i += 2) {
+                float2 ml[2];
+                float4 v[2][8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    v[k] = __ldcg(src + k * 32);
-                const bool none = ml.x == -INFINITY;  // (and then nothing may be wrong with it)
-                const float f = none ? -1.f : ex2_approx(ml.x - M);
-                l = none ? l : fmaf(f, ml.y, l);
+                for (int n = 0; n < 2; ++n) {
+                    const size_t at = part_rows(x, min(i + n, last), s) + w0;
+                    ml[n] = __ldcg(a.part_ml + at + lane);
+                    const float4 *src = reinterpret_cast<const float4 *>(a.part_o + at * kD) + k0 * 32 + lane;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float g = __shfl_sync(kFull, f, 2 * (k0 + k) + lane / 16);
-                    if (!(g < 0.f)) {
-                        o[k].x = fmaf(g, v[k].x, o[k].x);
-                        o[k].y = fmaf(g, v[k].y, o[k].y);
-                        o[k].z = fmaf(g, v[k].z, o[k].z);
-                        o[k].w = fmaf(g, v[k].w, o[k].w);
+                    for (int k = 0; k < 8; ++k)
+                        v[n][k] = __ldcg(src + k * 32);
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const bool none = ml[n].x == -INFINITY || i + n > last;  // (and then nothing may be wrong with it)
+                    const float f = none ? -1.f : ex2_approx(ml[n].x - M);
+                    l = none ? l : fmaf(f, ml[n].y, l);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float g = __shfl_sync(kFull, f, 2 * (k0 + k) + lane / 16);
+                        if (!(g < 0.f)) {
+                            o[k].x = fmaf(g, v[n][k].x, o[k].x);
+                            o[k].y = fmaf(g, v[n][k].y, o[k].y);
+                            o[k].z = fmaf(g, v[n][k].z, o[k].z);
+                            o[k].w = fmaf(g, v[n][k].w, o[k].w);
+                        }
                     }
                 }
             }
@@ -951,6 +974,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ C
             mbar_init(&sh.item_empty[i], TileRun<FP8>::kConsumers);
         }
         sh.stop = 0;
+        sh.claimed = 0;
         sh.taken[0][0] = sh.taken[0][1] = sh.taken[1][0] = sh.taken[1][1] = 0;
         fence_barrier_init();
     }
@@ -970,15 +994,17 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ C
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = sh.tmem;
-    // FP8: 512 threads of 128 registers; the softmax warps take 168, so that none spill, and leave the
-    // others 88.  (Registers move by fours of warps.)
+    // FP8: 512 threads of 128 registers; the softmax warps take 176 and leave the others 80 (168 and 88: 2048 tokens
+    // behind 63000 1366 us where this takes 1350; 184 and 72: 1452).  (Registers move by fours of warps.  BF16's
+    // 384 threads have 168 each; with 512, four of its warps to go through masked tiles: 251 us for 2048 behind
+    // 14000 where this takes 231.)
     if (warp < kLoader) {
         if constexpr (FP8)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         Softmax<FP8>(a, sh, stages, rows, tmem).run();
     } else {
         if constexpr (FP8)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         if (warp == kLoader)
             loader<FP8>(&tmap, a, stages, raws, sh);
         else if (warp < kIssuer + 2)

@@ -109,8 +109,7 @@ struct Team {
     // Ticket of a cut item, whose partials all threads have written; false if a wait gave up.
     __device__ __forceinline__ bool draw_ticket(const Item &x, bool &last)
     {
-        __threadfence();
-        if (!meet())
+        if (!meet())  // (no fences besides: see the tile kernel's)
             return false;
         if (threadIdx.x == 0) {
             int *ticket = &a.tickets[x.first * 2];
@@ -124,8 +123,6 @@ struct Team {
         if (!meet())
             return false;
         last = *(volatile int *)&sh.last != 0;
-        if (last)
-            __threadfence();
         return true;
     }
 

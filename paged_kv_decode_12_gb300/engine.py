@@ -53,6 +53,8 @@ from . import workloads as wl
 
 
 class DecodeEngine:
+    _device_tables = False  # chunk_tables has run (or is in a graph): bt is ahead of bt_host
+
     def __init__(self, num_pages: int, layers: int, batch: int, max_blocks: int = wl.MAX_BLOCKS,
                  pages_per_chunk: int = 16, variant: int = pkv.PKV_DECODE_DEFAULT, max_pos: int = wl.MAX_CONTEXT,
                  theta: float = wl.ROPE_THETA, pool_seed: int = 0, device: str = "cuda", fused: bool = True,
@@ -95,7 +97,6 @@ class DecodeEngine:
         self.attn_options = pkv.PKV_DECODE_SPLIT_MERGE | variant if split_merge else self.step_options
         self.bt = None
         self.bt_host = None
-        self._device_tables = False  # chunk_tables has run (or is in a graph): bt is ahead of bt_host
         self._extra_ws = {}   # workspaces of the shared, scored and evict calls, by call: [outgrown ones, current]
         self.chains = chains
         self.chain_bounds = chain_bounds(batch, chains)
