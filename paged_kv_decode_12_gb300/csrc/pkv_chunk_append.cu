@@ -25,6 +25,7 @@ namespace {
 using namespace dev;
 
 constexpr int kRowsWarps = 4, kRowsCtas = 8;  // of an SM: 64 registers a thread
+constexpr int kAhead = 2;                      // rounds whose loads are on their way (see the launch)
 constexpr int kMaxAxes = 3;
 
 struct ChunkAppendArgs {
@@ -46,14 +47,15 @@ struct ChunkAppendArgs {
 };
 
 // Four consecutive BF16 values.
-__device__ __forceinline__ void load4(const uint16_t *p, float (&x)[4])
+__device__ __forceinline__ void values4(uint2 w, float (&x)[4])
 {
-    const uint2 w = *reinterpret_cast<const uint2 *>(p);
     x[0] = bf16lo(w.x);
     x[1] = bf16hi(w.x);
     x[2] = bf16lo(w.y);
     x[3] = bf16hi(w.y);
 }
+
+__device__ __forceinline__ void load4(const uint16_t *p, float (&x)[4]) { values4(*reinterpret_cast<const uint2 *>(p), x); }
 
 // rope_comb with its last sum left in two parts.
 __device__ __forceinline__ void rope_parts(float a, float b, float ch, float cl, float sh, float sl, float &hi, float &lo)
@@ -216,11 +218,24 @@ __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float scale, flo
 }
 
 // One token: `part` of `parts` takes the rounds part, part + parts, ... of 10 (8 of four query heads, 2 of four KV heads).
-template <bool FP8, bool NORM>
-__device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int part, int parts)
+// WHOLE: one warp takes them all, and the first loads go out before slot, position and table entries are there.
+template <bool FP8, bool NORM, bool WHOLE>
+__device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int part_, int parts_)
 {
+    const int part = WHOLE ? 0 : part_, parts = WHOLE ? 1 : parts_;
     const int lane = threadIdx.x & 31, j = lane & 7, hh = lane >> 3;
     const int64_t at = a.slots[t];
+    uint2 ahead[kAhead][2];  // the query's next rounds
+    const uint16_t *src_q = a.q + t * a.q_stride + hh * kD + 4 * j;
+    const auto load_round = [&](int r, uint2 (&w)[2]) {
+        w[0] = *reinterpret_cast<const uint2 *>(src_q + r * 4 * kD);
+        w[1] = *reinterpret_cast<const uint2 *>(src_q + r * 4 * kD + kD / 2);
+    };
+    if (WHOLE && a.q) {
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            load_round(k, ahead[k]);
+    }
     if (at == -1)
         return;  // padding
     if (at < 0 || at >= (int64_t)a.num_pages * kPage) {
@@ -249,19 +264,34 @@ __device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int 
             load4(a.q_norm + 4 * j, w1);
             load4(a.q_norm + kD / 2 + 4 * j, w2);
         }
-        const uint16_t *src = a.q + t * a.q_stride + hh * kD + 4 * j;
         uint16_t *dst = a.q_out + (size_t)t * kHq * kD + hh * kD + 4 * j;
-#pragma unroll 2
-        for (int r = part; r < kHq / 4; r += parts) {
-            float x1[4], x2[4];
-            load4(src + r * 4 * kD, x1);
-            load4(src + r * 4 * kD + kD / 2, x2);
+        const auto round = [&](int r, float (&x1)[4], float (&x2)[4]) {
             if constexpr (NORM)
                 turn_query_row(x1, x2, w1, w2, a.eps, cs);
             else
                 turn_row<false>(x1, x2, w1, w2, a.eps, cs);
             *reinterpret_cast<uint2 *>(dst + r * 4 * kD) = pack4(x1);
             *reinterpret_cast<uint2 *>(dst + r * 4 * kD + kD / 2) = pack4(x2);
+        };
+        float x1[4], x2[4];
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int r = 0; r < kHq / 4; ++r) {
+                values4(ahead[r % kAhead][0], x1);
+                values4(ahead[r % kAhead][1], x2);
+                if (r + kAhead < kHq / 4)
+                    load_round(r + kAhead, ahead[r % kAhead]);
+                round(r, x1, x2);
+            }
+        } else {
+#pragma unroll 2
+            for (int r = part; r < kHq / 4; r += parts) {
+                uint2 w[2];
+                load_round(r, w);
+                values4(w[0], x1);
+                values4(w[1], x2);
+                round(r, x1, x2);
+            }
         }
     }
     if constexpr (NORM) {
@@ -313,7 +343,7 @@ __device__ __forceinline__ void token_rows(const ChunkAppendArgs &a, int t, int 
     }
 }
 
-template <bool FP8, bool NORM>
+template <bool FP8, bool NORM, bool WHOLE>
 __global__ void __launch_bounds__(kRowsWarps * 32, kRowsCtas) chunk_append_kernel(ChunkAppendArgs a, int parts)
 {
     grid_dependency_wait();
@@ -321,10 +351,12 @@ __global__ void __launch_bounds__(kRowsWarps * 32, kRowsCtas) chunk_append_kerne
     const int w = blockIdx.x * kRowsWarps + (threadIdx.x >> 5);
     const int t = w / parts;
     if (t < a.T)
-        token_rows<FP8, NORM>(a, t, w - t * parts, parts);
+        token_rows<FP8, NORM, WHOLE>(a, t, w - t * parts, parts);
 }
 
-// Few tokens are shared by several warps each, so that their rounds overlap: enough of them for 32 warps an SM.
+// Few tokens are shared by several warps each, so that their rounds overlap: enough of them for 32 warps an SM.  Many
+// have a warp each, which loads two rounds ahead (16384 tokens: 41 us, FP8 48, where the loop over its rounds took 52 and
+// 60; with four or eight rounds ahead, at more registers and fewer warps, 42 to 47 and 49 to 58).
 constexpr int kEnoughWarps = 152 * 32;
 
 template <bool FP8, bool NORM>
@@ -335,7 +367,7 @@ int launch_chunk_append(const ChunkAppendArgs &a, cudaStream_t s)
         if ((int64_t)a.T * parts < kEnoughWarps)
             parts = p;
     const int64_t warps = (int64_t)a.T * parts;
-    return launch_kernel(chunk_append_kernel<FP8, NORM>, dim3((unsigned)((warps + kRowsWarps - 1) / kRowsWarps)),
+    return launch_kernel(parts == 1 ? chunk_append_kernel<FP8, NORM, true> : chunk_append_kernel<FP8, NORM, false>, dim3((unsigned)((warps + kRowsWarps - 1) / kRowsWarps)),
                          dim3(kRowsWarps * 32), 0, s, true, a, parts);
 }
 
