@@ -40,7 +40,7 @@ struct TileRun {
     static constexpr int kThreads = (FP8 ? kPreparer + kPreparers : kPreparer) * 32;
     static constexpr int kConsumers = FP8 ? 8 + 3 + kPreparers : 8 + 3;
     static constexpr bool kSingles = false;
-    static constexpr int kLeast = 64;  // of a CTA's run
+    static constexpr int kLeast = 32;  // of a CTA's run (64 tokens behind 2000: 23 us; at 64 eighths 25, at 16 24; 200 behind 500: 21, 30, 21)
     // in eighths of the time of a BF16 key tile of two row tiles
     static __device__ __forceinline__ Costs costs()
     {
