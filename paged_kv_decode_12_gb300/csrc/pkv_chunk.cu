@@ -762,7 +762,7 @@ struct Softmax {
         float m = -INFINITY;
         int bad = 0;
         uint32_t nan_lo = 0, nan_hi = 0;
-        if (a.expire && s == 0 && used == 0 && blockIdx.x == 0) {
+        if (a.expire && s == 0 && used == 0) {
             *(volatile int *)&sh.stop = 1;
             return false;
         }

@@ -128,10 +128,11 @@ __device__ __forceinline__ int64_t row_cost(const ChunkArgs &a, const Row &x, co
 {
     if (!x.n || !length_fits(a, x))
         return 0;
-    const plan::Sequence seq(x.n, x.L - x.n, a.window, a.sinks, k);
-    if constexpr (Run::kSingles)
-        return x.n == 1 ? kHkv * seq.single_cost(k) : 0;
-    return a.apart && x.n == 1 ? 0 : seq.cost(k);
+    if (Run::kSingles ? x.n != 1 : a.apart && x.n == 1)
+        return 0;
+    if (plan::short_row(x.n, x.L))
+        return plan::row_cost<int>(x.n, x.L, a.window, a.sinks, k, Run::kSingles);
+    return plan::row_cost<int64_t>(x.n, x.L, a.window, a.sinks, k, Run::kSingles);
 }
 
 // All threads: the prefix sums of the sequences' costs, the rows that are refused.
@@ -198,16 +199,16 @@ __device__ __forceinline__ bool give(RunShared &sh, const Item &it, int &n)
 
 // The pieces of this CTA's run, in order, by a whole warp, given to the others; or (`over`: something gave up) the
 // tickets of cut items that were not drawn, so that the next call finds zeros.
-template <class Run, class Shared>
-__device__ __noinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
+template <class Run, class I, class Shared>
+__device__ __noinline__ void pieces_of(const ChunkArgs &a, Shared &sh, bool over)
 {
     int given = 0;
     const Costs k = Run::costs();
-    const plan::Line line = plan::line_of(sh.length, gridDim.x, Run::kLeast);
+    const plan::Line<I> line((I)sh.length, gridDim.x, Run::kLeast);
     const int lane = threadIdx.x & 31, per = (a.B + Run::kThreads - 1) / Run::kThreads;
     const bool work = line.length > 0 && (int)blockIdx.x < line.ctas;
-    const int64_t x0 = work ? line.border(blockIdx.x) : 0, x1 = work ? line.border(blockIdx.x + 1) : 0;
-    int64_t x = x0;
+    const I x0 = work ? line.border(blockIdx.x) : 0, x1 = work ? line.border(blockIdx.x + 1) : 0;
+    I x = x0;
     while (x < x1) {
         // the thread whose sequences hold x (the last whose sum is not above it), and the sequence
         int lo = 0, hi = Run::kThreads;
@@ -219,28 +220,29 @@ __device__ __noinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
                 hi = mid;
         }
         const int b0 = lo * per + lane;
-        const int64_t mine = lane < per && b0 < a.B ? row_cost<Run>(a, row_of(a, b0), k) : 0;
-        int64_t upto = mine;
+        const I mine = lane < per && b0 < a.B ? (I)row_cost<Run>(a, row_of(a, b0), k) : 0;
+        I upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(kFull, upto, off);
+            const I y = __shfl_up_sync(kFull, upto, off);
             if (lane >= off)
                 upto += y;
         }
-        const unsigned behind = __ballot_sync(kFull, sh.sums[lo] + upto > x);
+        const I sum = (I)sh.sums[lo];
+        const unsigned behind = __ballot_sync(kFull, sum + upto > x);
         if (!behind)
             break;  // (not reached: the sums add up to the length)
         const int at = __ffs(behind) - 1, b = lo * per + at;
-        const int64_t begin = sh.sums[lo] + __shfl_sync(kFull, upto - mine, at), end = sh.sums[lo] + __shfl_sync(kFull, upto, at);
+        const I begin = sum + __shfl_sync(kFull, upto - mine, at), end = sum + __shfl_sync(kFull, upto, at);
         const Row row = row_of(a, b);
-        const plan::Sequence seq(row.n, row.L - row.n, a.window, a.sinks, k);
-        const int64_t head = Run::kSingles ? 0 : seq.head_cost(), rest = Run::kSingles ? 0 : seq.rest_cost(k);
-        const int64_t single = Run::kSingles ? seq.single_cost(k) : 0;
+        const plan::Sequence<I> seq(row.n, row.L - row.n, a.window, a.sinks, k);
+        const I head = Run::kSingles ? 0 : seq.head_cost(), rest = Run::kSingles ? 0 : seq.rest_cost(k);
+        const I single = Run::kSingles ? seq.single_cost(k) : 0;
         while (x < x1 && x < end) {
             Item it;
             PageList pages;
-            int64_t s;  // where the item begins
-            int64_t y = x - begin;
+            I s;  // where the item begins
+            I y = x - begin;
             int token = 0;
             it.b = b;
             if (Run::kSingles) {
@@ -270,7 +272,7 @@ __device__ __noinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
                 pages = seq.pair_pages(r);
             } else {
                 it.kind = plan::kHeads;
-                const int h = plan::eighth(y - kHkv * head, rest);
+                const int h = plan::eighth((I)(y - kHkv * head), rest);
                 it.g = 2 * h;
                 s = begin + kHkv * head + h * rest;
                 token = 64 * seq.pairs;
@@ -302,13 +304,22 @@ __device__ __noinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
                             a.tickets[it.first * 2 + r] = 0;
                 }
             }
-            x = s + (int64_t)it.nt * tile + item;
+            x = s + (I)it.nt * tile + item;
         }
     }
     if (!over) {
         Item end = {};
         (void)give(sh, end, given);
     }
+}
+
+template <class Run, class Shared>
+__device__ __forceinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
+{
+    if (sh.length < 1 << 30)
+        pieces_of<Run, int>(a, sh, over);
+    else
+        pieces_of<Run, int64_t>(a, sh, over);
 }
 
 // The items in order, as a warp of another role goes through them; one is held until it is let go.

@@ -148,11 +148,11 @@ struct Team {
         int sent = min(pages, kSlots);  // of them, on their way or done with
         const int p = x.p0, lo = a.window ? max(p + 1 - a.window, 0) : 0;
         for (int k = 0; k < pages; ++k, ++seen) {
-            if (a.expire && blockIdx.x == 0 && feed.n == 0)
+            if (a.expire && feed.n == 0)
                 *(volatile int *)&sh.stop = 1;  // (and the wait is skipped)
             else if (!wait_for(&sh.here[warp][seen % kSlots], (seen / kSlots) & 1, &sh.stop))
                 return false;
-            if (a.expire && blockIdx.x == 0 && feed.n == 0)
+            if (a.expire && feed.n == 0)
                 return false;
             const uint8_t *page = places + seen % kSlots * kUnit;
             const int i = first_page(x) + k * kTeam;
