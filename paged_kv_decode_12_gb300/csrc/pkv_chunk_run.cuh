@@ -200,7 +200,7 @@ __device__ __forceinline__ bool give(RunShared &sh, const Item &it, int &n)
 // The pieces of this CTA's run, in order, by a whole warp, given to the others; or (`over`: something gave up) the
 // tickets of cut items that were not drawn, so that the next call finds zeros.
 template <class Run, class I, class Shared>
-__device__ __noinline__ void pieces_of(const ChunkArgs &a, Shared &sh, bool over)
+__device__ __forceinline__ void pieces_of(const ChunkArgs &a, Shared &sh, bool over)
 {
     int given = 0;
     const Costs k = Run::costs();
@@ -314,7 +314,7 @@ __device__ __noinline__ void pieces_of(const ChunkArgs &a, Shared &sh, bool over
 }
 
 template <class Run, class Shared>
-__device__ __forceinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
+__device__ __noinline__ void pieces(const ChunkArgs &a, Shared &sh, bool over)
 {
     if (sh.length < 1 << 30)
         pieces_of<Run, int>(a, sh, over);
