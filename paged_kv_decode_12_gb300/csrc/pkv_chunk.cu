@@ -5,14 +5,15 @@
 // 32 tokens and the 4 query heads of a KV head are 128 rows that meet the same keys: S = Q K^T and O += P V
 // on the tensor cores (tcgen05), Q, S, P and O in tensor memory, K and V in shared memory as TMA brought the
 // pages.  A CTA has two such row tiles at a time, each with four softmax warps (a thread a row) and an issuer
-// warp, so that one's products fill the other's exponentials.  Where there are many sequences, those that bring a
-// single token, 4 rows a KV head, are left to a kernel of their own (pkv_chunk_single.cu).  pkv_chunk_plan.cuh says
+// warp, so that one's products fill the other's exponentials.  Sequences that bring a single token, 4 rows a KV
+// head, are mostly left to a kernel of their own (pkv_chunk_single.cu; apart_of()).  pkv_chunk_plan.cuh says
 // how the work is cut into one run for every CTA.
 //
 // Masks: only tiles in which some row does not attend to some token (the last ones, and a window's
 // first) are masked, by 64 bits a row and half tile.  A weight of 0 times a value that is not finite would
 // not be 0, so in those tiles an issuer warp (FP8: the warps that convert) looks for such values and clears them; rows
-// that attend to one get NaN in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us where 259 were without.)
+// that attend to one get NaN in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us
+// where 259 were without.)
 #include <cmath>
 
 #include "pkv_chunk_run.cuh"
@@ -998,7 +999,9 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ C
     // behind 63000 1366 us where this takes 1350; 184 and 72: 1452).  (Registers move by fours of warps.  BF16's
     // 384 threads have 168 each; with 512, four of its warps to go through masked tiles: 251 us for 2048 behind
     // 14000 where this takes 231.)
-    if (warp < kLoader) {
+    if (sh.length == 0) {
+        // nothing (single tokens alone): at once to the end, so that the single tokens' kernel has the SM
+    } else if (warp < kLoader) {
         if constexpr (FP8)
             asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         Softmax<FP8>(a, sh, stages, rows, tmem).run();
@@ -1040,8 +1043,11 @@ ChunkWorkspace chunk_workspace()
     return w;
 }
 
-// Sequences from which on those with a single token are a kernel's of their own.
-constexpr int kApart = 16;
+// Whether single tokens are a kernel's of their own: where there must be some (fewer than two tokens a sequence: 4
+// sequences of up to 3000 BF16 tokens 17 us apart, 22 among the tiles; 24: 23 and 30), and in large batches.  Where
+// there need be none, the second kernel costs what finding that out takes: BF16, 2 prompts of 300 among 24 sequences
+// 46 us apart and 43 not, 8 of 700 among 64 231 and 245; FP8, whose tiles are dearer, 2 among 8 51 and 62.
+bool apart_of(bool fp8, int B, int T) { return B >= 2 && (T < 2 * B || B >= (fp8 ? 8 : 32)); }
 
 template <bool FP8>
 int launch_chunk(const pkv_pool *pool, const ChunkArgs &a, cudaStream_t s, bool pdl)
@@ -1111,8 +1117,7 @@ extern "C" int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, cons
     void *singles = static_cast<char *>(workspace) + ws.singles();
     if (T == 1)
         return launch_singles(pool, a, singles, s, pdl, false);
-    a.apart = B >= kApart;
-    a.refuses = true;
+    a.apart = apart_of(pool->kv_format == PKV_KV_FP8, B, T);
     if (const int st = pool->kv_format == PKV_KV_FP8 ? launch_chunk<true>(pool, a, s, pdl) : launch_chunk<false>(pool, a, s, pdl);
         st != PKV_OK || !a.apart)
         return st;

@@ -134,7 +134,7 @@ struct Team {
 
     __device__ __forceinline__ bool piece(Feed &feed, const Item &item, uint64_t policy)
     {
-        const Item x = item;
+        const Item &x = item;
         const int pages = own_pages(x);
         int ids = begun == feed.n ? first_ids : own_ids(x, 0);
         if (begun != feed.n)
@@ -195,26 +195,27 @@ struct Team {
             return false;
         if (bad && threadIdx.x == 0 && a.err)
             atomicOr(a.err, PKV_DEVERR_PAGE_RANGE);
-        bool write = x.parts == 1;
+        const Item z = x;  // (held in registers from here on only)
+        bool write = z.parts == 1;
         if (!write) {
-            const size_t at = part_rows(x, x.me) + warp;
+            const size_t at = part_rows(z, z.me) + warp;
             __stcg(reinterpret_cast<float2 *>(a.part_o + at * kD) + lane, make_float2(o0, o1));
             if (lane == 0)
                 __stcg(a.part_ml + at, make_float2(bad ? INFINITY : M, l));
-            if (!draw_ticket(x, write))
+            if (!draw_ticket(z, write))
                 return false;
             if (write) {
                 M = -INFINITY;
-                for (int i = lane; i < x.parts; i += 32)
-                    M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, i) + warp).x);
+                for (int i = lane; i < z.parts; i += 32)
+                    M = fmaxf(M, __ldcg(a.part_ml + part_rows(z, i) + warp).x);
 #pragma unroll
                 for (int off = 16; off; off >>= 1)
                     M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
                 bad = M == INFINITY;
                 l = o0 = o1 = 0.f;
 #pragma unroll 8
-                for (int i = 0; i < x.parts; ++i) {
-                    const size_t from = part_rows(x, i) + warp;
+                for (int i = 0; i < z.parts; ++i) {
+                    const size_t from = part_rows(z, i) + warp;
                     const float2 ml = __ldcg(a.part_ml + from);
                     const float2 v = __ldcg(reinterpret_cast<const float2 *>(a.part_o + from * kD) + lane);
                     const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);

@@ -305,3 +305,16 @@ def test_large_batches(kv, case):
             bad = ~((out[starts[b]:starts[b + 1], h].double() - want).abs() <= off)
             assert not bad.any(), (b, h, bad.nonzero()[:4].tolist())
     pkv.pkv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("B,T", [(1, 2), (2, 3), (2, 4), (7, 13), (7, 14), (8, 15), (8, 16), (31, 61), (31, 62), (32, 64)])
+def test_either_way_of_sharing_out_single_tokens(kv, B, T):
+    """Tokens a sequence next to where single tokens get a kernel of their own, in arrays of T with and without padding."""
+    rng = np.random.default_rng(B * 100 + T)
+    for full in (True, False):
+        new = np.ones(B, int)
+        new[rng.integers(0, B)] += (T - B if full else (T - B) // 2)
+        b = ch.Batch(kv, [(int(rng.integers(0, 150)), int(n)) for n in new], seed=T, pad=T - int(new.sum())).upload().call()
+        assert b.flag() == 0
+        b.check().close()
