@@ -631,7 +631,8 @@ int pkv_append_rope_at(const pkv_pool *pool, const uint16_t *k_new, const uint16
 /* Block tables extended, positions and slots of the new tokens, made on the GPU, for all layers.
  * Sequence b holds seq_lens[b] tokens (its table rows name their pages) and brings new[b] >= 0.
  *   bt_dev     int32 [layers][B][max_blocks]: the new pages' entries are written, layer by layer and
- *              sequence by sequence, from the list; the others stay as they are
+ *              sequence by sequence, from the list; the others stay as they are (a page that a row
+ *              names behind its sequence's last one is replaced, and stays with whoever allocated it)
  *   pages_dev  int32 [pages]: page ids to take (e.g. from pkv_pool_alloc); the first *pages_used_dev
  *              are taken already.  They must be distinct and nobody else's
  *   pages_used_out  int32: those taken after the call; may be pages_used_dev itself

@@ -15,6 +15,9 @@
 // A warp takes a token, or some of its rounds: 8 lanes a head, 4 pairs a lane (8-byte loads, whole sectors), four
 // heads at once, 8 rounds for the query and 2 for the keys and values.  A lane's 4 table entries serve all of its
 // rounds.
+//
+// Many tokens are bound by their bytes and, with FP8 pages, by issue: 16384 with norms 41 us (32 at the rate of a
+// copy), FP8 48 (29); without norms 43.  One token 2.6 us, 1111 7.2: loads behind one another.
 #include <cuda_bf16.h>
 
 #include "pkv_fp8.cuh"

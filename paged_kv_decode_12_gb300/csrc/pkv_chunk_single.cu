@@ -6,10 +6,10 @@
 // themselves, so that the next item's are on their way while this one's result is made.  What is cut is joined by the
 // part that ends last.
 //
-// The bytes of the pages bound it: 200 sequences of up to 4096 FP8 tokens take 97 us where 63 would do at the rate of a
-// copy (128 by a team of 8 warps beside the tile kernel's, 173 by one of 24 warps); BF16 126 us of 120.  A call of
-// one short sequence is bound by its steps one after the other: the plan 1 us, the first piece 2, the pages 2 to 4, the
-// join of what is cut 2.
+// Page products, whose dependent instructions 16 warps an SM hide in part, bound it: 200 sequences of up to 4096 FP8
+// tokens take 92 us where 63 would do at the rate of a copy (128 by a team of 8 warps beside the tile kernel's, 173
+// by one of 24 warps); BF16 128 us of 121.  A call of one short sequence (500 tokens: 10 us) is bound by its
+// steps one after the other: the plan, the first piece, the pages, the join of what is cut.
 #include <type_traits>
 
 #include "pkv_chunk_run.cuh"
@@ -43,7 +43,7 @@ template <bool FP8>
 struct Team {
     static constexpr int kUnit = FP8 ? kFp8Unit : kStageBytes;
     // A warp's places: what four CTAs an SM have room for.  (BF16 pages: 2 take 126 us where 3 take 132; FP8: with a
-    // fifth CTA, at fewer registers than the products need, 105 us where 97.)
+    // fifth CTA and 4 places, at fewer registers than the products need, 99 us where 94.)
     static constexpr int kSlots = FP8 ? 5 : 2;
     const CUtensorMap *tmap;
     const ChunkArgs &a;

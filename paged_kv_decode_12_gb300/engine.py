@@ -562,7 +562,8 @@ class DecodeEngine:
         """pkv_chunk_tables of all layers: sequence b, of seq_lens[b] tokens, brings new[b]; the pages come
         from ``pages_dev``, of which the first ``used_dev`` are taken.  Written: ``starts`` [batch + 1],
         ``pos`` [T], ``slots`` int64 [layers][T] for T tokens at most, the lengths and the count of taken
-        pages (in place by default).  The engine has tables before (``set_tables``: -1 everywhere for
+        pages (in place by default).  Pages that a row names behind its sequence's last one (``build_tables``
+        for more tokens, the ``room`` of ``evict``) are replaced.  The engine has tables before (``set_tables``: -1 everywhere for
         sequences without pages)."""
         seq_lens_out = seq_lens_dev if seq_lens_out is None else seq_lens_out
         used_out = used_dev if used_out is None else used_out
