@@ -341,23 +341,35 @@ __device__ __forceinline__ void issuer(uint8_t *stages, const uint8_t *sums, Chu
 // The low n bits, n of 0..8 after clamping.
 __device__ __forceinline__ uint32_t low_bits(int n) { return (1u << min(max(n, 0), 8)) - 1; }
 
-// What a row at position p attends to in half hf of key tile j.
+// The first columns of a half tile, those of the first t tokens (or fewer than none) from its first column's on, whose
+// pages follow one another: 8 columns, then 8 tokens of the other half.
+__device__ __forceinline__ uint2 first_columns(int t)
+{
+    t = min(max(t, 0), 8 * kPage);
+    const int n = t / kPage * 8 + min(t % kPage, 8);
+    const int lo = min(n, 32), hi = max(n - 32, 0);
+    return make_uint2(lo == 32 ? kFull : (1u << lo) - 1, hi == 32 ? kFull : (1u << hi) - 1);
+}
+
+// What a row at position p attends to in half hf of key tile j.  (What lies behind the item's last page lies behind p.)
 __device__ __forceinline__ uint2 columns(const Item &x, int j, int hf, int p, int window, int sinks)
 {
-    uint32_t w[2] = {0, 0};
-    if (!window) {  // (the pages are those from the first one on, and the last holds p at the latest)
-#pragma unroll
-        for (int i = 0; i < kTilePages; ++i)
-            w[i / 4] |= low_bits(p + 1 - (j * kTilePages + i) * kPage - 8 * hf) << (i % 4 * 8);
-        return make_uint2(w[0], w[1]);
+    const int at = j * kTilePages, lo = window ? max(p + 1 - window, 0) : 0;
+    if (at >= x.sink || at + kTilePages <= x.sink) {
+        const int first = x.page(at) * kPage + 8 * hf;
+        uint2 w = first_columns(p + 1 - first);
+        if (window) {
+            const uint2 below = first_columns(lo - first), sunk = first_columns(sinks - first);
+            w.x &= ~below.x | sunk.x;
+            w.y &= ~below.y | sunk.y;
+        }
+        return w;
     }
-    const int lo = max(p + 1 - window, 0), at = j * kTilePages;
+    uint32_t w[2] = {0, 0};  // (the tile in which the window's pages follow the first ones)
 #pragma unroll
     for (int i = 0; i < kTilePages; ++i) {
         const int first = x.page(at + i) * kPage + 8 * hf;
-        uint32_t bits = low_bits(p + 1 - first) & (~low_bits(lo - first) | low_bits(sinks - first));
-        if (at + i >= x.count)
-            bits = 0;
+        const uint32_t bits = low_bits(p + 1 - first) & (~low_bits(lo - first) | low_bits(sinks - first));
         w[i / 4] |= bits << (i % 4 * 8);
     }
     return make_uint2(w[0], w[1]);
