@@ -479,12 +479,12 @@ template <bool FP8, bool MASKED>
 __device__ __forceinline__ bool half_weights(const HalfRow &h, float m, uint32_t (&p)[32])
 {
     Excess<FP8> ex;
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        uint32_t w[32];
-        tc::ld32(h.ts + q * 32, w);
-        weigh<FP8, MASKED>(h, q, w, m, p + q * 16, ex);
-    }
+    uint32_t w0[32], w1[32];
+    tc::ld32(h.ts, w0);
+    tc::ld32_begin(h.ts + 32, w1);
+    weigh<FP8, MASKED>(h, 0, w0, m, p, ex);
+    tc::loads_done(w1);
+    weigh<FP8, MASKED>(h, 1, w1, m, p + 16, ex);
     return ex.any();
 }
 
@@ -702,11 +702,11 @@ struct Softmax {
                 return false;
 #pragma unroll 1
         for (int hf = 0; hf < 2; ++hf) {
+            HalfRow h = half_row(st, hf);
+            h.mask = columns(x, x.j0 + j, hf, pos, a.window, a.sinks);
             if (!wait_for(&sh.s_full[s][hf], (done + j) & 1, &sh.stop))
                 return false;
             tc::fence_after();
-            HalfRow h = half_row(st, hf);
-            h.mask = columns(x, x.j0 + j, hf, pos, a.window, a.sinks);
             softmax_half<FP8, true>(h, 2 * (done + j) + hf, &sh.o_step[s], &sh.stop, m);
             if (hf == 1) {  // (until its weights are there, the stage is this tile's)
                 bad |= *(volatile int *)&sh.bad[st];
