@@ -46,10 +46,11 @@ struct TileRun {
     static constexpr int kConsumers = FP8 ? 8 + 3 + kPreparers : 8 + 3;
     static constexpr bool kSingles = false;
     static constexpr int kLeast = 32;  // of a CTA's run (64 tokens behind 2000: 23 us; at 64 eighths 25, at 16 24; 200 behind 500: 21, 30, 21)
-    // in eighths of the time of a BF16 key tile of two row tiles
+    // in eighths of the time of a BF16 key tile of two row tiles; what an item costs besides: 24 (18: 16 prompts of 2048
+    // 203 us, 30: 194, where this takes 196, but 33 tokens behind 500, cut then, 18 where 15), FP8 38 (30: 395, this 381)
     static __device__ __forceinline__ Costs costs()
     {
-        return FP8 ? Costs{{0, 14, 16, 0}, {0, 30, 30, 0}} : Costs{{0, 8, 9, 0}, {0, 24, 24, 0}};
+        return FP8 ? Costs{{0, 14, 16, 0}, {0, 38, 38, 0}} : Costs{{0, 8, 9, 0}, {0, 24, 24, 0}};
     }
 };
 
