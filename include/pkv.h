@@ -667,8 +667,8 @@ size_t pkv_chunk_tables_workspace_bytes(int B);
  *   q_norm, k_norm  BF16 [64]: weights of the norms; NULL (both, where there is a q): no norms.  eps > 0 with
  *              norms.  (Weights up to 2^60 in size; rows of any finite values.)
  *   slots_dev  int64 [T]: the rows go to page slot / 16, place slot % 16; -1: the token is padding and
- *              nothing of it is written.  Slots of a call must be distinct (one that is not ends up
- *              with rows of either token)
+ *              nothing of it is written.  Slots of a call must be distinct (the rows of one that is
+ *              not are a mixture of the tokens'; nothing else is touched)
  *   pos_dev    int32 positions: one a token [T] (axis_pairs NULL), or three axes (e.g. time, height, width)
  *              [3][pos_stride], pos_stride >= T: the first axis_pairs[0] pairs turn by the first,
  *              the next axis_pairs[1] by the second, the last axis_pairs[2] by the third; axis_pairs

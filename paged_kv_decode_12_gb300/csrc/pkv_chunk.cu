@@ -15,9 +15,9 @@
 // that attend to one get NaN in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us
 // where 259 were without.)
 //
-// What bounds it is the way from a half tile's scores to its weights and back: 2048 tokens behind 14000 take 228 us (1107
+// What bounds it is the way from a half tile's scores to its weights and back: 2048 tokens behind 14000 take 225 us (1120
 // TFLOP/s, where a large product does 1964), with the tensor pipe and the special-function pipe half busy each; FP8
-// pages, whose codes are converted and whose scales go to scores and weights, 342.  16 prompts of 2048 221, FP8 about 400.
+// pages, whose codes are converted and whose scales go to scores and weights, 340.  16 prompts of 2048 196, FP8 382.
 #include <cmath>
 
 #include "pkv_chunk_run.cuh"
@@ -45,7 +45,8 @@ struct TileRun {
     static constexpr int kThreads = (FP8 ? kPreparer + kPreparers : kPreparer) * 32;
     static constexpr int kConsumers = FP8 ? 8 + 3 + kPreparers : 8 + 3;
     static constexpr bool kSingles = false;
-    static constexpr int kLeast = 32;  // of a CTA's run (64 tokens behind 2000: 23 us; at 64 eighths 25, at 16 24; 200 behind 500: 21, 30, 21)
+    // Of a CTA's run (64 tokens behind 2000 23 us, 200 behind 500 21; at 64 eighths 25 and 30, at 16 24 and 21).
+    static constexpr int kLeast = 32;
     // in eighths of the time of a BF16 key tile of two row tiles; what an item costs besides: 24 (18: 16 prompts of 2048
     // 203 us, 30: 194, where this takes 196, but 33 tokens behind 500, cut then, 18 where 15), FP8 38 (30: 395, this 381)
     static __device__ __forceinline__ Costs costs()

@@ -250,14 +250,11 @@ BIG = [
 ]
 
 
-@pytest.mark.parametrize("kv", KV)
-@pytest.mark.parametrize("case", range(len(BIG)))
-def test_large_batches(kv, case):
+def check_on_gpu(kv, sizes, window, sinks, case):
     """Long and many sequences: every output row against attention in 64 bits on the GPU.  The bound is
     ``chunk_helpers.attend``'s with the weights' part summed in closed form: off = 2 * 2^-8 * sum p |v| for the
     rounded weights and their sum, 2^-8 |out| for the output, 2^-12 sum p |v| for the scores (|s| < 2^7, off by
     at most 2^-18 of the products' absolute sum, itself below 2^6 here, as is checked)."""
-    sizes, window, sinks = BIG[case]
     rng = np.random.default_rng(case)
     lens = np.array([c + n for c, n in sizes])
     need = -(-lens // PS)
@@ -306,6 +303,25 @@ def test_large_batches(kv, case):
             bad = ~((out[starts[b]:starts[b + 1], h].double() - want).abs() <= off)
             assert not bad.any(), (b, h, bad.nonzero()[:4].tolist())
     pkv.pkv_pool_destroy(pool)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("case", range(len(BIG)))
+def test_large_batches(kv, case):
+    check_on_gpu(kv, *BIG[case], case)
+
+
+@pytest.mark.parametrize("kv", KV)
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(kv, seed):
+    """Batches of 1 to 60 sequences: chunks, single tokens and nothing, fresh and continued, with and without windows."""
+    r = np.random.default_rng(1000 + seed)
+    B = int(np.exp(r.uniform(0, np.log(60))))
+    cached = np.exp(r.uniform(0, np.log(4000), B)).astype(int) * (r.random(B) < 0.8)
+    new = np.where(r.random(B) < r.random(), 1, np.exp(r.uniform(0, np.log(600), B)).astype(int)) * (r.random(B) < 0.9)
+    new[int(r.integers(0, B))] += 1
+    window = int(np.exp(r.uniform(0, np.log(1500)))) if r.random() < 0.5 else 0
+    check_on_gpu(kv, list(zip(cached.tolist(), new.tolist())), window, int(r.integers(0, 200)) if window else 0, seed)
 
 
 @pytest.mark.parametrize("kv", KV)
