@@ -219,3 +219,18 @@ def test_on_another_stream(kv, rope):
     c = Case(kv, 60, 13)
     assert c.run(rope, stream=torch.cuda.Stream()) == 0
     c.check()
+
+
+@pytest.mark.parametrize("kv", KV)
+def test_one_slot_twice_touches_nothing_else(kv, rope):
+    pools = []
+    for twice in (True, False):
+        c = Case(kv, 40, 77)
+        place = int(c.slots[0])
+        c.slots[:2] = place if twice else -1
+        assert c.run(rope) == 0
+        c.cache.host[:] = c.cache.download()
+        c.cache.put(place // PS, place % PS, np.ones((HKV, D)), np.ones((HKV, D)))
+        pools.append(c.cache.host.copy())
+        c.cache.close()
+    assert np.array_equal(*pools)

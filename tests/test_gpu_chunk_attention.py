@@ -349,3 +349,14 @@ def test_same_bits_without_programmatic_launches(kv):
         b.call(options=pkv.PKV_STEP_NO_PDL)
     assert b.flag() == 0 and torch.equal(b.out, first)
     b.check(rows=range(0, 41, 7)).close()
+
+
+@pytest.mark.parametrize("kv", KV)
+def test_pages_that_sequences_share(kv):
+    """Two sequences behind the same first pages, one of which is also named twice by one table."""
+    b = ch.Batch(kv, [(100, 40), (100, 1), (90, 17)], seed=51)
+    b.bt[1, :6] = b.bt[0, :6]
+    b.bt[2, 1] = b.bt[2, 0]
+    b.upload().call()
+    assert b.flag() == 0
+    b.check().close()
