@@ -855,7 +855,7 @@ struct Softmax {
                 store_rows(live, reinterpret_cast<uint4 *>(a.part_o + at * kD) + 8 * q2, kGroup * kD / 4, kD / 4);
             }
             if (lane / kGroup < live)
-                __stcg(a.part_ml + at + lane, make_float2(bad ? INFINITY : m, l));
+                __stcg(a.part_ml + at + lane, bad ? bad_part() : make_float2(m, l));
             bool last;
             if (!draw_ticket(x, last))
                 return false;
@@ -884,12 +884,17 @@ struct Softmax {
             return;
         const int w0 = (warp & 3) * 32, last = x.parts - 1;
         float M = -INFINITY;  // of row `lane`
+        bool bad = false;
 #pragma unroll 1
         for (int i = 0; i < x.parts; i += 4) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                M = fmaxf(M, __ldcg(a.part_ml + part_rows(x, min(i + k, last), s) + w0 + lane).x);
+            for (int k = 0; k < 4; ++k) {
+                const float2 ml = __ldcg(a.part_ml + part_rows(x, min(i + k, last), s) + w0 + lane);
+                M = fmaxf(M, ml.x);
+                bad |= is_bad_part(ml.y);
+            }
         }
+        const unsigned zeros = __ballot_sync(kFull, bad);
 #pragma unroll 1
         for (int k0 = 0; k0 < 16; k0 += 8) {
             float l = 0.f;
@@ -912,8 +917,10 @@ struct Softmax {
                 }
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const bool none = ml[n].x == -INFINITY || i + n > last;  // (and then nothing may be wrong with it)
-                    const float f = none ? -1.f : ex2_approx(ml[n].x - M);
+                    // (a part without scores counts nothing; one whose scores are not numbers has no maximum either,
+                    // and its sums, which are not numbers, go on.  The last part again, where there is no other, is left out.)
+                    const bool none = i + n > last;
+                    const float f = none ? -1.f : ml[n].x == -INFINITY ? 0.f : ex2_approx(ml[n].x - M);
                     l = none ? l : fmaf(f, ml[n].y, l);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -931,9 +938,9 @@ struct Softmax {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
                 const int row = 2 * (k0 + k) + lane / 16;
-                const float g = __shfl_sync(kFull, inv, row), top = __shfl_sync(kFull, M, row);
+                const float g = __shfl_sync(kFull, inv, row);
                 uint2 v = make_uint2(pack_bf16x2(o[k].x * g, o[k].y * g), pack_bf16x2(o[k].z * g, o[k].w * g));
-                if (top == INFINITY)
+                if (zeros >> row & 1u)
                     v = make_uint2(0, 0);
                 if (row / kGroup < live)
                     *reinterpret_cast<uint2 *>(a.out + rows_at(x) + row / kGroup * kTokenRow + row % kGroup * kD +

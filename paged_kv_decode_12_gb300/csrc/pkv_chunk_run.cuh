@@ -371,6 +371,11 @@ struct Feed {
 
 inline bool chunk_args_ok(int B, int T) { return B >= 1 && B <= kMaxRows && T >= 1 && T <= INT32_MAX / 16; }
 
+// A row's (m, l) of a part with a bad page id: what no scores make (l is a sum of weights; m becomes +inf by itself
+// where a score is).
+__device__ __forceinline__ float2 bad_part() { return make_float2(-INFINITY, -1.f); }
+__device__ __forceinline__ bool is_bad_part(float l) { return l < 0.f; }
+
 // Sums and rounded quotients: nothing attended to is zeros, something not finite stays so.
 __device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 

@@ -201,17 +201,21 @@ struct Team {
             const size_t at = part_rows(z, z.me) + warp;
             __stcg(reinterpret_cast<float2 *>(a.part_o + at * kD) + lane, make_float2(o0, o1));
             if (lane == 0)
-                __stcg(a.part_ml + at, make_float2(bad ? INFINITY : M, l));
+                __stcg(a.part_ml + at, bad ? bad_part() : make_float2(M, l));
             if (!draw_ticket(z, write))
                 return false;
             if (write) {
                 M = -INFINITY;
-                for (int i = lane; i < z.parts; i += 32)
-                    M = fmaxf(M, __ldcg(a.part_ml + part_rows(z, i) + warp).x);
+                bad = false;
+                for (int i = lane; i < z.parts; i += 32) {
+                    const float2 ml = __ldcg(a.part_ml + part_rows(z, i) + warp);
+                    M = fmaxf(M, ml.x);
+                    bad |= is_bad_part(ml.y);
+                }
 #pragma unroll
                 for (int off = 16; off; off >>= 1)
                     M = fmaxf(M, __shfl_xor_sync(kFull, M, off));
-                bad = M == INFINITY;
+                bad = __any_sync(kFull, bad);
                 l = o0 = o1 = 0.f;
 #pragma unroll 8
                 for (int i = 0; i < z.parts; ++i) {
