@@ -208,7 +208,8 @@ struct Fp8MmaWarpOf {
             qt[0][j] = t1;
             qt[1][j] = t2;
         }
-        const float hfac = gid < kGroup ? scale_log2 * undo : 0.f;
+        // (the terms of an infinite entry saturate: the factor makes the head's scores infinite, with their signs)
+        const float hfac = gid < kGroup ? scale_log2 * (amax < INFINITY ? undo : INFINITY) : 0.f;
         hf[0] = __shfl_sync(kFull, hfac, 8 * tig);      // lanes 4h.. hold head h
         hf[1] = __shfl_sync(kFull, hfac, 8 * tig + 4);
 #pragma unroll
