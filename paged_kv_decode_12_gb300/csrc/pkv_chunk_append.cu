@@ -203,14 +203,15 @@ __device__ __forceinline__ float row_scale8(const float (&x1)[4], const float (&
 
 // E4M3 codes of x / scale, the quotient as FP32 division rounds it: from the rounded reciprocal, one step with
 // the remainder gives the rounded quotient (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990).  A scale whose reciprocal leaves the range takes the division.
+// System/6000 processor", 1990).  (The remainder with its sign turned: one of nothing is then -0 in the step, and a
+// quotient of -0 stays one.)  A scale whose reciprocal leaves the range takes the division.
 __device__ __forceinline__ uint32_t codes4(const float (&x)[4], float scale, float inv)
 {
     float q[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float y = __fmul_rn(x[i], inv);
-        q[i] = __fmaf_rn(__fmaf_rn(-y, scale, x[i]), inv, y);
+        q[i] = __fmaf_rn(-__fmaf_rn(y, scale, -x[i]), inv, y);
     }
     if (!(scale >= 0x1p-100f && scale <= 0x1p100f)) {
 #pragma unroll
