@@ -699,10 +699,10 @@ int pkv_chunk_append(const pkv_pool *pool, const uint16_t *k, int64_t k_stride, 
  * Results are the same from run to run; in another batch they may differ by rounding.
  * What is not attended to has no effect, whatever is there (NaN included).
  * Launch: programmatic dependent launch, everything read behind the dependency wait.
- * Device checks: starts that decrease or leave [0, T], a sequence shorter than its new tokens or longer
- * than its table set PKV_DEVERR_LENGTH; a page id outside the pool PKV_DEVERR_PAGE_RANGE.  Outputs of
- * the tokens concerned are zeros (of a bad page: those of the tokens that are worked on together
- * with one that attends to it; tokens that starts places nowhere have none). */
+ * Device checks: starts that do not begin at 0, decrease or leave [0, T], a sequence shorter than its new
+ * tokens or longer than its table set PKV_DEVERR_LENGTH; a page id outside the pool PKV_DEVERR_PAGE_RANGE.
+ * Outputs of the tokens concerned are zeros: for starts all T rows, of a bad page those of the tokens that are
+ * worked on together with one that attends to it. */
 int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, const int32_t *bt_dev, int max_blocks,
                         const int32_t *seq_lens_dev, const int32_t *starts_dev, int B, int T, float scale, int window,
                         int sinks, void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *dev_err_flag,

@@ -108,7 +108,7 @@ struct Row {
     bool ok;
 };
 
-// Sequence b; not ok if its tokens or its length are out of range.
+// Sequence b; not ok if its tokens are out of range.
 __device__ __forceinline__ Row row_of(const ChunkArgs &a, int b)
 {
     Row x;
@@ -137,7 +137,9 @@ __device__ __forceinline__ int64_t row_cost(const ChunkArgs &a, const Row &x, co
     return plan::row_cost<int64_t>(x.n, x.L, a.window, a.sinks, k, Run::kSingles);
 }
 
-// All threads: the prefix sums of the sequences' costs, the rows that are refused.
+// All threads: the prefix sums of the sequences' costs, the rows that are refused.  Starts that are no prefix sums (from
+// 0 on, none below the one before, T at most) say nothing about whose a token is, and two sequences may name the same:
+// then nothing is worked on and every row is zeros.
 template <class Run, class Shared>
 __device__ __forceinline__ void make_plan(const ChunkArgs &a, Shared &sh)
 {
@@ -145,13 +147,13 @@ __device__ __forceinline__ void make_plan(const ChunkArgs &a, Shared &sh)
     const int per = (a.B + Run::kThreads - 1) / Run::kThreads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t sum = 0;
-    bool bad = threadIdx.x == 0 && a.starts[0] != 0;
+    bool bad = false, no_starts = threadIdx.x == 0 && a.starts[0] != 0;
     for (int i = 0; i < per; ++i) {
         const int b = threadIdx.x * per + i;
         if (b >= a.B)
             break;
         const Row x = row_of(a, b);
-        bad |= !x.ok;
+        no_starts |= !x.ok;
         if (x.n && !length_fits(a, x)) {  // zeros; the CTAs share the tokens
             bad = true;
             for (int t = blockIdx.x; a.refuses && t < x.n; t += gridDim.x)
@@ -167,14 +169,24 @@ __device__ __forceinline__ void make_plan(const ChunkArgs &a, Shared &sh)
         if (lane >= off)
             upto += y;
     }
+    no_starts = __any_sync(kFull, no_starts);
     if (lane == 31)
-        sh.warp_sums[warp] = upto;
-    bad = __syncthreads_or(bad);
+        sh.warp_sums[warp] = no_starts ? -1 : upto;
+    bad = __syncthreads_or(bad || no_starts);
     int64_t before = upto - sum, all = 0;
+    no_starts = false;
     for (int w = 0; w < Run::kThreads / 32; ++w) {
+        const int64_t of = sh.warp_sums[w];
         if (w < warp)
-            before += sh.warp_sums[w];
-        all += sh.warp_sums[w];
+            before += of;
+        all += of;
+        no_starts |= of < 0;
+    }
+    if (no_starts) {  // (all threads of all CTAs alike)
+        all = 0;
+        const int64_t words = (int64_t)a.T * (kTokenRow / 8), threads = (int64_t)gridDim.x * Run::kThreads;
+        for (int64_t i = blockIdx.x * (int64_t)Run::kThreads + threadIdx.x; a.refuses && i < words; i += threads)
+            reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
     }
     sh.sums[threadIdx.x] = before;
     if (threadIdx.x == 0) {
