@@ -1014,6 +1014,11 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ C
         fence_proxy_async_smem();
     }
     grid_dependency_wait();
+    if (a.apart && blockIdx.x == 0) {  // (see launch_singles)
+        if (threadIdx.x == 0)
+            asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(a.arrived), "r"(1) : "memory");
+        __syncthreads();
+    }
     allow_dependent_launch();
     make_plan<TileRun<FP8>>(a, sh);
     tc::fence_before();
@@ -1052,7 +1057,7 @@ chunk_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ C
         tc::dealloc<kCols>(tmem);
 }
 
-// Workspace: the tile kernel's tickets and partials, then the single tokens'.
+// Workspace: the tile kernel's tickets and `arrived`, its partials, then the single tokens' own.
 struct ChunkWorkspace {
     size_t tickets, ml, o;
     size_t singles() const { return tickets + ml + o; }
@@ -1062,7 +1067,7 @@ struct ChunkWorkspace {
 ChunkWorkspace chunk_workspace()
 {
     ChunkWorkspace w;
-    w.tickets = align256((size_t)kSms * 2 * sizeof(int));
+    w.tickets = align256(((size_t)kSms * 2 + 1) * sizeof(int));
     w.ml = align256((size_t)kSms * 4 * kRowTile * sizeof(float2));
     w.o = (size_t)kSms * 4 * kRowTile * kD * sizeof(float);
     return w;
@@ -1132,6 +1137,7 @@ extern "C" int pkv_chunk_attention(const pkv_pool *pool, const uint16_t *q, cons
     a.out = out;
     a.err = dev_err_flag;
     a.tickets = static_cast<int *>(workspace);
+    a.arrived = a.tickets + kSms * 2;
     a.part_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + ws.tickets);
     a.part_o = reinterpret_cast<float *>(static_cast<char *>(workspace) + ws.tickets + ws.ml);
     a.expire = (options & PKV_STEP_TEST_EXPIRE_WAIT) ? 1 : 0;

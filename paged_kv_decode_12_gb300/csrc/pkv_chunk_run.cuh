@@ -35,6 +35,7 @@ struct ChunkArgs {
     uint16_t *out;
     int32_t *err;
     int *tickets;    // [CTA][2] of cut items that begin there, zero between launches
+    int *arrived;    // what came before this call's first kernel has ended; zero between calls (see launch_singles)
     float2 *part_ml; // partials of cut items: (m, l), and O, of [CTA][went on, begun][rows]
     float *part_o;
     int expire;      // testing aid (PKV_STEP_TEST_EXPIRE_WAIT)
@@ -409,8 +410,13 @@ inline SingleWorkspace single_workspace()
     return w;
 }
 
-// The sequences that bring one token, by a kernel of their own; `follows`: behind the kernel of the others, which has
-// waited for what came before (its refused rows are dealt with there).
+// The sequences that bring one token, by a kernel of their own; `follows`: behind the kernel of the others, beside which
+// it runs (refused rows are dealt with there).  It begins when the other's CTAs have waited for what came before,
+// lengths, queries and pages among it.  Of a launch that another one waited for, the programming model promises nothing to
+// a grid that does not wait itself; so the other's first CTA hands its wait on: a release store to `arrived` before it
+// lets this kernel begin, which every CTA here acquires.  A CTA that finds nothing there waits for the other kernel
+// itself.  This kernel's first CTA does that at its end in any case, because what comes behind waits for this kernel
+// alone, and takes the mark back then: CTAs that begin later have nothing left to wait for.
 int launch_singles(const pkv_pool *pool, ChunkArgs a, void *workspace, cudaStream_t s, bool pdl, bool follows);
 
 }  // namespace chunk

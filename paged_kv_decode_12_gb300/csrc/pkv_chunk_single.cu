@@ -35,6 +35,7 @@ struct SingleShared : RunShared {
     uint64_t here[kTeam][8];  // a warp's place holds a page
     uint64_t group;           // times the warps have met
     int last, bad;            // this CTA finished the item last; the last item with a bad page id
+    int arrived;              // the other sequences' kernel has handed its wait on
     alignas(16) float states[kTeam][kStateFloats];
     int64_t sums[(kTeam + 1) * 32];
 };
@@ -270,15 +271,19 @@ single_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ 
         sh.bad = -1;
         sh.taken[0][0] = sh.taken[1][0] = 0;
         fence_barrier_init();
+        if (follows)
+            asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(sh.arrived) : "l"(a.arrived) : "memory");
     }
-    // Behind the kernel of the other sequences this one begins beside it: what came before that has ended, because
-    // its CTAs let this one begin after their own wait; what comes behind waits for this kernel, whose first CTA
-    // therefore ends after it.
     if (!follows) {
         grid_dependency_wait();
         allow_dependent_launch();
     }
     __syncthreads();
+    if (follows) {  // (see launch_singles)
+        if (!sh.arrived)
+            grid_dependency_wait();
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // (pages are read by copies)
+    }
     make_plan<Run>(a, sh);
     __syncthreads();
     if (warp == kTeam)
@@ -291,8 +296,11 @@ single_kernel(const __grid_constant__ CUtensorMap tmap, const __grid_constant__ 
         if ((threadIdx.x & 31) == 0 && a.err)
             atomicOr(a.err, PKV_DEVERR_TIMEOUT);
     }
-    if (follows && blockIdx.x == 0)
+    if (follows && blockIdx.x == 0) {
         grid_dependency_wait();
+        if (threadIdx.x == 0)
+            *a.arrived = 0;
+    }
 }
 
 template <bool FP8>
