@@ -138,6 +138,14 @@ __device__ __forceinline__ int64_t row_cost(const ChunkArgs &a, const Row &x, co
     return plan::row_cost<int64_t>(x.n, x.L, a.window, a.sinks, k, Run::kSingles);
 }
 
+// All rows zeros.  (Out of line: within the plan, 16 prompts of 2048 took 203.6 us where this takes 200.8.)
+static __device__ __noinline__ void refuse_all(uint16_t *out, int T)
+{
+    const int64_t words = (int64_t)T * (kTokenRow / 8), threads = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < words; i += threads)
+        reinterpret_cast<uint4 *>(out)[i] = make_uint4(0, 0, 0, 0);
+}
+
 // All threads: the prefix sums of the sequences' costs, the rows that are refused.  Starts that are no prefix sums (from
 // 0 on, none below the one before, T at most) say nothing about whose a token is, and two sequences may name the same:
 // then nothing is worked on and every row is zeros.
@@ -185,9 +193,8 @@ __device__ __forceinline__ void make_plan(const ChunkArgs &a, Shared &sh)
     }
     if (no_starts) {  // (all threads of all CTAs alike)
         all = 0;
-        const int64_t words = (int64_t)a.T * (kTokenRow / 8), threads = (int64_t)gridDim.x * Run::kThreads;
-        for (int64_t i = blockIdx.x * (int64_t)Run::kThreads + threadIdx.x; a.refuses && i < words; i += threads)
-            reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0, 0, 0, 0);
+        if (a.refuses)
+            refuse_all(a.out, a.T);
     }
     sh.sums[threadIdx.x] = before;
     if (threadIdx.x == 0) {
