@@ -54,6 +54,7 @@ from . import workloads as wl
 
 class DecodeEngine:
     _device_tables = False  # chunk_tables has run (or is in a graph): bt is ahead of bt_host
+    _room = {}              # by layer: pages that evict took for tokens to come (replaced, never changed)
 
     def __init__(self, num_pages: int, layers: int, batch: int, max_blocks: int = wl.MAX_BLOCKS,
                  pages_per_chunk: int = 16, variant: int = pkv.PKV_DECODE_DEFAULT, max_pos: int = wl.MAX_CONTEXT,
@@ -146,6 +147,9 @@ class DecodeEngine:
         """The block tables of all layers.  New ones take the old ones' place on the device, where
         captured graphs read them, once the work in flight is done."""
         assert bt_host.shape == (self.layers, self.batch, self.max_blocks)
+        if self._device_tables and self._room:
+            self.read_tables()
+        self._room = {}
         self.bt_host = np.ascontiguousarray(bt_host, dtype=np.int32)
         if self.bt is None:
             self.bt = torch.empty(self.bt_host.shape, dtype=torch.int32, device=self.device)
@@ -492,6 +496,8 @@ class DecodeEngine:
         them, and the old pages given back (work on the stream so far still reads them; later work on it
         comes behind).  Returns the lengths after it.  Keep ``seq_lens`` and the table of all layers in
         step: each layer is cut by its own call with the same arguments.
+        The room's pages are the engine's to give back, with the next eviction or where ``chunk_tables`` has
+        put others in their place.
         A row names all of its sequence's pages (a ValueError otherwise: it need not for
         ``attention_shared`` or behind a window); rows may share some (a prefix), and no longer do
         after it.  Every page must be the caller's to give back (allocated, and not a scheduler's:
@@ -537,18 +543,33 @@ class DecodeEngine:
         pkv.pkv_pool_free(self.pool, old)
         self.bt_host = self.bt_host.copy()  # (the caller may hold the old tables)
         self.bt_host[layer] = dst
+        held = (after + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
+        self._room = {**self._room, layer: dst[(np.arange(self.max_blocks)[None, :] >= held[:, None]) & (dst >= 0)]}
         return after
 
     # ------------------------------------------------------------------ chunks of new tokens
     def take_pages(self, n: int) -> torch.Tensor:
         """``n`` pages of the pool as a list for ``chunk_tables`` (int32, on the device)."""
-        return torch.from_numpy(pkv.pkv_pool_alloc(self.pool, n)).to(self.device)
+        ids = pkv.pkv_pool_alloc(self.pool, n)
+        # (the caller's from here on, also where one was an eviction's room that somebody has given back)
+        self._room = {layer: room[~np.isin(room, ids)] for layer, room in self._room.items()}
+        return torch.from_numpy(ids).to(self.device)
 
     def read_tables(self, stream=None) -> np.ndarray:
         """``bt_host`` from the device, where ``chunk_tables`` extends the tables, once the work on the
-        stream is done."""
+        stream is done.  Pages of an eviction's room that no table names any more go back to the pool."""
         with torch.cuda.stream(self._on(stream)):
             self.bt_host = self.bt.cpu().numpy()
+        for layer, room in self._room.items():
+            gone = ~np.isin(room, self.bt_host)
+            self._room = {**self._room, layer: room[~gone]}
+            for page in room[gone]:
+                try:
+                    pkv.pkv_pool_free(self.pool, [page])
+                except pkv.PkvError as e:
+                    # (somebody has given it back already, and it is free or a scheduler's)
+                    if e.status not in (pkv.PKV_ERR_DOUBLE_FREE, pkv.PKV_ERR_INVALID_ARG):
+                        raise
         return self.bt_host
 
     def _device_arrays(self, **arrays) -> None:
@@ -562,9 +583,10 @@ class DecodeEngine:
         """pkv_chunk_tables of all layers: sequence b, of seq_lens[b] tokens, brings new[b]; the pages come
         from ``pages_dev``, of which the first ``used_dev`` are taken.  Written: ``starts`` [batch + 1],
         ``pos`` [T], ``slots`` int64 [layers][T] for T tokens at most, the lengths and the count of taken
-        pages (in place by default).  Pages that a row names behind its sequence's last one (``build_tables``
-        for more tokens, the ``room`` of ``evict``) are replaced.  The engine has tables before (``set_tables``: -1 everywhere for
-        sequences without pages)."""
+        pages (in place by default).  Pages that a row names behind its sequence's last one are replaced: those of
+        the ``room`` of ``evict`` go back to the pool with the next ``read_tables`` or ``evict``; those of
+        ``build_tables`` for more tokens stay with the caller, who has its tables.  The engine has tables
+        before (``set_tables``: -1 everywhere for sequences without pages)."""
         seq_lens_out = seq_lens_dev if seq_lens_out is None else seq_lens_out
         used_out = used_dev if used_out is None else used_out
         B, T, i32 = self.batch, pos.numel(), torch.int32
