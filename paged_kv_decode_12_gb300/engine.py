@@ -79,6 +79,7 @@ class DecodeEngine:
         self.scale = 1.0 / math.sqrt(wl.HEAD_DIM)
         self.page_bytes = pkv.PKV_PAGE_BYTES_FP8 if kv == "fp8" else pkv.PKV_PAGE_BYTES
         self.slab = torch.empty(num_pages * self.page_bytes, dtype=torch.uint8, device=self.device)
+        self.device = self.slab.device  # (with its index: what is on another GPU is refused)
         if kv == "fp8":
             self.pool = pkv.pkv_pool_create_fp8(self.slab, self.slab.numel(), seed=pool_seed)
         else:
@@ -438,7 +439,7 @@ class DecodeEngine:
     def _acc_stride(self, *accs) -> int:
         for acc in accs:
             if (acc.dtype != torch.float32 or acc.shape != accs[0].shape or not acc.is_contiguous() or
-                    acc.device.type != self.device.type or acc.dim() != 3 or
+                    acc.device != self.device or acc.dim() != 3 or
                     acc.shape[:2] != (self.batch, wl.NUM_KV_HEADS)):
                 raise ValueError("weights: float32 [batch][8][n], contiguous, on the engine's device")
         return acc.shape[-1]
@@ -467,7 +468,7 @@ class DecodeEngine:
         ppc = self.pages_per_chunk if pages_per_chunk is None else pages_per_chunk
         groups = prefix_pages_dev.numel()
         for t, n in ((group_starts_dev, groups + 1), (prefix_pages_dev, max(groups, 1))):
-            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device.type != self.device.type:
+            if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous() or t.device != self.device:
                 raise ValueError("groups: int32, contiguous, on the engine's device; n + 1 starts for n prefixes")
         args = (self.batch, self.max_blocks, groups, max_prefix_pages, ppc, prefix_pages_per_chunk)
         nbytes = pkv.pkv_decode_shared_workspace_bytes(*args)
@@ -575,7 +576,7 @@ class DecodeEngine:
     def _device_arrays(self, **arrays) -> None:
         for name, (t, dtype, shape) in arrays.items():
             if (t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous() or
-                    t.device.type != self.device.type):
+                    t.device != self.device):
                 raise ValueError(f"{name}: {dtype} {tuple(shape)}, contiguous, on the engine's device")
 
     def chunk_tables(self, seq_lens_dev, new_dev, pages_dev, used_dev, starts, pos, slots, seq_lens_out=None,
@@ -614,7 +615,7 @@ class DecodeEngine:
         q_out = q if q_out is None else q_out
         for name, x, heads in (("k", k, wl.NUM_KV_HEADS), ("v", v, wl.NUM_KV_HEADS), ("q", q, wl.NUM_Q_HEADS),
                                ("q_out", q_out, wl.NUM_Q_HEADS)):
-            if (x.dtype != torch.bfloat16 or tuple(x.shape) != (T, heads, wl.HEAD_DIM) or x.device.type != self.device.type or
+            if (x.dtype != torch.bfloat16 or tuple(x.shape) != (T, heads, wl.HEAD_DIM) or x.device != self.device or
                     x.stride()[1:] != (wl.HEAD_DIM, 1)):
                 raise ValueError(f"{name}: bfloat16 [T][{heads}][{wl.HEAD_DIM}], a token's heads together, on the engine's device")
         self._device_arrays(slots=(slots, torch.int64, (T,)),

@@ -135,3 +135,61 @@ def test_new_tables_end_the_bookkeeping(eng):
     before = free(eng)
     eng.read_tables()
     assert free(eng) == before
+
+
+class Elsewhere(torch.Tensor):
+    """A tensor that says it is on some device."""
+
+    @staticmethod
+    def on(t, device):
+        t = t.as_subclass(Elsewhere)
+        t.where = torch.device(device)
+        return t
+
+    @property
+    def device(self):
+        return self.where
+
+
+def test_arrays_on_another_gpu_are_refused(bare, monkeypatch):  # noqa: F811
+    bare.device, here, there = torch.device("cuda:0"), "cuda:0", "cuda:1"
+    bare.layers, bare.batch, bare.max_blocks, bare.bt, bare.err = 1, 2, 4, torch.zeros((1, 2, 4), dtype=torch.int32), None
+    bare.scale, bare.window, bare.sinks, bare.step_options, bare.rope, bare.max_pos = 0.125, 0, 0, 0, None, 64
+    bare.pages_per_chunk = 4
+    monkeypatch.setattr(bare, "_workspace", lambda *a: None)
+    called = []
+    for name in ("pkv_chunk_tables", "pkv_chunk_append", "pkv_chunk_attention", "pkv_decode_shared"):
+        monkeypatch.setattr(pkv, name, lambda *a, name=name: called.append(name))
+
+    def i32(*shape):
+        return torch.zeros(shape, dtype=torch.int32)
+
+    def bf16(*shape):
+        return torch.zeros(shape, dtype=torch.bfloat16)
+
+    calls = {
+        "chunk_tables": dict(seq_lens_dev=i32(2), new_dev=i32(2), pages_dev=i32(5), used_dev=i32(1), starts=i32(3), pos=i32(7),
+                             slots=torch.zeros((1, 7), dtype=torch.int64), seq_lens_out=i32(2), used_out=i32(1)),
+        "chunk_append": dict(k=bf16(7, 8, 64), v=bf16(7, 8, 64), q=bf16(7, 32, 64), slots=torch.zeros(7, dtype=torch.int64),
+                             pos=i32(7), q_out=bf16(7, 32, 64), q_norm=bf16(64), k_norm=bf16(64)),
+        "chunk_attention": dict(q=bf16(7, 32, 64), seq_lens_dev=i32(2), starts=i32(3), out=bf16(7, 32, 64)),
+    }
+    for call, arrays in calls.items():
+        def run(at):
+            args = {x: Elsewhere.on(t, at.get(x, here)) for x, t in arrays.items()}
+            getattr(bare, call)(**(dict(args, layer=0) if call == "chunk_attention" else args))
+
+        run({})
+        assert called.pop() == "pkv_" + call
+        for x in arrays:
+            with pytest.raises(ValueError):
+                run({x: there})
+            assert not called, x
+    acc = torch.zeros(2, 8, 64)
+    assert bare._acc_stride(Elsewhere.on(acc, here)) == 64
+    with pytest.raises(ValueError):
+        bare._acc_stride(Elsewhere.on(acc, there))
+    for starts, prefix in ((there, here), (here, there)):
+        with pytest.raises(ValueError):
+            bare.attention_shared(0, None, None, Elsewhere.on(i32(2), starts), Elsewhere.on(i32(1), prefix), 2, None)
+    assert not called
