@@ -155,32 +155,18 @@ struct RowScales {
 };
 
 // Which of a row's 64 scores of half a key tile count; drop() replaces those of pair i of columns
-// 32 k .. that do not.  kScalesToo: places whose scales may be anything (NaN included).
+// 32 k .. that do not.
 struct EveryColumn {
-    static constexpr bool kScalesToo = false;
     __device__ __forceinline__ void drop(int, int, float2 &, float) const {}
 };
 
 // The first `pages` pages of the tile.
 struct FirstPages {
-    static constexpr bool kScalesToo = false;
     int pages;
     __device__ __forceinline__ void drop(int k, int i, float2 &x, float to) const
     {
         if (!(k * 4 + i / 4 < pages))
             x = make_float2(to, to);
-    }
-};
-
-// Any of them: bit j of w[k] is column 32 k + j.
-struct ColumnBits {
-    static constexpr bool kScalesToo = true;
-    uint32_t w0, w1;
-    __device__ __forceinline__ void drop(int k, int i, float2 &x, float to) const
-    {
-        const uint32_t w = k ? w1 : w0;
-        x.x = w & (1u << (2 * i)) ? x.x : to;
-        x.y = w & (2u << (2 * i)) ? x.y : to;
     }
 };
 
@@ -212,14 +198,9 @@ __device__ __forceinline__ float make_weights(uint32_t ts, int k, const Scale &s
             tc::fma2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i), m2);
         float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
         mask.drop(k, i, e, 0.f);
-        float2 p = sc.weight(k * 16 + i, e);
-        if constexpr (Mask::kScalesToo)
-            mask.drop(k, i, p, 0.f);
+        const float2 p = sc.weight(k * 16 + i, e);
         pk[i] = pack_bf16x2(p.x, p.y);
-        float2 counted = sc.counted(k * 16 + i, e, pk[i]);
-        if constexpr (Mask::kScalesToo)
-            mask.drop(k, i, counted, 0.f);
-        sum[i % 4] = tc::add2(sum[i % 4], counted);
+        sum[i % 4] = tc::add2(sum[i % 4], sc.counted(k * 16 + i, e, pk[i]));
     }
     const float2 s = tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3]));
     return s.x + s.y;
