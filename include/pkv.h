@@ -658,9 +658,9 @@ size_t pkv_chunk_tables_workspace_bytes(int B);
 
 /* Norms of the query and key heads, rotation, and append of T tokens, for one layer.  A head's row x:
  *     y = R(x * w) / sqrt(mean(x^2) + eps)    (without weights: R(x))
- * in FP32 (the number next to the exact one), rounded to BF16 (FP8 pools: key rows are then quantized as pkv_append_rope does).  R turns
- * the pairs (i, i + 32) by pos * theta^(-2i/64), from the table.  Without norms the
- * results are pkv_append_rope's bit for bit.
+ * rounded to BF16 from FP32: keys from the FP32 number next to the exact one (FP8 pools: then quantized as
+ * pkv_append_rope does), queries with norms from one within 2^-20 of it.  R turns the pairs (i, i + 32) by
+ * pos * theta^(-2i/64), from the table.  Without norms the results are pkv_append_rope's bit for bit.
  *   k, v       [T][8][64], token t at k + t * k_stride (BF16 elements, at least 512, a multiple of 4)
  *   q, q_out   [T][32][64]: rows of q at q_stride (at least 2048, a multiple of 4), q_out contiguous;
  *              q_out may be q where q_stride is 2048.  Both may be NULL
@@ -696,8 +696,14 @@ int pkv_chunk_append(const pkv_pool *pool, const uint16_t *k, int64_t k_stride, 
  *   workspace  >= pkv_chunk_attention_workspace_bytes(B, T) bytes, 16-byte aligned, zero before the FIRST
  *              call (its counters are zero after every call).  Calls sharing it must not overlap on the GPU.
  *   options    0, or PKV_STEP_NO_PDL | PKV_STEP_TEST_EXPIRE_WAIT
- * Results are the same from run to run; in another batch they may differ by rounding.
- * What is not attended to has no effect, whatever is there (NaN included).
+ * Results are the same from run to run; in another batch they may differ by rounding: weights are rounded to BF16,
+ * those of single tokens over FP8 pages, where such tokens have a kernel of their own, to FP16.
+ * Values up to 2^39 in size.  Besides rounding, an output may be off by 2^-70 for every token that its row attends
+ * to: what FP32 does not hold of products of small weights and small values (single tokens with a kernel of their
+ * own: 2^-126).
+ * What is not attended to has no effect, whatever is there (NaN included).  A row that attends to something not
+ * finite, or whose query is not, need not be finite: it is NaN if a score is NaN or +inf; an infinite value leaves
+ * its dimension infinite or NaN, and the others as they are.
  * Launch: programmatic dependent launch, everything read behind the dependency wait.
  * Device checks: starts that do not begin at 0, decrease or leave [0, T], a sequence shorter than its new
  * tokens or longer than its table set PKV_DEVERR_LENGTH; a page id outside the pool PKV_DEVERR_PAGE_RANGE.

@@ -434,6 +434,10 @@ __device__ __noinline__ float top_score(HalfRow h)
 // 14000); so it lies 2^60 above, and weights down to 2^-66 of the first ones' largest count.  (2^32
 // above: outliers among the keys move it, 305 us for 16 prompts of 2048 where 239 were.)  FP8 pages: the
 // weights are multiplied with V's scales, which may be small, so it lies at the maximum, and 2^64 moves it.
+//
+// What is 2^60 above costs is small values: the sum of a row's weights is 2^-60 (1 - 2^-8) at least, and products below
+// FP32's 2^-126, 16 tokens a step, are lost beside it: 2^-70 a token.  At the other end, weights below 2^64 (BF16: 2) of
+// the 2^24 tokens that a table holds leave room for values up to 2^39.
 template <bool FP8>
 constexpr float kAbove = FP8 ? 0.f : 60.f;
 
@@ -1073,10 +1077,13 @@ ChunkWorkspace chunk_workspace()
     return w;
 }
 
-// Whether single tokens are a kernel's of their own: where there must be some (fewer than two tokens a sequence: 4
-// sequences of up to 3000 BF16 tokens 17 us apart, 22 among the tiles; 24: 23 and 30), and in large batches.  Where
-// there need be none, the second kernel costs what finding that out takes: BF16, 2 prompts of 300 among 24 sequences
-// 46 us apart and 43 not, 8 of 700 among 64 231 and 245; FP8, whose tiles are dearer, 2 among 8 51 and 62.
+// Whether single tokens are a kernel's of their own: where there must be some (fewer than two tokens a sequence: 2 to
+// 128 sequences of up to 600 to 16000 tokens take 0.57 to 0.89 of the time among the tiles, FP8 0.31 to 0.83), and in large
+// batches.  Where there need be none, the second kernel costs what finding that out takes.  Time apart by time among the
+// tiles, 1 prompt of 300 or 2 of 700 beside single tokens of up to 600, 3000 and 16000: BF16, 16 sequences 1.12 to 1.16,
+// 1.15 to 1.16 and 0.96 to 0.98, 24 1.08 to 1.14, 1.09 to 1.17 and 0.93 to 0.96, 32 0.88 to 1.06, 1.02 to 1.04 and 0.91 to
+// 0.93, 64 0.96 to 1.02, 0.95 to 0.96 and 0.89 to 0.91; FP8, whose tiles are dearer, 4 1.02 to 1.10, 1.07 to 1.12 and 0.94 to
+// 0.97, 8 0.95 to 1.07, 0.99 to 1.04 and 0.90, 16 0.90 to 1.03, 0.89 to 0.91 and 0.76 to 0.80.
 bool apart_of(bool fp8, int B, int T) { return B >= 2 && (T < 2 * B || B >= (fp8 ? 8 : 32)); }
 
 template <bool FP8>
