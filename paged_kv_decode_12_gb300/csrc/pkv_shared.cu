@@ -98,6 +98,7 @@ constexpr int kLoader = 8, kIssuer = 9, kConverter = 12;       // warps: 2 x 4 s
 constexpr int kConverters = 4;                                 // converters
 constexpr int kOutRow = 32 * 4 + 16;                           // half an output row, padded to other banks
 constexpr int kOutSize = 2 * kRowTile * kOutRow;               // 36 KiB: of every row
+constexpr int kScales = 3 * kTilePages * kPage;                // row scales of a tile: K's, V's, 1 / V's
 constexpr int kCols = 512;                                     // tensor memory, all of it
 constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384, kColL = 448;  // + 128 / 64 / 32 / 16 for the second tile
 constexpr int kOnesSize = 16 * 128;                            // BF16 pages: 16 rows of ones, for the sums
@@ -300,6 +301,24 @@ __device__ __forceinline__ void prefix_loader(const CUtensorMap *tmap, const Pre
             (void)mbar_wait_warp(&full[i % kRing], (i / kRing) & 1);
 }
 
+// A tile's row scales, [K (times scale log2 e), V, 1 / V][half][64] in the order of the scores' columns.
+__device__ __forceinline__ void convert_scales(const uint8_t *raw, float *scales, float scale_log2, int t)
+{
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {  // thread = (page, slot)
+        const int page = t / kPage, slot = t % kPage;
+        const float f = reinterpret_cast<const float *>(raw + page * kFp8Unit + kFp8UnitCodes)[kv * kPage + slot];
+        float *to = scales + slot / 8 * 64 + page * 8 + slot % 8;
+        if (kv) {  // (a scale below 2^-100, of rows of nothing, as 2^-100: weights are counted by its inverse)
+            const float v = fabsf(f) < 0x1p-100f ? 0x1p-100f : f;
+            to[128] = v;
+            to[256] = __frcp_rn(v);
+        } else {
+            to[0] = f * scale_log2;
+        }
+    }
+}
+
 // Converters (FP8; 128 threads): raw units into a stage of the BF16 layout.  The codes become
 // BF16 as they are; the row scales go to the scores and the weights instead of the rows, so
 // that nothing is rounded here.
@@ -396,22 +415,106 @@ __device__ __forceinline__ void prefix_issuer(const PrefixArgs &a, uint8_t *stag
     }
 }
 
+// What turns 64 scores into exponents and weights into the second product's operand: one
+// factor, or (FP8) a factor and a scale for every column.
+struct OneFactor {
+    static constexpr bool kSum = false;  // the sum is made by the matrix instruction
+    float c;
+    __device__ __forceinline__ float2 factor(int) const { return make_float2(c, c); }
+    __device__ __forceinline__ float2 weight(int, float2 e) const { return e; }
+    __device__ __forceinline__ float2 counted(int, float2 e, uint32_t) const { return e; }
+};
+
+struct RowScales {
+    static constexpr bool kSum = true;
+    const float2 *k, *v, *inverse;  // 32 pairs of columns
+    __device__ __forceinline__ float2 factor(int i) const { return k[i]; }
+    __device__ __forceinline__ float2 weight(int i, float2 e) const { return tc::mul2(e, v[i]); }
+    // The weight that the product holds: what was rounded, without V's scale again.
+    __device__ __forceinline__ float2 counted(int i, float2, uint32_t p) const
+    {
+        return tc::mul2(make_float2(__uint_as_float(p << 16), __uint_as_float(p & 0xffff0000u)), inverse[i]);
+    }
+};
+
+// 32 scores of one query row (columns 32 k ..) as weights 2^(S c - m): their sum, and the weights
+// in pairs rounded to BF16 (half a step, 2^-8) for the second product: what the matrix instruction
+// takes beside BF16 values.  MASK: columns of pages from `pages` on weigh nothing.  Four chains of
+// sums, so that no chain's latency is the time of the whole.
+//
+// BF16 pages: the softmax's sum is of the weights as rounded, made by the matrix instruction too (L
+// += P 1, 16 equal columns), so that the quotient has none of their rounding where few weights make
+// it.  256 sequences behind 32768 tokens: error 0.0017 in 94 us, where the sum of the unrounded
+// weights, which this function returns, gives 0.0023 in 92, and unpacking the rounded ones took 108.
+// FP8 pages: what is rounded is the weight times V's row scale; the sum takes it times the scale's
+// inverse (error 0.0017 instead of 0.0023; 72 sequences in 5 groups 32 us instead of 31).
+template <bool MASK, class Scale>
+__device__ __forceinline__ float make_weights(uint32_t ts, int k, const Scale &sc, int pages, float m, uint32_t (&pk)[16])
+{
+    uint32_t w[32];
+    tc::ld32(ts + k * 32, w);
+    float2 sum[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        sum[i] = make_float2(0.f, 0.f);
+    const float2 m2 = make_float2(-m, -m);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 x =
+            tc::fma2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i), m2);
+        float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+        if (MASK && !(k * 4 + i / 4 < pages))
+            e = make_float2(0.f, 0.f);
+        const float2 p = sc.weight(k * 16 + i, e);
+        pk[i] = pack_bf16x2(p.x, p.y);
+        sum[i % 4] = tc::add2(sum[i % 4], sc.counted(k * 16 + i, e, pk[i]));
+    }
+    const float2 s = tc::add2(tc::add2(sum[0], sum[1]), tc::add2(sum[2], sum[3]));
+    return s.x + s.y;
+}
+
+// Their maximum, times the factors.
+template <bool MASK, class Scale>
+__device__ __forceinline__ float max_score(uint32_t ts, int k, const Scale &sc, int pages)
+{
+    uint32_t w[32];
+    tc::ld32(ts + k * 32, w);
+    float mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const float2 x = tc::mul2(make_float2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1])), sc.factor(k * 16 + i));
+        if (!MASK || k * 4 + i / 4 < pages)
+            mx = tc::max3(mx, x.x, x.y);
+    }
+    return mx;
+}
+
+// An item's first half tile: the row's maximum.  (Not inlined: the loop would pay for its
+// registers; 256 sequences behind 32768 tokens 94.5 us instead of 95.1, though 4 behind 512 tokens
+// 7.5 instead of 7.2.)
+template <class Scale>
+__device__ __noinline__ float first_reference(uint32_t ts, Scale sc, int pages)
+{
+    return fmaxf(max_score<true>(ts, 0, sc, pages), max_score<true>(ts, 1, sc, pages));
+}
+
 // Half a key tile's scores of one query row become weights, in place: P is the first half of
-// S's columns.  Returns false if a wait gave up.
-template <class Mask, class Scale>
-__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, uint32_t tl, const Scale &sc, const Mask &mask, int before,
+// S's columns.  MASK: only the first `pages` pages of the tile count.  Returns false if a wait
+// gave up.
+template <bool MASK, class Scale>
+__device__ __forceinline__ bool softmax_half(uint32_t ts, uint32_t to, uint32_t tl, const Scale &sc, int pages, int before,
                                              uint64_t *o_step, volatile int *stop, float &m, float &l)
 {
     uint32_t p0[16], p1[16];
-    float s = make_weights(ts, 0, sc, mask, m, p0) + make_weights(ts, 1, sc, mask, m, p1);
+    float s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
     const bool move = !(s < kMostWeight);
     if (__any_sync(kFull, move)) {
-        const float top = fmaxf(max_score(ts, 0, sc, mask), max_score(ts, 1, sc, mask));
+        const float top = fmaxf(max_score<MASK>(ts, 0, sc, pages), max_score<MASK>(ts, 1, sc, pages));
         const float mn = move ? fmaxf(top, m) : m;
         const float f = ex2_approx(m - mn);  // 1 where the reference stays
         m = mn;
         l *= f;
-        s = make_weights(ts, 0, sc, mask, m, p0) + make_weights(ts, 1, sc, mask, m, p1);
+        s = make_weights<MASK>(ts, 0, sc, pages, m, p0) + make_weights<MASK>(ts, 1, sc, pages, m, p1);
         // Once the product before this one is done, nothing else touches O.  (These scores came
         // after the product before that, so the wait is one phase behind at most.)
         if (!tc::wait_warp(o_step, (before - 1) & 1, stop))
@@ -518,11 +621,12 @@ __device__ __forceinline__ void prefix_softmax(const PrefixArgs &a, PrefixBars &
                 const int seq = loaded + x.order(s, j), st = seq % kStages;
                 const auto half = [&](const auto &sc) {
                     if (j == 0 && hf == 0)
-                        m = first_reference(ts, sc, FirstPages{pages});
+                        m = first_reference(ts, sc, pages);
                     return pages >= kTilePages
-                               ? softmax_half(ts + hf * kHalf, to, tl, sc, EveryColumn{}, before, &bars.o_step[s], &bars.stop, m, l)
-                               : softmax_half(ts + hf * kHalf, to, tl, sc, FirstPages{pages}, before, &bars.o_step[s], &bars.stop,
-                                              m, l);
+                               ? softmax_half<false>(ts + hf * kHalf, to, tl, sc, kTilePages, before, &bars.o_step[s], &bars.stop,
+                                                     m, l)
+                               : softmax_half<true>(ts + hf * kHalf, to, tl, sc, pages, before, &bars.o_step[s], &bars.stop, m,
+                                                    l);
                 };
                 bool go;
                 if constexpr (FP8) {
