@@ -183,15 +183,13 @@ decode_merge_kernel(const int32_t *__restrict__ seq_lens, int max_blocks, int pa
     for (int c = 0; c < nchunks; ++c)
         M = fmaxf(M, part_ml[base + c].x);
     float lsum = 0.f, o0 = 0.f, o1 = 0.f;
-    if (M != -INFINITY) {
-        for (int c = 0; c < nchunks; ++c) {
-            const float2 ml = part_ml[base + c];
-            const float f = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
-            const float2 oc = reinterpret_cast<const float2 *>(part_o + (base + c) * kD)[dp];
-            lsum = fmaf(f, ml.y, lsum);
-            o0 = fmaf(f, oc.x, o0);
-            o1 = fmaf(f, oc.y, o1);
-        }
+    for (int c = 0; c < nchunks; ++c) {
+        const float2 ml = part_ml[base + c];
+        const float f = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - M);
+        const float2 oc = reinterpret_cast<const float2 *>(part_o + (base + c) * kD)[dp];
+        lsum = fmaf(f, ml.y, lsum);
+        o0 = fmaf(f, oc.x, o0);
+        o1 = fmaf(f, oc.y, o1);
     }
     const float inv = lsum > 0.f ? 1.f / lsum : 0.f;
     reinterpret_cast<uint32_t *>(out + ((size_t)b * kHq + h) * kD)[dp] = pack_bf16x2(o0 * inv, o1 * inv);

@@ -338,7 +338,8 @@ __device__ __forceinline__ void write_zero_unit(const StepArgs &a, int b, int g)
 // Chunk counts up to which the merging unit holds every partial in registers.
 constexpr int kMergeRegs = 8;
 
-// The log-sum-exp merge, in chunk order, of a head's partials (ml_row, and o_col one dim pair).
+// The log-sum-exp merge, in chunk order, of a head's partials (ml_row, and o_col one dim pair).  A partial without
+// a maximum counts nothing; where its scores are not numbers, neither are its sums, and they go on.
 __device__ __forceinline__ void merge_partials(const float2 *ml_row, const float2 *o_col, int nchunks, float &Mx, float &ls,
                                                float &r0, float &r1)
 {
@@ -358,30 +359,26 @@ __device__ __forceinline__ void merge_partials(const float2 *ml_row, const float
         for (int cc = 0; cc < kMergeRegs; ++cc)
             if (cc < nchunks)
                 Mx = fmaxf(Mx, ml[cc].x);
-        if (Mx != -INFINITY) {
 #pragma unroll
-            for (int cc = 0; cc < kMergeRegs; ++cc)
-                if (cc < nchunks) {
-                    const float f = (ml[cc].x == -INFINITY) ? 0.f : exp2f(ml[cc].x - Mx);
-                    ls = fmaf(f, ml[cc].y, ls);
-                    r0 = fmaf(f, oc[cc].x, r0);
-                    r1 = fmaf(f, oc[cc].y, r1);
-                }
-        }
+        for (int cc = 0; cc < kMergeRegs; ++cc)
+            if (cc < nchunks) {
+                const float f = (ml[cc].x == -INFINITY) ? 0.f : exp2f(ml[cc].x - Mx);
+                ls = fmaf(f, ml[cc].y, ls);
+                r0 = fmaf(f, oc[cc].x, r0);
+                r1 = fmaf(f, oc[cc].y, r1);
+            }
     } else {
 #pragma unroll 4
         for (int cc = 0; cc < nchunks; ++cc)
             Mx = fmaxf(Mx, __ldcg(ml_row + cc).x);
-        if (Mx != -INFINITY) {
 #pragma unroll 4
-            for (int cc = 0; cc < nchunks; ++cc) {
-                const float2 ml = __ldcg(ml_row + cc);
-                const float f = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - Mx);
-                const float2 oc = __ldcg(o_col + cc * (kD / 2));
-                ls = fmaf(f, ml.y, ls);
-                r0 = fmaf(f, oc.x, r0);
-                r1 = fmaf(f, oc.y, r1);
-            }
+        for (int cc = 0; cc < nchunks; ++cc) {
+            const float2 ml = __ldcg(ml_row + cc);
+            const float f = (ml.x == -INFINITY) ? 0.f : exp2f(ml.x - Mx);
+            const float2 oc = __ldcg(o_col + cc * (kD / 2));
+            ls = fmaf(f, ml.y, ls);
+            r0 = fmaf(f, oc.x, r0);
+            r1 = fmaf(f, oc.y, r1);
         }
     }
 }
@@ -390,7 +387,7 @@ __device__ __forceinline__ void merge_partials(const float2 *ml_row, const float
 // one memory round trip for each eight instead of two for each four.
 __device__ __forceinline__ void merge_eights(const float2 *ml_row, const float2 *o_col, int n, float &ls, float &r0, float &r1)
 {
-    float M = -INFINITY;
+    float M = -3.402823466e38f;  // (a number, from which a partial without a maximum is infinitely far)
     ls = r0 = r1 = 0.f;
     for (int c0 = 0; c0 < n; c0 += 8) {
         float2 ml[8], oc[8];
@@ -407,8 +404,6 @@ __device__ __forceinline__ void merge_eights(const float2 *ml_row, const float2 
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             top = fmaxf(top, ml[i].x);
-        if (top == -INFINITY)
-            continue;
         const float keep = exp2f(M - top);
         ls *= keep;
         r0 *= keep;
