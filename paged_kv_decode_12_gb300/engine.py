@@ -149,6 +149,7 @@ class DecodeEngine:
         captured graphs read them, once the work in flight is done."""
         assert bt_host.shape == (self.layers, self.batch, self.max_blocks)
         if self._device_tables and self._room:
+            torch.cuda.synchronize(self.device)
             self.read_tables()
         self._room = {}
         self.bt_host = np.ascontiguousarray(bt_host, dtype=np.int32)
