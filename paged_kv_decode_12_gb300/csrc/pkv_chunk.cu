@@ -15,9 +15,10 @@
 // that attend to one get NaN in its dimension at the end.  (By the softmax warps themselves: 16 prompts of 2048 305 us
 // where 259 were without.)
 //
-// What bounds it is the way from a half tile's scores to its weights and back: 2048 tokens behind 14000 take 225 us (1120
+// What bounds it is the way from a half tile's scores to its weights and back: 2048 tokens behind 14000 take 228 us (1110
 // TFLOP/s, where a large product does 1964), with the tensor pipe and the special-function pipe half busy each; FP8
-// pages, whose codes are converted and whose scales go to scores and weights, 340.  16 prompts of 2048 196, FP8 382.
+// pages, whose codes are converted and whose scales go to scores and weights, 339.  16 prompts of 2048 200, FP8 371.  (The
+// comparisons below were each taken in turn, when the choice was made: 16 prompts then took 194 to 260.)
 #include <cmath>
 
 #include "pkv_chunk_run.cuh"

@@ -16,8 +16,10 @@
 // heads at once, 8 rounds for the query and 2 for the keys and values.  A lane's 4 table entries serve all of its
 // rounds.
 //
-// Many tokens are bound by their bytes and, with FP8 pages, by issue: 16384 with norms 41 us (32 at the rate of a
-// copy), FP8 48 (29); without norms 43.  One token 2.6 us, 1111 7.2: loads behind one another.
+// Many tokens are bound by their bytes and, with FP8 pages, by issue: 16384 with norms 41 us (31.5 at the rate of a
+// copy), FP8 48 (29).  Without norms 43 and 51: there the query's rotation is in two FP32 parts as well, because its bits
+// are those of the other appends.  One token 2.6 us, 1111 7.4: loads behind one another, slot, position, table entry and
+// (of a token that several warps share) row; only the table entry's has to wait for one before it.
 #include <cuda_bf16.h>
 
 #include "pkv_fp8.cuh"

@@ -7,8 +7,8 @@
 // part that ends last.
 //
 // Page products, whose dependent instructions 16 warps an SM hide in part, bound it: 200 sequences of up to 4096 FP8
-// tokens take 92 us where 63 would do at the rate of a copy (128 by a team of 8 warps beside the tile kernel's, 173
-// by one of 24 warps); BF16 124 us of 121.  A call of one short sequence (500 tokens: 10 us) is bound by its
+// tokens take 92.5 us where 63 would do at the rate of a copy (128 by a team of 8 warps beside the tile kernel's, 173
+// by one of 24 warps); BF16 125 us of 119.  A call of one short sequence (500 tokens: 10 us) is bound by its
 // steps one after the other: the plan, the first piece, the pages, the join of what is cut.
 #include <type_traits>
 

@@ -1,6 +1,6 @@
 """Attention of chunks whose work is cut between CTAs: keys, queries and scores that are not finite, and bad page
 ids, give what they give in one piece.  (3000 tokens are 24 key tiles a KV head, cut into several parts by either
-kernel: a run is at least 4 key tiles of the tile kernel's work, 5 of the single tokens'.)"""
+kernel: a CTA gets at least 4 key tiles of the tile kernel's work, 3 (FP8 pages: 5) of the single tokens'.)"""
 import numpy as np
 import pytest
 import torch
