@@ -21,10 +21,15 @@ dependent launch).
 
 The default run also measures further configurations (``--extra``: the ragged
 batch 64, batch 8, the separate calls on batch 64, FP8 pages on batch 64 and
-256) and reports them under ``configs``; a read-only HBM probe gives the
+256) and reports their figures under ``configs``; a read-only HBM probe gives the
 streaming ceiling the fractions are also reported against.  The CPU baseline is
 the FP64 oracle on the GPU batch's own inputs, single-threaded and on every
 host core.
+
+The JSON line on standard output stays below ``LINE_LIMIT`` characters, so that
+whoever keeps the end of the output has all of it; everything measured (how, the
+probes, each configuration's own settings, roofline and baselines) goes to
+standard error as one line behind ``detail:``.
 
 ``--impl reference`` times the FP64 CPU oracle on a bounded sample of the same
 workload on the host cores (the reference arm; it runs none of the CUDA path).
@@ -401,6 +406,47 @@ def config_block(w, a, variant_name: str, graph: bool) -> dict:
                   "no flush", "seed": a.seed}
 
 
+LINE_LIMIT = 3000  # characters of the JSON line
+
+
+def short(x):
+    """Figures of a detail with 6 digits."""
+    if isinstance(x, float):
+        return float(f"{x:.6g}")
+    if isinstance(x, dict):
+        return {k: short(v) for k, v in x.items()}
+    return [short(v) for v in x] if isinstance(x, list) else x
+
+
+def pick(d, *keys):
+    return None if d is None else {k: short(d[k]) for k in keys if k in d}
+
+
+def brief(line: dict) -> dict:
+    """The JSON line of a run: ``line`` without what explains its figures."""
+    out = dict(line)
+    for k, v in out.items():
+        if k not in ("value", "ms_per_step", "config", "clocks"):
+            out[k] = short(v)
+    out["roofline"] = pick(line.get("roofline"), "bound", "achieved", "peak", "unit", "frac", "traffic")
+    out["cpu_baseline"] = pick(line.get("cpu_baseline"), "value", "unit", "cores", "kind")
+    e2e = line.get("e2e")
+    out["e2e"] = None if e2e is None else {**e2e, "path": e2e.get("path", "").split(" (")[0].split(":")[0]}
+    if line.get("read_ceiling"):
+        out["read_ceiling"] = pick(line["read_ceiling"], "gbs", "best_probe")
+    if "configs" in line:
+        out["configs"] = {spec: {**pick(c, "value", "ms_per_step", "steps", "gpu_launches"),
+                                 "frac": short(c["hbm_frac_of_peak"]),
+                                 "e2e": short(c["e2e"]["value"]) if c.get("e2e") else None}
+                          for spec, c in line["configs"].items()}
+    return out
+
+
+def print_line(line: dict) -> None:
+    print("detail: " + json.dumps(line), file=sys.stderr, flush=True)
+    print(json.dumps(brief(line)), flush=True)
+
+
 def run_reference(args):
     """The reference arm: the FP64 oracle, as it stands, on the host cores (one thread per
     core), over a bounded sample of the workload per step (the pages ship no code)."""
@@ -499,7 +545,7 @@ def run_trace(args):
             "scheduler_stats": res.stats, "cpu_baseline": None,
             "gpu_launches": res.launches, "clocks": clocks}
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print_line(line)
     runner.close()
     return 0
 
@@ -731,7 +777,7 @@ def run_pkv(args):
             "read_ceiling": read_peak, "nominal_hbm_gbs": NOMINAL_HBM_GBS,
             "configs": extras}
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print_line(line)
     if world > 1:
         torch.distributed.destroy_process_group()
     return 0
