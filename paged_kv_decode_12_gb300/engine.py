@@ -527,7 +527,7 @@ class DecodeEngine:
         need = (last + wl.PAGE_SIZE - 1) // wl.PAGE_SIZE
         nbytes = pkv.pkv_evict_workspace_bytes(self.batch, keep)
         workspace = self._workspace("evict", nbytes, stream)
-        ids = pkv.pkv_pool_alloc(self.pool, int(need.sum()))
+        ids = self._taken(int(need.sum()))
         try:
             dst = np.full((self.batch, self.max_blocks), -1, dtype=np.int32)
             dst[np.arange(self.max_blocks)[None, :] < need[:, None]] = ids
@@ -552,10 +552,14 @@ class DecodeEngine:
     # ------------------------------------------------------------------ chunks of new tokens
     def take_pages(self, n: int) -> torch.Tensor:
         """``n`` pages of the pool as a list for ``chunk_tables`` (int32, on the device)."""
+        return torch.from_numpy(self._taken(n)).to(self.device)
+
+    def _taken(self, n: int) -> np.ndarray:
+        """``n`` pages of the pool.  (From here on they are the taker's, also where one was an eviction's room
+        that somebody has given back.)"""
         ids = pkv.pkv_pool_alloc(self.pool, n)
-        # (the caller's from here on, also where one was an eviction's room that somebody has given back)
         self._room = {layer: room[~np.isin(room, ids)] for layer, room in self._room.items()}
-        return torch.from_numpy(ids).to(self.device)
+        return ids
 
     def read_tables(self, stream=None) -> np.ndarray:
         """``bt_host`` from the device, where ``chunk_tables`` extends the tables, once the work on the

@@ -193,3 +193,26 @@ def test_arrays_on_another_gpu_are_refused(bare, monkeypatch):  # noqa: F811
         with pytest.raises(ValueError):
             bare.attention_shared(0, None, None, Elsewhere.on(i32(2), starts), Elsewhere.on(i32(1), prefix), 2, None)
     assert not called
+
+
+def test_pages_that_another_eviction_has_taken_stay_with_it(eng):
+    """The same where an eviction of another layer gets the pages that the caller has given back."""
+    c = Chunks(eng, 12)
+    c.step([16, 16, 16])
+    eng.read_tables()
+    eng._device_tables = False                                       # (as before the first chunk_tables)
+    pkv.pkv_pool_alloc(eng.pool, free(eng) - 9)                      # (few pages are left)
+    acc = torch.zeros(3, 8, 12 * PS)
+    eng.evict(0, c.lens, acc, 16, 4, 1, room=32)
+    room = eng._room[0]
+    pkv.pkv_pool_free(eng.pool, room)                                # the caller gives layer 0's room back
+    keep = eng.bt[0].clone()
+    keep[torch.from_numpy(np.isin(eng.bt[0].numpy(), room))] = -1
+    eng.bt[0].copy_(keep)
+    eng.evict(1, c.lens, acc, 16, 4, 1)                              # takes three of them
+    taken = eng.bt_host[1][eng.bt_host[1] >= 0]
+    assert np.isin(taken, room).any()
+    before = free(eng)
+    eng.bt[1].fill_(-1)                                              # (sequences that have ended, pages not given back)
+    eng.read_tables()
+    assert free(eng) == before
