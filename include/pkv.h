@@ -690,7 +690,7 @@ int pkv_chunk_append(const pkv_pool *pool, const uint16_t *k, int64_t k_stride, 
  *     out[t][h] = sum_j softmax_j(scale * q[t][h] . K_j) V_j   over j <= p
  * and, with a window > 0, of those with j > p - window or j < sinks (a token by itself: what
  * pkv_decode_window gives).  Only pages that hold such tokens are read and looked up.
- *   q, out     BF16 [T][32][64] (16-byte aligned); rows behind starts[B] are neither read nor written
+ *   q, out     BF16 [T][32][64] (16-byte aligned; out may be q); rows behind starts[B] are neither read nor written
  *   seq_lens_dev int32 [B], after the append; starts_dev int32 [B + 1], starts[0] = 0, starts[B] <= T.
  *              A sequence without new tokens is not looked at
  *   workspace  >= pkv_chunk_attention_workspace_bytes(B, T) bytes, 16-byte aligned, zero before the FIRST
